@@ -331,6 +331,121 @@ psgd_status psgd_adam_update(psgd_ctx* ctx, const psgd_adam_tensor* pass, int n_
                              hipStream_t stream);
 
 /*
+ * Orthogonalising an update by Newton-Schulz products, for an optimizer that steps a matrix by
+ * the orthogonal factor of its momentum (Muon) instead of Adam's quotient. For an update U (m x n)
+ *     X0 = U / max(||U||_F, eps)
+ *     repeat `steps` times, on the smaller side s = min(m, n) (X transposed when m > n):
+ *         A = X X^T,  X <- a X + (b A + c A A) X
+ * which sends every singular value x of X0 through x <- a x + b x^3 + c x^5 and keeps the
+ * singular vectors. U = 0 gives 0. A non-finite element of U makes its own matrix's result NaN
+ * and leaves the others alone.
+ *
+ * Products. PSGD_NS_FAST multiplies factors rounded to fp16 (2^-12 each) with fp32 sums and
+ * carries X itself in 22 bits: the result is within about 2e-3 of its Frobenius norm, the
+ * rounding of a bf16 output. PSGD_NS_ACCURATE multiplies fp16 halves hi + lo (three products),
+ * as close to the exact result as fp32 products, at about a third of the speed.
+ *
+ * Coefficients: the singular values entering each step must stay below 1.97 and |b x^2 + c x^4|
+ * below 60 (checked on the host by following the polynomial from [0, 1]); others are rejected with PSGD_EUNSUPPORTED. The usual (3.4445, -4.7750, 2.0315) and (1.5, -0.5, 0) pass.
+ */
+typedef enum psgd_ns_precision { PSGD_NS_FAST = 0, PSGD_NS_ACCURATE = 1 } psgd_ns_precision;
+
+typedef struct psgd_ns_hparams {
+  float a, b, c;
+  float eps;              /* > 0 */
+  int32_t steps;          /* 1..32 */
+} psgd_ns_hparams;
+
+/* One matrix of a group: in (m x n, in_dtype, read) and out (m x n, out_dtype, written), row-major
+ * with any leading dimension >= n and the alignment of their element type; 1 <= m, n <= 2^28.
+ * out may be the same memory as in (same type and leading dimension); otherwise an out must
+ * overlap no other buffer of the group. */
+typedef struct psgd_ns_matrix {
+  const void* in;   int64_t ld_in;
+  void* out;        int64_t ld_out;
+  int64_t m, n;
+} psgd_ns_matrix;
+
+typedef struct psgd_ns_plan psgd_ns_plan;
+
+/* Describe a group orthogonalised in grouped launches. Allocates the plan's workspace (8 bytes per
+ * element of the matrices padded to whole tiles plus 4 per element of s x s, 8 when accurate) and
+ * uploads the tables (synchronously). The pointers are captured. One plan runs one call at a time. */
+psgd_status psgd_ns_plan_create(psgd_ctx* ctx, const psgd_ns_matrix* mats, int n_mats, psgd_dtype in_dtype,
+                                psgd_dtype out_dtype, psgd_ns_precision precision, psgd_ns_plan** plan);
+
+/* Free a plan and its workspace (synchronises the device). NULL is accepted. */
+psgd_status psgd_ns_plan_destroy(psgd_ns_plan* plan);
+
+/* Orthogonalise every matrix of the plan: kernels only, on stream, no host sync (capturable). */
+psgd_status psgd_newton_schulz(psgd_ctx* ctx, psgd_ns_plan* plan, const psgd_ns_hparams* hp, hipStream_t stream);
+
+/*
+ * The Muon step on the matrices of a compression plan, from their decompressed gradients D (the
+ * matrices' out buffers, so every matrix needs one):
+ *     g = c D;  mom <- mu mom + g;  U = g + mu mom (nesterov) or mom;  O = Newton-Schulz(U)
+ *     theta <- theta - lr (f O + wd theta)
+ *     f = sqrt(max(1, m / n)) (adjust 0) or 0.2 sqrt(max(m, n)) (adjust 1: the update's root mean
+ *     square is then near Adam's, so learning rates carry over)
+ * with c the clipping factor norm_dev[1] of psgd_adam_prepare. Call order per step:
+ *     psgd_compress -> psgd_check_finite -> psgd_adam_prepare -> psgd_decompress_update
+ *     -> psgd_muon_update -> psgd_adam_update (the pass-through tensors)
+ */
+typedef struct psgd_muon_hparams {
+  float lr, momentum, weight_decay;       /* lr, weight_decay >= 0; 0 <= momentum < 1 */
+  int32_t nesterov;                       /* 0 or 1 */
+  int32_t adjust;                         /* 0 or 1 */
+  psgd_ns_hparams ns;
+} psgd_muon_hparams;
+
+/* Optimizer state of one plan matrix: param (m x n, ld_param >= n, aligned to its element type) and
+ * momentum (m x n fp32, leading dimension n, 16-byte aligned). Caller-owned, updated in place. */
+typedef struct psgd_muon_matrix {
+  void* param;       int64_t ld_param;
+  float* momentum;
+} psgd_muon_matrix;
+
+/* Attach Muon state to every matrix of the plan (opt has n_mats entries, in plan order). Allocates
+ * the Newton-Schulz workspace and, when no optimizer was attached before, the norm-reduction buffer
+ * of psgd_adam_prepare (synchronises the device). A second call replaces the first. PSGD_EINVAL
+ * when a matrix has no out buffer. Adam state may be attached to the same plan as well. */
+psgd_status psgd_muon_attach(psgd_ctx* ctx, psgd_plan* plan, const psgd_muon_matrix* opt, psgd_dtype param_dtype,
+                             psgd_ns_precision precision);
+
+/* One Muon step, after psgd_decompress_update. A step whose skip word is set changes nothing.
+ * norm_dev may be NULL (no clipping), skip_dev may not. */
+psgd_status psgd_muon_update(psgd_ctx* ctx, psgd_plan* plan, const int32_t* skip_dev, const float* norm_dev,
+                             const psgd_muon_hparams* hp, hipStream_t stream);
+
+/*
+ * Embeddings, the largest of the uncompressed 32-bit tensors: the scaled lookup and its gradient,
+ * which is a pass-through gradient of psgd_check_finite, psgd_adam_prepare and psgd_adam_update.
+ *   psgd_embed_lookup: out[t] = round(scale * table[ids[t]]), t = 0..n-1, rounded once to
+ *     out_dtype; a row of zeros for an id outside [0, vocab) (padding).
+ *   psgd_embed_grad: dtable[v] = scale * sum of dx[t] over the t with ids[t] = v, in fp32 in the
+ *     order of the batch (the same bits on every run); rows of absent tokens become 0. With
+ *     accumulate != 0 the sums are added to dtable instead and rows of absent tokens are not
+ *     touched. Ids outside [0, vocab) are ignored. Non-finite dx values end up in dtable.
+ * table, dx and out: fp16, bf16 or fp32, row-major, any leading dimension >= dim, aligned to their
+ * element type. ids: n int32 (PSGD_I32) or int64 (PSGD_I64) on the device. dtable: fp32.
+ * 0 <= n < 2^31 (0: lookup does nothing, gradient clears dtable unless accumulating),
+ * 1 <= vocab < 2^31, 1 <= dim <= 2^23. Outputs must not overlap inputs.
+ *   workspace: psgd_embed_grad_workspace(n, vocab, dim) bytes of device memory, 16-byte aligned,
+ *     contents ignored and overwritten; calls that may overlap need one each.
+ * Asynchronous on stream; no plan involved, no allocation.
+ */
+typedef enum psgd_itype { PSGD_I32 = 4, PSGD_I64 = 8 } psgd_itype;
+
+psgd_status psgd_embed_lookup(psgd_ctx* ctx, const void* table, int64_t ld_table, int64_t vocab, int64_t dim,
+                              psgd_dtype table_dtype, const void* ids, psgd_itype id_type, int64_t n, float scale,
+                              void* out, int64_t ld_out, psgd_dtype out_dtype, hipStream_t stream);
+psgd_status psgd_embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim, int64_t* bytes);
+psgd_status psgd_embed_grad(psgd_ctx* ctx, const void* dx, int64_t ld_dx, psgd_dtype dx_dtype, const void* ids,
+                            psgd_itype id_type, int64_t n, int64_t vocab, int64_t dim, float scale, float* dtable,
+                            int64_t ld_dtable, int accumulate, void* workspace, int64_t workspace_bytes,
+                            hipStream_t stream);
+
+/*
  * One whole step (psgd_compress, psgd_check_finite without the host copy, then
  * psgd_decompress_update) on a group given by its descriptors, with no plan and no device
  * allocation: for callers that cannot allocate (code under HIP graph capture, tight serving

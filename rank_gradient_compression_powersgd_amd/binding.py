@@ -15,6 +15,8 @@ LIB_PATH = os.path.join(_PKG, "libpsgd.so")
 
 PSGD_OK, PSGD_EINVAL, PSGD_EDTYPE, PSGD_ENOMEM, PSGD_EHIP, PSGD_EUNSUPPORTED = range(6)
 PSGD_F16, PSGD_BF16, PSGD_F32 = 1, 2, 3
+PSGD_NS_FAST, PSGD_NS_ACCURATE = 0, 1
+PSGD_I32, PSGD_I64 = 4, 8
 STATUS_NAMES = {0: "PSGD_OK", 1: "PSGD_EINVAL", 2: "PSGD_EDTYPE", 3: "PSGD_ENOMEM",
                 4: "PSGD_EHIP", 5: "PSGD_EUNSUPPORTED"}
 
@@ -55,6 +57,27 @@ class psgd_adam_matrix(ctypes.Structure):
 class psgd_adam_tensor(ctypes.Structure):
     _fields_ = [("param", ctypes.c_void_p), ("m1", ctypes.c_void_p), ("m2", ctypes.c_void_p),
                 ("grad", ctypes.c_void_p), ("numel", ctypes.c_int64)]
+
+
+class psgd_ns_hparams(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float), ("eps", ctypes.c_float),
+                ("steps", ctypes.c_int32)]
+
+
+class psgd_ns_matrix(ctypes.Structure):
+    # the C field is named `in`, a Python keyword: reach it with getattr
+    _fields_ = [("in", ctypes.c_void_p), ("ld_in", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("ld_out", ctypes.c_int64),
+                ("m", ctypes.c_int64), ("n", ctypes.c_int64)]
+
+
+class psgd_muon_hparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("nesterov", ctypes.c_int32), ("adjust", ctypes.c_int32), ("ns", psgd_ns_hparams)]
+
+
+class psgd_muon_matrix(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("ld_param", ctypes.c_int64), ("momentum", ctypes.c_void_p)]
 
 
 class PsgdError(RuntimeError):
@@ -114,7 +137,20 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.psgd_block_grad_enter.argtypes = [vp, vp, i64, vp, vp, ctypes.c_int, vp]
     lib.psgd_block_grad_exit.argtypes = [vp, vp, vp, i64, vp, ctypes.c_int, vp, vp]
     lib.psgd_block_grad_exit_enter.argtypes = [vp, vp, vp, i64, vp, vp, vp, ctypes.c_int, vp, vp]
-    for name in ("psgd_create", "psgd_destroy", "psgd_plan_create", "psgd_plan_destroy",
+    lib.psgd_ns_plan_create.argtypes = [vp, ctypes.POINTER(psgd_ns_matrix), ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                        ctypes.c_int, ctypes.POINTER(vp)]
+    lib.psgd_ns_plan_destroy.argtypes = [vp]
+    lib.psgd_newton_schulz.argtypes = [vp, vp, ctypes.POINTER(psgd_ns_hparams), vp]
+    lib.psgd_muon_attach.argtypes = [vp, vp, ctypes.POINTER(psgd_muon_matrix), ctypes.c_int, ctypes.c_int]
+    lib.psgd_muon_update.argtypes = [vp, vp, vp, vp, ctypes.POINTER(psgd_muon_hparams), vp]
+    lib.psgd_embed_lookup.argtypes = [vp, vp, i64, i64, i64, ctypes.c_int, vp, ctypes.c_int, i64, ctypes.c_float,
+                                      vp, i64, ctypes.c_int, vp]
+    lib.psgd_embed_grad_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
+    lib.psgd_embed_grad.argtypes = [vp, vp, i64, ctypes.c_int, vp, ctypes.c_int, i64, i64, i64, ctypes.c_float,
+                                    vp, i64, ctypes.c_int, vp, i64, vp]
+    for name in ("psgd_ns_plan_create", "psgd_ns_plan_destroy", "psgd_newton_schulz", "psgd_muon_attach",
+                 "psgd_muon_update", "psgd_embed_lookup", "psgd_embed_grad_workspace", "psgd_embed_grad",
+                 "psgd_create", "psgd_destroy", "psgd_plan_create", "psgd_plan_destroy",
                  "psgd_compress", "psgd_check_finite", "psgd_decompress_update",
                  "psgd_debug_buffer", "psgd_profile_events", "psgd_compress_p", "psgd_orthogonalize",
                  "psgd_compress_q", "psgd_refresh_q", "psgd_factor_buffer", "psgd_reset_errors",
@@ -140,10 +176,10 @@ def _ptr(t) -> int:
     return 0 if t is None else int(t.data_ptr())
 
 
-def _stream(stream) -> int:
+def _stream(stream, device=None) -> int:
     if stream is None:
         import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        return int(torch.cuda.current_stream(device).cuda_stream)
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -381,6 +417,171 @@ def psgd_block_grad_exit_enter(ctx: int, dx, g, scale_exit, scale_enter, out, fl
                                                      _ptr(scale_enter), _ptr(out),
                                                      _block_dtype(g, "psgd_block_grad_exit_enter"),
                                                      _ptr(flag), _stream(stream)))
+
+
+def ns_hparams(a: float = 3.4445, b: float = -4.7750, c: float = 2.0315, steps: int = 5,
+               eps: float = 1e-20) -> psgd_ns_hparams:
+    """Newton-Schulz coefficients of X <- a X + (b A + c A A) X, A = X X^T, and the smallest norm
+    an update is divided by."""
+    return psgd_ns_hparams(a, b, c, eps, steps)
+
+
+def muon_hparams(lr: float, momentum: float = 0.95, weight_decay: float = 0.0, nesterov: bool = True, adjust: int = 1,
+                 **ns) -> psgd_muon_hparams:
+    """Scalars of psgd_muon_update; further keywords go to ns_hparams."""
+    return psgd_muon_hparams(lr, momentum, weight_decay, int(nesterov), adjust, ns_hparams(**ns))
+
+
+def make_ns_matrix(update, out) -> psgd_ns_matrix:
+    """psgd_ns_matrix over torch tensors of one 2-D shape with unit row stride."""
+    call = "psgd_ns_plan_create"
+    if update.dim() != 2 or tuple(update.shape) != tuple(out.shape):
+        raise PsgdError(call, PSGD_EINVAL, "update and out must be 2-D tensors of one shape")
+    return psgd_ns_matrix(_ptr(update), _row_stride(update, call), _ptr(out), _row_stride(out, call), *update.shape)
+
+
+def make_muon_matrix(param, momentum) -> psgd_muon_matrix:
+    """psgd_muon_matrix over torch tensors: param m x n (unit row stride), momentum contiguous fp32."""
+    import torch
+    call = "psgd_muon_attach"
+    if tuple(param.shape) != tuple(momentum.shape) or param.dim() != 2:
+        raise PsgdError(call, PSGD_EINVAL, "param and momentum must be 2-D tensors of one shape")
+    if momentum.dtype != torch.float32:
+        raise PsgdError(call, PSGD_EDTYPE, "momentum must be float32")
+    if not momentum.is_contiguous():
+        raise PsgdError(call, PSGD_EINVAL, "momentum must be contiguous")
+    return psgd_muon_matrix(_ptr(param), _row_stride(param, call), _ptr(momentum))
+
+
+def _row_stride(t, call: str) -> int:
+    """Leading dimension of a 2-D tensor whose rows are contiguous and do not overlap."""
+    m, n = t.shape
+    if n > 1 and t.stride(1) != 1:
+        raise PsgdError(call, PSGD_EINVAL, "tensors need unit stride along rows")
+    if m <= 1:
+        return max(n, 1)                     # one row: its stride is never used
+    if t.stride(0) < n:
+        raise PsgdError(call, PSGD_EINVAL, "the rows of a tensor must not overlap")
+    return t.stride(0)
+
+
+def _dtype(t, call: str) -> int:
+    import torch
+    codes = {torch.float16: PSGD_F16, torch.bfloat16: PSGD_BF16, torch.float32: PSGD_F32}
+    if t.dtype not in codes:
+        raise PsgdError(call, PSGD_EDTYPE, f"tensors must be float16, bfloat16 or float32, got {t.dtype}")
+    return codes[t.dtype]
+
+
+def psgd_ns_plan_create(ctx: int, mats: Sequence[psgd_ns_matrix], in_dtype: int, out_dtype: int,
+                        precision: int = PSGD_NS_FAST) -> int:
+    arr = (psgd_ns_matrix * max(1, len(mats)))(*mats)
+    h = ctypes.c_void_p()
+    _check(ctx, "psgd_ns_plan_create",
+           load_library().psgd_ns_plan_create(ctx, arr, len(mats), in_dtype, out_dtype, precision, ctypes.byref(h)))
+    return h.value
+
+
+def psgd_ns_plan_destroy(plan: int) -> None:
+    load_library().psgd_ns_plan_destroy(plan)
+
+
+def psgd_newton_schulz(ctx: int, plan: int, hp: Optional[psgd_ns_hparams] = None, stream=None) -> None:
+    """Orthogonalise every matrix of the plan."""
+    _check(ctx, "psgd_newton_schulz",
+           load_library().psgd_newton_schulz(ctx, plan, ctypes.byref(hp or ns_hparams()), _stream(stream)))
+
+
+def psgd_muon_attach(ctx: int, plan: int, opt: Sequence[psgd_muon_matrix], param_dtype: int,
+                     precision: int = PSGD_NS_FAST) -> None:
+    arr = (psgd_muon_matrix * max(1, len(opt)))(*opt)
+    _check(ctx, "psgd_muon_attach", load_library().psgd_muon_attach(ctx, plan, arr, param_dtype, precision))
+
+
+def psgd_muon_update(ctx: int, plan: int, skip_dev, norm_dev, hp: psgd_muon_hparams, stream=None) -> None:
+    """One Muon step of every matrix of the plan on its decompressed gradient (norm_dev may be None)."""
+    _check(ctx, "psgd_muon_update",
+           load_library().psgd_muon_update(ctx, plan, _ptr(skip_dev), _ptr(norm_dev), ctypes.byref(hp), _stream(stream)))
+
+
+def _ids(ids, call: str):
+    import torch
+    codes = {torch.int32: PSGD_I32, torch.int64: PSGD_I64}
+    if ids.dtype not in codes:
+        raise PsgdError(call, PSGD_EDTYPE, f"ids must be int32 or int64, got {ids.dtype}")
+    if not ids.is_contiguous():
+        raise PsgdError(call, PSGD_EINVAL, "ids must be contiguous")
+    return codes[ids.dtype]
+
+
+def _embed_rows(t, n: int, dim: int, name: str, call: str) -> int:
+    """Row stride of a tensor that holds one row of dim values per token (2-D, or contiguous with
+    the tokens spread over the leading dimensions)."""
+    if t.dim() < 2 or t.shape[-1] != dim or t.numel() != n * dim:
+        raise PsgdError(call, PSGD_EINVAL, f"{name} must hold one row of {dim} values per token")
+    if t.dim() > 2:
+        if not t.is_contiguous():
+            raise PsgdError(call, PSGD_EINVAL, f"{name} with more than two dimensions must be contiguous")
+        return dim
+    return _row_stride(t, call)
+
+
+def _same_device(call: str, *tensors):
+    if len({t.device for t in tensors}) != 1 or not tensors[0].is_cuda:
+        raise PsgdError(call, PSGD_EINVAL, "tensors must live on one GPU")
+
+
+def psgd_embed_lookup(ctx: int, table, ids, out, scale: float = 1.0, stream=None) -> None:
+    """out[t] = round(scale * table[ids[t]]) over all tokens of ids (any shape; out has one row per
+    token); a row of zeros where the id lies outside the table."""
+    call = "psgd_embed_lookup"
+    if table.dim() != 2 or table.shape[0] < 1 or table.shape[1] < 1:
+        raise PsgdError(call, PSGD_EINVAL, "table must be a vocab x dim tensor")
+    vocab, dim = table.shape
+    ld_out = _embed_rows(out, ids.numel(), dim, "out", call)
+    _same_device(call, table, ids, out)
+    _check(ctx, call, load_library().psgd_embed_lookup(
+        ctx, _ptr(table), _row_stride(table, call), vocab, dim, _dtype(table, call), _ptr(ids), _ids(ids, call),
+        ids.numel(), float(scale), _ptr(out), ld_out, _dtype(out, call), _stream(stream, table.device)))
+
+
+def psgd_embed_grad_workspace(n: int, vocab: int, dim: int) -> int:
+    """Bytes of device workspace of psgd_embed_grad for n tokens."""
+    out = ctypes.c_int64()
+    _check(None, "psgd_embed_grad_workspace", load_library().psgd_embed_grad_workspace(n, vocab, dim, ctypes.byref(out)))
+    return out.value
+
+
+def psgd_embed_grad(ctx: int, dx, ids, dtable, scale: float = 1.0, accumulate: bool = False, workspace=None,
+                    stream=None) -> None:
+    """dtable[v] = (accumulate: dtable[v] +) scale * sum of dx[t] over the tokens with ids[t] = v.
+    dtable is vocab x dim fp32; workspace is a contiguous device tensor of at least
+    psgd_embed_grad_workspace(...) bytes, allocated for the call on its stream when None."""
+    import torch
+    call = "psgd_embed_grad"
+    if dtable.dim() != 2 or dtable.shape[0] < 1 or dtable.shape[1] < 1:
+        raise PsgdError(call, PSGD_EINVAL, "dtable must be a vocab x dim tensor")
+    if dtable.dtype != torch.float32:
+        raise PsgdError(call, PSGD_EDTYPE, "dtable must be float32")
+    vocab, dim = dtable.shape
+    n = ids.numel()
+    ld_dx, ld_dt = _embed_rows(dx, n, dim, "dx", call), _row_stride(dtable, call)
+    dt, it = _dtype(dx, call), _ids(ids, call)
+    _same_device(call, dx, ids, dtable, *([] if workspace is None else [workspace]))
+    if workspace is None:
+        need = psgd_embed_grad_workspace(n, vocab, dim)
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dtable.device)
+        else:
+            # allocated on the stream that uses it, so that its memory is not handed out earlier
+            s = torch.cuda.ExternalStream(stream, dtable.device) if isinstance(stream, int) else stream
+            with torch.cuda.stream(s):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dtable.device)
+    elif not workspace.is_contiguous():
+        raise PsgdError(call, PSGD_EINVAL, "workspace must be contiguous")
+    _check(ctx, call, load_library().psgd_embed_grad(
+        ctx, _ptr(dx), ld_dx, dt, _ptr(ids), it, n, vocab, dim, float(scale), _ptr(dtable), ld_dt, int(accumulate),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream, dtable.device)))
 
 
 def psgd_last_error(ctx: int) -> str:

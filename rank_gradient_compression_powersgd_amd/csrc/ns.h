@@ -1,0 +1,81 @@
+// Newton-Schulz orthogonalisation of a group of matrices: descriptors shared by its kernels
+// (k_ns.hip, k_ns_gemm.hip) and its host side (ns_group.hip).
+#pragma once
+
+#include <vector>
+
+#include "psgd_internal.h"
+
+namespace psgd {
+
+// The iteration works on the smaller side: X is s x l with s = min(m, n), l = max(m, n), the
+// update transposed when m > n. Everything between the first and the last kernel lives in the
+// workspace as fp16 values times a fixed power of two, zero-padded to whole tiles:
+//   X  (sp x lp)  as hi + lo, X * 2^14 = hi + lo to 2^-22: singular values stay below 4
+//   A  (sp x sp)  X X^T, times 2^14 (entries bounded by the squared singular values)
+//   B  (sp x sp)  b A + c A A, times 2^10
+// A and B are symmetric: only the tiles on and below the diagonal are computed, and each is
+// stored twice.
+constexpr float kNsScaleX = 16384.0f, kNsScaleA = 16384.0f, kNsScaleB = 1024.0f;
+
+struct NsMat {
+  const void* in;    int64_t ld_in;      // update (Newton-Schulz) or gradient (Muon), m x n
+  float* mom;                            // Muon: m x n fp32 momentum (leading dimension n)
+  void* out;         int64_t ld_out;     // orthogonal factor (Newton-Schulz) or parameter (Muon)
+  int32_t m, n;
+  int32_t s, l, sp, lp;
+  int32_t flip;                          // 1: X holds the transposed update (m > n)
+  int32_t parts, part_rows;              // partial sums of squares: rows per part
+  float factor;                          // Muon: scale of the orthogonal update
+  uint16_t* xh[2];   uint16_t* xl[2];    // X, ping-pong between steps
+  uint16_t* ah;      uint16_t* al;       // A (lo: accurate products only)
+  uint16_t* bh;      uint16_t* bl;       // B likewise
+  double* partial;                       // parts fp64 sums of u^2
+};
+
+// Scalars of one call.
+struct NsArgs {
+  float a, b, c;
+  double eps;
+  int steps;
+  // Muon (mu unused otherwise)
+  int muon, nesterov;
+  float lr, mu, weight_decay;
+  const int32_t* skip;                   // NULL: never skipped
+  const float* norm;                     // norm[1] = clipping factor; NULL: 1
+};
+
+// Elements of the update as they enter the iteration and of the result as they leave it.
+enum NsStage : int { NS_GRAM = 0, NS_POLY = 1, NS_UPDATE = 2 };
+
+hipError_t launch_ns_norm(int it, const NsMat* mats, const Work* work, int n_work, const NsArgs& a, hipStream_t s);
+hipError_t launch_ns_x0(int it, const NsMat* mats, const Work* work, int n_work, const NsArgs& a, hipStream_t s);
+// One product stage of step `step` (0-based) over a tile list; `last` writes the caller's output.
+hipError_t launch_ns_gemm(NsStage st, int tile, bool accurate, int ot, bool last, const NsMat* mats,
+                          const Work* work, int n_work, int step, const NsArgs& a, hipStream_t s);
+
+// A group of matrices orthogonalised together: validated by the caller, laid out and allocated
+// here. One instance serves one call at a time.
+class NsGroup {
+ public:
+  struct Item { const void* in; int64_t ld_in; float* mom; void* out; int64_t ld_out; int64_t m, n; };
+  ~NsGroup();
+  // types are GradType; adds no host work to later calls. Returns hipErrorOutOfMemory when the
+  // workspace does not fit, hipErrorInvalidValue when a matrix is too large for 32-bit tiles.
+  hipError_t create(const std::vector<Item>& items, int in_type, int out_type, bool accurate);
+  // factor(m, n) of every matrix for Muon calls (adjust: 0 sqrt(max(1, m/n)), 1 0.2 sqrt(max(m, n)))
+  hipError_t run(const NsArgs& a, int adjust, hipStream_t s);
+  size_t workspace_bytes() const { return bytes_; }
+
+ private:
+  struct List { int off = 0, cnt = 0; };
+  void* buf_ = nullptr;                  // workspace, descriptors (one table per adjust), work lists
+  size_t bytes_ = 0;
+  NsMat* d_mats_[2] = {nullptr, nullptr};
+  Work* d_work_ = nullptr;
+  List norm_, x0_, gram_, poly_, update_;
+  int it_ = 0, ot_ = 0, tile_ = 128;
+  bool accurate_ = false;
+};
+
+}  // namespace psgd

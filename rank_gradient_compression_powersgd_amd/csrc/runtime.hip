@@ -14,6 +14,8 @@
 
 #include "../../include/psgd.h"
 #include "psgd_internal.h"
+#include "embed.h"
+#include "ns.h"
 
 namespace psgd {
 int ef_mq_rows_per_block();
@@ -87,6 +89,12 @@ struct psgd_plan {
   psgd::NormItem* d_items = nullptr;
   double* d_partial = nullptr;
   int n_plan_items = 0;
+  std::unique_ptr<psgd::NsGroup> muon;   // Newton-Schulz workspace (psgd_muon_attach)
+};
+
+struct psgd_ns_plan {
+  psgd_ctx* ctx = nullptr;
+  psgd::NsGroup group;
 };
 
 namespace {
@@ -876,6 +884,19 @@ psgd_status psgd_step_noalloc(psgd_ctx* ctx, const psgd_matrix* mats, int n_mats
 // ------------------------------------------------------------------------------------------
 // the optimizer step that consumes the decompressed gradient
 // ------------------------------------------------------------------------------------------
+namespace {
+// The norm of D is that of q_next (n x r): items of at most kNormItem floats.
+std::vector<psgd::NormItem> norm_items(const psgd_plan* plan) {
+  std::vector<psgd::NormItem> items;
+  for (const DevMat& d : plan->mats) {
+    const int64_t cnt = (int64_t)d.n * d.r;
+    for (int64_t o = 0; o < cnt; o += psgd::kNormItem)
+      items.push_back(psgd::NormItem{d.q_next + o, std::min<int64_t>(psgd::kNormItem, cnt - o)});
+  }
+  return items;
+}
+}  // namespace
+
 psgd_status psgd_adam_attach(psgd_ctx* ctx, psgd_plan* plan, const psgd_adam_matrix* opt,
                              psgd_dtype param_dtype) {
   if (psgd_status st = check_call(ctx, plan); st != PSGD_OK) return st;
@@ -888,7 +909,6 @@ psgd_status psgd_adam_attach(psgd_ctx* ctx, psgd_plan* plan, const psgd_adam_mat
     default: return fail(ctx, PSGD_EDTYPE, "unknown parameter dtype %d", (int)param_dtype);
   }
   std::vector<DevMat> mats = plan->mats;
-  std::vector<psgd::NormItem> items;
   for (int i = 0; i < plan->n_mats; ++i) {
     const psgd_adam_matrix& a = opt[i];
     DevMat& d = mats[i];
@@ -907,11 +927,8 @@ psgd_status psgd_adam_attach(psgd_ctx* ctx, psgd_plan* plan, const psgd_adam_mat
     d.m2 = a.m2;
     d.p_bytes = (uint32_t)pb;
     d.mo_bytes = (uint32_t)mb;
-    // the norm of D is that of q_next (n x r): items of at most kNormItem floats
-    const int64_t cnt = (int64_t)d.n * d.r;
-    for (int64_t o = 0; o < cnt; o += psgd::kNormItem)
-      items.push_back(psgd::NormItem{d.q_next + o, std::min<int64_t>(psgd::kNormItem, cnt - o)});
   }
+  const std::vector<psgd::NormItem> items = norm_items(plan);
   const size_t items_bytes = (size_t)rup((int64_t)((items.size() + kMaxPassItems) * sizeof(psgd::NormItem)), 256);
   const size_t bytes = items_bytes + (items.size() + kMaxPassItems) * sizeof(double);
   void* buf = nullptr;
@@ -964,7 +981,7 @@ psgd_status psgd_adam_prepare(psgd_ctx* ctx, psgd_plan* plan, const psgd_adam_te
                               float max_norm, const int32_t* skip_dev, int32_t* step_dev,
                               float* norm_dev, hipStream_t stream) {
   if (psgd_status st = check_call(ctx, plan); st != PSGD_OK) return st;
-  if (!plan->adam_pt) return fail(ctx, PSGD_EINVAL, "no optimizer attached to the plan (psgd_adam_attach)");
+  if (!plan->adam_pt && !plan->muon) return fail(ctx, PSGD_EINVAL, "no optimizer attached to the plan (psgd_adam_attach)");
   if (!skip_dev || !step_dev || !norm_dev) return fail(ctx, PSGD_EINVAL, "skip_dev, step_dev and norm_dev are required");
   if (psgd_status st = check_pass_tensors(ctx, pass, n_pass, false); st != PSGD_OK) return st;
   std::vector<psgd::NormItem> items;
@@ -1016,6 +1033,281 @@ psgd_status psgd_adam_update(psgd_ctx* ctx, const psgd_adam_tensor* pass, int n_
   const psgd::AdamArgs aa = adam_args(hp, step_dev, norm_dev);
   HIPCHK(ctx, traced(ctx, S_ADAM_PASS, stream, [&] {
     return psgd::launch_adam_f32(ts.data(), (int)ts.size(), aa, skip_dev, stream); }), "pass-through Adam");
+  return PSGD_OK;
+}
+
+// ------------------------------------------------------------------------------------------
+// Newton-Schulz, the Muon step, embeddings
+// ------------------------------------------------------------------------------------------
+namespace {
+
+// Makes a context's device current for one call and gives the caller's back.
+struct DeviceGuard {
+  int prev = -1;
+  hipError_t err;
+  explicit DeviceGuard(int device) {
+    err = hipGetDevice(&prev);
+    if (err == hipSuccess && prev != device) err = hipSetDevice(device);
+    else prev = -1;
+  }
+  ~DeviceGuard() { if (prev >= 0) (void)hipSetDevice(prev); }
+};
+
+int grad_type(psgd_dtype dt) {
+  switch (dt) {
+    case PSGD_F16: return psgd::G_F16;
+    case PSGD_BF16: return psgd::G_BF16;
+    case PSGD_F32: return psgd::G_F32;
+  }
+  return 0;
+}
+int type_size(int gt) { return gt == psgd::G_F32 ? 4 : 2; }
+bool aligned_to(const void* p, int size) { return reinterpret_cast<uintptr_t>(p) % size == 0; }
+
+psgd_status check_ns(psgd_ctx* ctx, const psgd_ns_hparams& h) {
+  if (!std::isfinite(h.a) || !std::isfinite(h.b) || !std::isfinite(h.c))
+    return fail(ctx, PSGD_EINVAL, "the Newton-Schulz coefficients must be finite");
+  if (!(h.eps > 0.0f) || !std::isfinite(h.eps)) return fail(ctx, PSGD_EINVAL, "eps must be finite and > 0");
+  if (h.steps < 1 || h.steps > 32) return fail(ctx, PSGD_EINVAL, "steps must lie in [1, 32], got %d", h.steps);
+  // Follow the largest singular value the polynomial can produce from [0, hi]: fp16 holds
+  // 2^14 X, 2^14 X X^T and 2^10 B.
+  const double a = h.a, b = h.b, c = h.c;
+  double hi = 1.0;
+  for (int k = 0; k < h.steps; ++k) {
+    double next = 0.0;
+    for (int i = 0; i <= 512; ++i) {
+      const double x = hi * i / 512, x2 = x * x, p = b * x2 + c * x2 * x2;
+      if (std::fabs(p) > 60.0)
+        return fail(ctx, PSGD_EUNSUPPORTED, "the Newton-Schulz coefficients leave the fp16 range of B at step %d", k);
+      next = std::max(next, std::fabs(x * (a + p)));
+    }
+    // a smooth polynomial of degree 5 moves little between samples
+    next *= 1.001;
+    if (k + 1 < h.steps && next * next > 7.8 / 2)
+      return fail(ctx, PSGD_EUNSUPPORTED, "the Newton-Schulz coefficients let singular values grow to %g after step %d", next, k);
+    hi = next;
+  }
+  return PSGD_OK;
+}
+
+psgd_status make_group(psgd_ctx* ctx, psgd::NsGroup& g, const std::vector<psgd::NsGroup::Item>& items, int it, int ot,
+                       psgd_ns_precision precision) {
+  if (precision != PSGD_NS_FAST && precision != PSGD_NS_ACCURATE)
+    return fail(ctx, PSGD_EINVAL, "unknown precision %d", (int)precision);
+  const hipError_t e = g.create(items, it, ot, precision == PSGD_NS_ACCURATE);
+  if (e == hipErrorOutOfMemory) return fail(ctx, PSGD_ENOMEM, "Newton-Schulz workspace of %zu bytes", g.workspace_bytes());
+  if (e != hipSuccess) return hip_fail(ctx, e, "Newton-Schulz plan");
+  return PSGD_OK;
+}
+
+}  // namespace
+
+psgd_status psgd_ns_plan_create(psgd_ctx* ctx, const psgd_ns_matrix* mats, int n_mats, psgd_dtype in_dtype,
+                                psgd_dtype out_dtype, psgd_ns_precision precision, psgd_ns_plan** plan_out) try {
+  if (!ctx) return PSGD_EINVAL;
+  ctx->err.clear();
+  if (!plan_out) return fail(ctx, PSGD_EINVAL, "plan pointer is NULL");
+  *plan_out = nullptr;
+  if (!mats || n_mats < 1) return fail(ctx, PSGD_EINVAL, "need at least one matrix");
+  const int it = grad_type(in_dtype), ot = grad_type(out_dtype);
+  if (!it) return fail(ctx, PSGD_EDTYPE, "unknown input dtype %d", (int)in_dtype);
+  if (!ot) return fail(ctx, PSGD_EDTYPE, "unknown output dtype %d", (int)out_dtype);
+  std::vector<psgd::NsGroup::Item> items;
+  for (int i = 0; i < n_mats; ++i) {
+    const psgd_ns_matrix& a = mats[i];
+    if (!a.in || !a.out) return fail(ctx, PSGD_EINVAL, "matrix %d: in and out are required", i);
+    if (a.m < 1 || a.n < 1 || a.m > (1 << 28) || a.n > (1 << 28))
+      return fail(ctx, PSGD_EINVAL, "matrix %d: bad shape %lld x %lld", i, (long long)a.m, (long long)a.n);
+    if (a.ld_in < a.n || a.ld_out < a.n) return fail(ctx, PSGD_EINVAL, "matrix %d: leading dimensions must be >= n", i);
+    if (!aligned_to(a.in, type_size(it)) || !aligned_to(a.out, type_size(ot)))
+      return fail(ctx, PSGD_EINVAL, "matrix %d: pointers must be aligned to their element type", i);
+    items.push_back({a.in, a.ld_in, nullptr, a.out, a.ld_out, a.m, a.n});
+  }
+  DeviceGuard dev(ctx->device);
+  HIPCHK(ctx, dev.err, "hipSetDevice");
+  std::unique_ptr<psgd_ns_plan> p(new psgd_ns_plan);
+  p->ctx = ctx;
+  if (psgd_status st = make_group(ctx, p->group, items, it, ot, precision); st != PSGD_OK) return st;
+  *plan_out = p.release();
+  return PSGD_OK;
+} catch (const std::exception&) {
+  return fail(ctx, PSGD_ENOMEM, "out of host memory");
+}
+
+psgd_status psgd_ns_plan_destroy(psgd_ns_plan* plan) {
+  if (!plan) return PSGD_OK;
+  DeviceGuard dev(plan->ctx->device);
+  (void)hipDeviceSynchronize();
+  delete plan;
+  return PSGD_OK;
+}
+
+psgd_status psgd_newton_schulz(psgd_ctx* ctx, psgd_ns_plan* plan, const psgd_ns_hparams* hp, hipStream_t stream) {
+  if (!ctx) return PSGD_EINVAL;
+  ctx->err.clear();
+  if (!plan || plan->ctx != ctx) return fail(ctx, PSGD_EINVAL, "plan does not belong to this context");
+  if (!hp) return fail(ctx, PSGD_EINVAL, "hyperparameters are required");
+  if (psgd_status st = check_ns(ctx, *hp); st != PSGD_OK) return st;
+  DeviceGuard dev(ctx->device);
+  HIPCHK(ctx, dev.err, "hipSetDevice");
+  psgd::NsArgs a{};
+  a.a = hp->a; a.b = hp->b; a.c = hp->c; a.eps = hp->eps; a.steps = hp->steps;
+  HIPCHK(ctx, plan->group.run(a, 0, stream), "Newton-Schulz");
+  return PSGD_OK;
+}
+
+psgd_status psgd_muon_attach(psgd_ctx* ctx, psgd_plan* plan, const psgd_muon_matrix* opt, psgd_dtype param_dtype,
+                             psgd_ns_precision precision) try {
+  if (!ctx) return PSGD_EINVAL;
+  ctx->err.clear();
+  if (!plan || plan->ctx != ctx) return fail(ctx, PSGD_EINVAL, "plan does not belong to this context");
+  if (!opt) return fail(ctx, PSGD_EINVAL, "optimizer descriptors are required");
+  const int pt = grad_type(param_dtype);
+  if (!pt) return fail(ctx, PSGD_EDTYPE, "unknown parameter dtype %d", (int)param_dtype);
+  std::vector<psgd::NsGroup::Item> items;
+  for (int i = 0; i < plan->n_mats; ++i) {
+    const DevMat& d = plan->mats[i];
+    const psgd_muon_matrix& a = opt[i];
+    if (!d.out) return fail(ctx, PSGD_EINVAL, "matrix %d: Muon reads the decompressed gradient, the matrix has no out buffer", i);
+    if (!a.param || !a.momentum) return fail(ctx, PSGD_EINVAL, "matrix %d: param and momentum are required", i);
+    if (a.ld_param < d.n) return fail(ctx, PSGD_EINVAL, "matrix %d: ld_param must be >= n", i);
+    if (!aligned_to(a.param, type_size(pt)) || !aligned16(a.momentum))
+      return fail(ctx, PSGD_EINVAL, "matrix %d: param must be aligned to its element type, momentum to 16 bytes", i);
+    items.push_back({d.out, d.ld_out, a.momentum, a.param, a.ld_param, d.m, d.n});
+  }
+  DeviceGuard dev(ctx->device);
+  HIPCHK(ctx, dev.err, "hipSetDevice");
+  std::unique_ptr<psgd::NsGroup> g(new psgd::NsGroup);
+  if (psgd_status st = make_group(ctx, *g, items, psgd::G_F32, pt, precision); st != PSGD_OK) return st;
+  if (!plan->adam_buf) {                   // psgd_adam_prepare's norm over the plan's gradients
+    const std::vector<psgd::NormItem> norm = norm_items(plan);
+    const size_t items_bytes = (size_t)rup((int64_t)((norm.size() + kMaxPassItems) * sizeof(psgd::NormItem)), 256);
+    const size_t bytes = items_bytes + (norm.size() + kMaxPassItems) * sizeof(double);
+    void* buf = nullptr;
+    if (hipMalloc(&buf, bytes) != hipSuccess) return fail(ctx, PSGD_ENOMEM, "optimizer buffer of %zu bytes", bytes);
+    const hipError_t e = hipMemcpy(buf, norm.data(), norm.size() * sizeof(psgd::NormItem), hipMemcpyHostToDevice);
+    if (e != hipSuccess) {
+      (void)hipFree(buf);
+      return hip_fail(ctx, e, "optimizer upload");
+    }
+    plan->adam_buf = buf;
+    plan->d_items = static_cast<psgd::NormItem*>(buf);
+    plan->d_partial = reinterpret_cast<double*>(static_cast<char*>(buf) + items_bytes);
+    plan->n_plan_items = (int)norm.size();
+  }
+  // no step of this plan may still be running on a workspace that is replaced
+  HIPCHK(ctx, hipDeviceSynchronize(), "synchronise before attaching");
+  plan->muon = std::move(g);
+  return PSGD_OK;
+} catch (const std::exception&) {
+  return fail(ctx, PSGD_ENOMEM, "out of host memory");
+}
+
+psgd_status psgd_muon_update(psgd_ctx* ctx, psgd_plan* plan, const int32_t* skip_dev, const float* norm_dev,
+                             const psgd_muon_hparams* hp, hipStream_t stream) {
+  if (!ctx) return PSGD_EINVAL;
+  ctx->err.clear();
+  if (!plan || plan->ctx != ctx) return fail(ctx, PSGD_EINVAL, "plan does not belong to this context");
+  if (!plan->muon) return fail(ctx, PSGD_EINVAL, "no Muon state attached to the plan (psgd_muon_attach)");
+  if (!skip_dev) return fail(ctx, PSGD_EINVAL, "skip_dev is required");
+  if (!hp) return fail(ctx, PSGD_EINVAL, "hyperparameters are required");
+  if (!(hp->momentum >= 0.0f && hp->momentum < 1.0f)) return fail(ctx, PSGD_EINVAL, "momentum must lie in [0, 1)");
+  if (!(hp->lr >= 0.0f) || !(hp->weight_decay >= 0.0f) || !std::isfinite(hp->lr) || !std::isfinite(hp->weight_decay))
+    return fail(ctx, PSGD_EINVAL, "lr and weight_decay must be finite and >= 0");
+  if ((hp->nesterov | 1) != 1 || (hp->adjust | 1) != 1) return fail(ctx, PSGD_EINVAL, "nesterov and adjust must be 0 or 1");
+  if (psgd_status st = check_ns(ctx, hp->ns); st != PSGD_OK) return st;
+  DeviceGuard dev(ctx->device);
+  HIPCHK(ctx, dev.err, "hipSetDevice");
+  psgd::NsArgs a{};
+  a.a = hp->ns.a; a.b = hp->ns.b; a.c = hp->ns.c; a.eps = hp->ns.eps; a.steps = hp->ns.steps;
+  a.muon = 1; a.nesterov = hp->nesterov;
+  a.lr = hp->lr; a.mu = hp->momentum; a.weight_decay = hp->weight_decay;
+  a.skip = skip_dev;
+  a.norm = norm_dev;
+  HIPCHK(ctx, plan->muon->run(a, hp->adjust, stream), "Muon step");
+  return PSGD_OK;
+}
+
+namespace {
+psgd_status check_embed(psgd_ctx* ctx, const void* ids, psgd_itype it, int64_t n, int64_t vocab, int64_t dim, float scale) {
+  if (it != PSGD_I32 && it != PSGD_I64) return fail(ctx, PSGD_EDTYPE, "ids must be int32 or int64");
+  if (n < 0 || n > 0x7fffffffll) return fail(ctx, PSGD_EINVAL, "n = %lld outside [0, 2^31)", (long long)n);
+  if (vocab < 1 || vocab > 0x7fffffffll) return fail(ctx, PSGD_EINVAL, "vocab = %lld outside [1, 2^31)", (long long)vocab);
+  if (dim < 1 || dim > (1 << 23)) return fail(ctx, PSGD_EINVAL, "dim = %lld outside [1, 2^23]", (long long)dim);
+  if (n > 0 && (!ids || !aligned_to(ids, (int)it))) return fail(ctx, PSGD_EINVAL, "ids must be a pointer aligned to its element type");
+  if (!std::isfinite(scale)) return fail(ctx, PSGD_EINVAL, "scale must be finite");
+  return PSGD_OK;
+}
+struct EmbedLayout { int64_t chunk, chunks, list, sorted, seg, partial, ld_partial, bytes; };
+EmbedLayout embed_layout(int64_t n, int64_t vocab, int64_t dim) {
+  EmbedLayout L{};
+  L.chunk = psgd::embed_chunk(n, dim);
+  L.chunks = (n + L.chunk - 1) / L.chunk;
+  L.list = 0;
+  L.sorted = L.list + rup(8 * n, 256);
+  L.seg = L.sorted + rup(8 * n, 256);
+  L.partial = L.seg + rup(4 * (vocab + 1), 256);
+  L.ld_partial = rup(dim, 4);
+  L.bytes = L.partial + 8 * L.chunks * L.ld_partial;
+  return L;
+}
+}  // namespace
+
+psgd_status psgd_embed_lookup(psgd_ctx* ctx, const void* table, int64_t ld_table, int64_t vocab, int64_t dim,
+                              psgd_dtype table_dtype, const void* ids, psgd_itype id_type, int64_t n, float scale,
+                              void* out, int64_t ld_out, psgd_dtype out_dtype, hipStream_t stream) {
+  if (!ctx) return PSGD_EINVAL;
+  ctx->err.clear();
+  const int tt = grad_type(table_dtype), ot = grad_type(out_dtype);
+  if (!tt || !ot) return fail(ctx, PSGD_EDTYPE, "unknown table or output dtype");
+  if (psgd_status st = check_embed(ctx, ids, id_type, n, vocab, dim, scale); st != PSGD_OK) return st;
+  if (ld_table < dim || ld_out < dim) return fail(ctx, PSGD_EINVAL, "leading dimensions must be >= dim");
+  if (n == 0) return PSGD_OK;
+  if (!table || !out || !aligned_to(table, type_size(tt)) || !aligned_to(out, type_size(ot)))
+    return fail(ctx, PSGD_EINVAL, "table and out must be pointers aligned to their element type");
+  DeviceGuard dev(ctx->device);
+  HIPCHK(ctx, dev.err, "hipSetDevice");
+  const psgd::EmbedLookup a{table, ld_table, vocab, dim, ids, n, out, ld_out, scale};
+  HIPCHK(ctx, psgd::launch_embed_lookup(a, tt, ot, (int)id_type, stream), "embedding lookup");
+  return PSGD_OK;
+}
+
+psgd_status psgd_embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim, int64_t* bytes) {
+  if (!bytes || check_embed(nullptr, reinterpret_cast<const void*>(8), PSGD_I64, n, vocab, dim, 1.0f) != PSGD_OK) return PSGD_EINVAL;
+  *bytes = embed_layout(n, vocab, dim).bytes;
+  return PSGD_OK;
+}
+
+psgd_status psgd_embed_grad(psgd_ctx* ctx, const void* dx, int64_t ld_dx, psgd_dtype dx_dtype, const void* ids,
+                            psgd_itype id_type, int64_t n, int64_t vocab, int64_t dim, float scale, float* dtable,
+                            int64_t ld_dtable, int accumulate, void* workspace, int64_t workspace_bytes,
+                            hipStream_t stream) {
+  if (!ctx) return PSGD_EINVAL;
+  ctx->err.clear();
+  const int dt = grad_type(dx_dtype);
+  if (!dt) return fail(ctx, PSGD_EDTYPE, "unknown gradient dtype %d", (int)dx_dtype);
+  if (psgd_status st = check_embed(ctx, ids, id_type, n, vocab, dim, scale); st != PSGD_OK) return st;
+  if (ld_dx < dim || ld_dtable < dim) return fail(ctx, PSGD_EINVAL, "leading dimensions must be >= dim");
+  if (!dtable || !aligned_to(dtable, 4)) return fail(ctx, PSGD_EINVAL, "dtable must be a pointer aligned to its element type");
+  if (n > 0 && (!dx || !aligned_to(dx, type_size(dt)))) return fail(ctx, PSGD_EINVAL, "dx must be a pointer aligned to its element type");
+  const EmbedLayout L = embed_layout(n, vocab, dim);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < L.bytes)
+    return fail(ctx, PSGD_EINVAL, "the workspace needs %lld bytes at a 16-byte aligned address, got %lld", (long long)L.bytes,
+                (long long)workspace_bytes);
+  DeviceGuard dev(ctx->device);
+  HIPCHK(ctx, dev.err, "hipSetDevice");
+  char* ws = static_cast<char*>(workspace);
+  psgd::EmbedGrad a{};
+  a.dx = dx; a.ld_dx = ld_dx; a.ids = ids; a.n = n; a.vocab = vocab; a.dim = dim;
+  a.dtable = dtable; a.ld_dtable = ld_dtable; a.scale = scale; a.accumulate = accumulate != 0;
+  a.range = psgd::embed_range(vocab);
+  a.chunk = (int32_t)L.chunk; a.chunks = L.chunks;
+  a.list = reinterpret_cast<uint64_t*>(ws + L.list);
+  a.sorted = reinterpret_cast<uint64_t*>(ws + L.sorted);
+  a.seg = reinterpret_cast<int32_t*>(ws + L.seg);
+  a.partial = reinterpret_cast<float*>(ws + L.partial);
+  a.ld_partial = L.ld_partial;
+  HIPCHK(ctx, psgd::launch_embed_grad(a, dt, (int)id_type, stream), "embedding gradient");
   return PSGD_OK;
 }
 

@@ -1,6 +1,7 @@
-"""One group of gradient matrices compressed together, over torch device tensors.
+"""Groups of matrices over torch device tensors: gradients compressed together, and updates
+orthogonalised together.
 
-Holds the context, the plan and the per-step device words (flags, skip), and calls the three
+PowerSGDGroup holds the context, the plan and the per-step device words (flags, skip), and calls the three
 entry points in order. All compute happens in libpsgd.so.
 """
 from __future__ import annotations
@@ -110,6 +111,49 @@ class PowerSGDGroup:
             B.psgd_adam_update(self.ctx, ts, self.skip, self.adam_step, self.adam_norm, hp_pass or hp, stream)
         return s
 
+    def attach_muon(self, params: Sequence, momentum: Sequence, accurate: Optional[bool] = None):
+        """Attach per-matrix Muon state (caller-owned device tensors, updated in place): params
+        m x n (fp16, bf16 or fp32), momentum m x n fp32. The group needs its out buffers
+        (write_out). accurate: products as exact as fp32 ones; default: for fp32 parameters,
+        whose rounding the fast products' 2e-3 of the update would exceed."""
+        torch = self.torch
+        self.muon_params, self.momentum = list(params), list(momentum)
+        if accurate is None:
+            accurate = self.muon_params[0].dtype == torch.float32
+        if any(p.dtype != self.muon_params[0].dtype for p in self.muon_params):
+            raise B.PsgdError("psgd_muon_attach", B.PSGD_EDTYPE, "parameters must have one dtype")
+        if len(self.muon_params) != len(self.err) or len(self.momentum) != len(self.err):
+            raise B.PsgdError("psgd_muon_attach", B.PSGD_EINVAL, "one param and one momentum per matrix")
+        for p, e in zip(self.muon_params, self.err):
+            if tuple(p.shape) != tuple(e.shape):
+                raise B.PsgdError("psgd_muon_attach", B.PSGD_EINVAL, "param and matrix shapes differ")
+        B._same_device("psgd_muon_attach", self.flags, *self.muon_params, *self.momentum)
+        opt = [B.make_muon_matrix(p, m) for p, m in zip(self.muon_params, self.momentum)]
+        B.psgd_muon_attach(self.ctx, self.plan, opt, B._dtype(self.muon_params[0], "psgd_muon_attach"),
+                           B.PSGD_NS_ACCURATE if accurate else B.PSGD_NS_FAST)
+        if not hasattr(self, "adam_step"):
+            dev = self.flags.device
+            self.adam_step = torch.zeros(1, dtype=torch.int32, device=dev)
+            self.adam_norm = torch.zeros(2, dtype=torch.float32, device=dev)
+
+    def step_muon(self, hp, passthrough: Sequence = (), hp_pass=None, max_norm: float = 0.0,
+                  host: bool = False, stream=None):
+        """One step with Muon on the matrices: compress, finite check, global norm and clipping,
+        decompression, momentum and orthogonalised update, fp32 Adam (hp_pass) on the
+        pass-through tensors. passthrough: (param, m1, m2, grad) fp32 tensors, e.g. an embedding
+        with its psgd_embed_grad gradient."""
+        if passthrough and hp_pass is None:
+            raise ValueError("pass-through tensors need their Adam hyperparameters (hp_pass)")
+        self.compress(stream)
+        s = self.check_finite([t[3] for t in passthrough], host, stream)
+        ts = [B.make_adam_tensor(*t) for t in passthrough]
+        B.psgd_adam_prepare(self.ctx, self.plan, ts, max_norm, self.skip, self.adam_step, self.adam_norm, stream)
+        self.decompress_update(stream)
+        B.psgd_muon_update(self.ctx, self.plan, self.skip, self.adam_norm, hp, stream)
+        if ts:
+            B.psgd_adam_update(self.ctx, ts, self.skip, self.adam_step, self.adam_norm, hp_pass, stream)
+        return s
+
     def step(self, passthrough: Sequence = (), host: bool = False, stream=None):
         self.compress(stream)
         s = self.check_finite(passthrough, host, stream)
@@ -119,6 +163,52 @@ class PowerSGDGroup:
     def close(self):
         if getattr(self, "plan", None):
             B.psgd_plan_destroy(self.plan)
+            self.plan = None
+        if getattr(self, "ctx", None):
+            B.psgd_destroy(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class NewtonSchulzGroup:
+    """Update matrices orthogonalised together: out[i] = Newton-Schulz(updates[i]) on run().
+
+    updates, outs: lists of 2-D device tensors (unit row stride), each list of one dtype (fp16,
+                   bf16 or fp32); out may be its update itself. The buffers are captured.
+    accurate: products as exact as fp32 ones (default: unless the outputs are bf16, whose rounding
+              is as large as the fast products' error)
+    """
+
+    def __init__(self, updates: Sequence, outs: Sequence, accurate: Optional[bool] = None):
+        import torch
+        self.ctx = self.plan = None
+        self.updates, self.outs = list(updates), list(outs)
+        call = "psgd_ns_plan_create"
+        if not self.updates or len(self.updates) != len(self.outs):
+            raise B.PsgdError(call, B.PSGD_EINVAL, "need one out per update, and at least one")
+        for ts in (self.updates, self.outs):
+            if any(t.dtype != ts[0].dtype for t in ts):
+                raise B.PsgdError(call, B.PSGD_EDTYPE, "updates and outs must each have one dtype")
+        if accurate is None:
+            accurate = self.outs[0].dtype != torch.bfloat16
+        mats = [B.make_ns_matrix(u, o) for u, o in zip(self.updates, self.outs)]
+        it, ot = B._dtype(self.updates[0], call), B._dtype(self.outs[0], call)
+        B._same_device(call, *self.updates, *self.outs)
+        self.device = self.updates[0].device
+        self.ctx = B.psgd_create(self.device.index or 0, 1)
+        self.plan = B.psgd_ns_plan_create(self.ctx, mats, it, ot, B.PSGD_NS_ACCURATE if accurate else B.PSGD_NS_FAST)
+
+    def run(self, hp=None, stream=None):
+        B.psgd_newton_schulz(self.ctx, self.plan, hp, B._stream(stream, self.device))
+
+    def close(self):
+        if getattr(self, "plan", None):
+            B.psgd_ns_plan_destroy(self.plan)
             self.plan = None
         if getattr(self, "ctx", None):
             B.psgd_destroy(self.ctx)

@@ -1,0 +1,328 @@
+"""Newton-Schulz orthogonalisation and the Muon step against the float64 oracle.
+
+Tolerances, as a share of the result's Frobenius norm, on top of the output's own rounding
+(at most eps/2 per element):
+  accurate  1e-4. The hi + lo halves leave 2^-22 of every factor and the sums 2^-24 sqrt(K). Five
+            steps multiply what a matrix of small singular values carries by up to 3.4445^5 = 485,
+            noise and signal alike; noise that lands in directions the update lacks (a share of up
+            to sqrt(s / rank) = 4 here) grows with nothing beside it: 485 * 2^-24 * 3 = 9e-5.
+  fast      5e-3. One rounding to fp16 is 2^-12 at most, 1.0e-4 in the mean square. A holds three
+            (two factors, its own storage): 1.7e-4 of A. B's derivative in A stays below 4.8 and
+            adds its own storage (2.8 of B's bound): 4.8 * 1.46 * 1.7e-4 + 2.8e-4 = 1.5e-3; the
+            factor X of B X: 2.8e-4. Per step sqrt(1.5^2 + 0.28^2) 1e-3 * 1.2 = 1.8e-3, five
+            independent steps sqrt(5) times that: 4.1e-3.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import oracle
+from tests.gpu_helpers import log
+
+pytestmark = pytest.mark.gpu
+
+ACC_TOL, FAST_TOL = 1e-4, 5e-3
+EPS2 = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}
+
+
+def _dt(code):
+    import torch
+    return {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}[code]
+
+
+def _np(t):
+    return t.detach().to("cpu").double().numpy()
+
+
+def _update(m, n, seed, rank=None):
+    rng = np.random.default_rng(seed)
+    if rank is None:
+        return rng.standard_normal((m, n)) * np.exp(rng.uniform(np.log(1e-2), 0.0, (m, 1)))
+    return rng.standard_normal((m, rank)) @ rng.standard_normal((rank, n))
+
+
+def _check(got, want, out, accurate, what):
+    norm = np.linalg.norm(want)
+    err = np.linalg.norm(got - want)
+    tol = (ACC_TOL if accurate else FAST_TOL) * norm + EPS2[out] * np.linalg.norm(want)
+    log(f"  {what}: {err / max(norm, 1e-300):.2e} of the norm, allowed {tol / max(norm, 1e-300):.2e}")
+    assert err <= tol, (what, err, tol)
+
+
+SHAPES = [(1, 1), (1, 9), (7, 1), (16, 16), (63, 65), (130, 511), (257, 128), (64, 1025), (333, 300)]
+
+
+@pytest.mark.parametrize("accurate", [True, False])
+@pytest.mark.parametrize("inp,out", [("f32", "f32"), ("f32", "bf16"), ("f16", "f16"), ("bf16", "f32")])
+def test_group_of_odd_shapes(inp, out, accurate):
+    import torch
+    from rank_gradient_compression_powersgd_amd import NewtonSchulzGroup
+    ups = [torch.from_numpy(_update(m, n, 10 + i)).to(_dt(inp)).cuda() for i, (m, n) in enumerate(SHAPES)]
+    outs = [torch.empty(u.shape, dtype=_dt(out), device="cuda") for u in ups]
+    log(f"newton-schulz {inp} -> {out} accurate={accurate}")
+    g = NewtonSchulzGroup(ups, outs, accurate)
+    g.run()
+    torch.cuda.synchronize()
+    first = [o.clone() for o in outs]
+    for u, o, sh in zip(ups, outs, SHAPES):
+        _check(_np(o), oracle.newton_schulz(_np(u)), out, accurate, sh)
+    g.run()
+    torch.cuda.synchronize()
+    for a, b in zip(first, outs):
+        assert torch.equal(a, b)                     # bit-reproducible
+    g.close()
+
+
+@pytest.mark.parametrize("accurate", [True, False])
+@pytest.mark.parametrize("shapes", [[(700, 333)], [(496, 1984), (1984, 496)], [(1001, 777)] * 5])
+def test_larger_groups_and_low_rank(shapes, accurate):
+    """Both tile sizes, tall and wide, full and low rank (an update of few directions must gain
+    no others)."""
+    import torch
+    from rank_gradient_compression_powersgd_amd import NewtonSchulzGroup
+    src = [_update(m, n, 50 + i, None if i % 2 == 0 else max(1, min(m, n) // 13)) for i, (m, n) in enumerate(shapes)]
+    ups = [torch.from_numpy(u).float().cuda() for u in src]
+    outs = [torch.empty_like(u) for u in ups]
+    log(f"newton-schulz {shapes} accurate={accurate}")
+    g = NewtonSchulzGroup(ups, outs, accurate)
+    g.run()
+    torch.cuda.synchronize()
+    for u, o, sh in zip(ups, outs, shapes):
+        _check(_np(o), oracle.newton_schulz(_np(u)), "f32", accurate, sh)
+    g.close()
+
+
+@pytest.mark.parametrize("steps,coef", [(1, oracle.muon.QUINTIC), (2, oracle.muon.QUINTIC), (12, (1.5, -0.5, 0.0))])
+def test_steps_and_coefficients(steps, coef):
+    import torch
+    from rank_gradient_compression_powersgd_amd import NewtonSchulzGroup, ns_hparams
+    u = torch.from_numpy(_update(150, 90, 3)).float().cuda()
+    o = torch.empty_like(u)
+    g = NewtonSchulzGroup([u], [o])
+    g.run(ns_hparams(*coef, steps=steps))
+    torch.cuda.synchronize()
+    _check(_np(o), oracle.newton_schulz(_np(u), tuple(float(np.float32(x)) for x in coef), steps), "f32", True, (steps, coef))
+    g.close()
+
+
+def test_strides_alignment_in_place_and_untouched_memory():
+    import torch
+    from rank_gradient_compression_powersgd_amd import NewtonSchulzGroup
+    m, n = 130, 77
+    u64 = _update(m, n, 7)
+    buf = torch.full((m + 2, n + 5), 9.0, dtype=torch.float32, device="cuda")
+    up = buf[1:m + 1, 3:n + 3]                       # rows start at odd 4-byte addresses
+    up.copy_(torch.from_numpy(u64))
+    obuf = torch.full((m + 2, n + 7), 5.0, dtype=torch.float32, device="cuda")
+    o = obuf[1:m + 1, 1:n + 1]
+    flat = torch.full((m * n + 3,), 2.0, dtype=torch.float32, device="cuda")
+    same = flat[1:1 + m * n].view(m, n)
+    same.copy_(torch.from_numpy(u64))
+    want = oracle.newton_schulz(_np(up))
+    g, h = NewtonSchulzGroup([up], [o]), NewtonSchulzGroup([same], [same])
+    g.run()
+    h.run()
+    torch.cuda.synchronize()
+    _check(_np(o), want, "f32", True, "strided")
+    _check(_np(same), want, "f32", True, "in place")
+    keep = torch.ones_like(obuf, dtype=torch.bool)
+    keep[1:m + 1, 1:n + 1] = False
+    assert bool((obuf[keep] == 5.0).all())
+    assert float(flat[0]) == 2.0 and bool((flat[1 + m * n:] == 2.0).all())
+    g.close()
+    h.close()
+
+
+def test_zero_tiny_huge_and_non_finite_updates():
+    """A zero update gives zeros; the scale of an update does not matter over fp32's range; a
+    non-finite element spoils its own matrix only, and nothing of it is left for the next call."""
+    import torch
+    from rank_gradient_compression_powersgd_amd import NewtonSchulzGroup
+    base = _update(96, 130, 21)
+    ups = [torch.from_numpy(x).float().cuda() for x in
+           (np.zeros((96, 130)), base * 1e-18, base * 1e30, base, base, base)]
+    ups[4][5, 6] = float("inf")
+    ups[5][95, 129] = float("nan")
+    outs = [torch.empty_like(u) for u in ups]
+    g = NewtonSchulzGroup(ups, outs)
+    g.run()
+    torch.cuda.synchronize()
+    assert bool((outs[0] == 0).all())
+    want = oracle.newton_schulz(base)
+    for i in (1, 2, 3):
+        _check(_np(outs[i]), want, "f32", True, f"scale {i}")
+    assert bool(outs[4].isnan().all()) and bool(outs[5].isnan().all())
+    clean = outs[3].clone()
+    ups[4].copy_(ups[3])
+    ups[5].copy_(ups[3])
+    g.run()
+    torch.cuda.synchronize()
+    for i in (3, 4, 5):
+        assert torch.equal(outs[i], clean)
+    g.close()
+
+
+def test_other_stream_and_graph_replays():
+    import torch
+    from rank_gradient_compression_powersgd_amd import NewtonSchulzGroup
+    shapes = [(200, 120), (64, 300)]
+    ups = [torch.from_numpy(_update(m, n, 31 + i)).float().cuda() for i, (m, n) in enumerate(shapes)]
+    outs, ref = [torch.empty_like(u) for u in ups], [torch.empty_like(u) for u in ups]
+    g, h = NewtonSchulzGroup(ups, outs), NewtonSchulzGroup(ups, ref)
+    h.run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    g.run(stream=side)
+    side.synchronize()
+    for a, b in zip(outs, ref):
+        assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        g.run()
+    for t in range(3):
+        for i, (m, n) in enumerate(shapes):
+            ups[i].copy_(torch.from_numpy(_update(m, n, 100 + 10 * t + i)))
+        graph.replay()
+        h.run()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, ref):
+            assert torch.equal(a, b), t
+    g.close()
+    h.close()
+
+
+# ---- the Muon step -------------------------------------------------------------------------
+def _muon_group(shapes, pdt, seed, rank=16):
+    import torch
+    from rank_gradient_compression_powersgd_amd import PowerSGDGroup
+    rng = np.random.default_rng(seed)
+    grads = [torch.from_numpy(rng.standard_normal(s)).half().cuda() for s in shapes]
+    q0 = [torch.from_numpy(rng.standard_normal((s[1], rank))).float() for s in shapes]
+    g = PowerSGDGroup(grads, [0] * len(shapes), torch.ones(1, device="cuda"), rank, q0)
+    params = [torch.from_numpy(rng.standard_normal(s) * 0.02).to(_dt(pdt)).cuda() for s in shapes]
+    mom = [torch.from_numpy(rng.standard_normal(s) * 0.3).float().cuda() for s in shapes]
+    return g, params, mom
+
+
+def _check_muon(got_p, got_m, want_p, want_m, old_p, pdt, accurate, hp, what):
+    # momentum: three fp32 roundings (two products, one sum) of values no larger than the terms
+    assert np.linalg.norm(got_m - want_m) <= 4 * 2.0 ** -24 * (np.linalg.norm(want_m) * 2), what
+    upd = np.linalg.norm(want_p - old_p * (1 - hp.lr * hp.weight_decay))
+    tol = (ACC_TOL if accurate else FAST_TOL) * upd + (EPS2[pdt] + 3 * 2.0 ** -24) * np.linalg.norm(want_p)
+    err = np.linalg.norm(got_p - want_p)
+    log(f"  {what}: param off by {err:.2e}, allowed {tol:.2e}")
+    assert err <= tol, (what, err, tol)
+
+
+@pytest.mark.parametrize("pdt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("nesterov,adjust", [(True, 1), (False, 0)])
+def test_muon_step_against_oracle(pdt, nesterov, adjust):
+    import torch
+    from rank_gradient_compression_powersgd_amd import muon_hparams, psgd_muon_update
+    shapes = [(130, 264), (300, 72), (64, 64)]
+    g, params, mom = _muon_group(shapes, pdt, 400)
+    hp = muon_hparams(0.02, 0.9, 0.1, nesterov, adjust)
+    g.attach_muon(params, mom)
+    for i, o in enumerate(g.out):
+        o.copy_(torch.from_numpy(_update(*shapes[i], 70 + i)))
+    skip = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for norm in (None, torch.tensor([4.0, 0.25], device="cuda")):
+        old_p, old_m = [_np(p) for p in params], [_np(m) for m in mom]
+        psgd_muon_update(g.ctx, g.plan, skip, norm, hp)
+        torch.cuda.synchronize()
+        clip = 1.0 if norm is None else 0.25
+        for i in range(len(shapes)):
+            wp, wm = oracle.muon_step(old_p[i], old_m[i], _np(g.out[i]), clip, hp.lr, hp.momentum, hp.weight_decay, nesterov, adjust)
+            _check_muon(_np(params[i]), _np(mom[i]), wp, wm, old_p[i], pdt, pdt == "f32", hp, (shapes[i], clip))
+    before = [t.clone() for t in params + mom]
+    skip.fill_(1)
+    psgd_muon_update(g.ctx, g.plan, skip, None, hp)
+    torch.cuda.synchronize()
+    for a, b in zip(before, params + mom):
+        assert torch.equal(a, b)                    # a skipped step changes nothing
+    g.close()
+
+
+def test_training_steps_with_embedding():
+    """Embedding lookup, its gradient as a pass-through tensor, and the whole Muon step with Adam on
+    the embedding: three steps against the oracle, the last one skipped on a non-finite value that
+    only the embedding's gradient carries."""
+    import torch
+    from rank_gradient_compression_powersgd_amd import muon_hparams, psgd_embed_grad, psgd_embed_lookup
+    from rank_gradient_compression_powersgd_amd.binding import psgd_adam_hparams
+    shapes = [(96, 136), (200, 64)]
+    vocab, dim, tokens = 40, 96, 128
+    g, params, mom = _muon_group(shapes, "f32", 500, rank=16)
+    g.attach_muon(params, mom)
+    rng = np.random.default_rng(77)
+    table = torch.from_numpy(rng.standard_normal((vocab, dim)) * 0.02).float().cuda()
+    m1, m2, dtable = torch.zeros_like(table), torch.zeros_like(table), torch.empty_like(table)
+    hp, hpa = muon_hparams(0.01, 0.95, 0.01), psgd_adam_hparams(1e-3, 0.9, 0.999, 1e-8, 0.0)
+    state = oracle.AdamState(_np(table), _np(m1), _np(m2), "f32", "f32", "f32")
+    t = 0
+    for step in range(3):
+        ids = torch.from_numpy(rng.integers(-1, vocab, tokens)).cuda()
+        x = torch.empty(tokens, dim, dtype=torch.bfloat16, device="cuda")
+        psgd_embed_lookup(g.ctx, table, ids, x, 3.0)
+        dx = torch.from_numpy(rng.standard_normal((tokens, dim))).float().cuda()
+        if step == 2:
+            dx[int((ids >= 0).nonzero()[0]), 5] = float("nan")
+        psgd_embed_grad(g.ctx, dx, ids, dtable, 3.0)
+        for grad in g.grads:
+            grad.copy_(torch.from_numpy(rng.standard_normal(grad.shape)))
+        old_p, old_m = [_np(p) for p in params], [_np(m) for m in mom]
+        skip = g.step_muon(hp, [(table, m1, m2, dtable)], hpa, max_norm=5.0, host=True)
+        torch.cuda.synchronize()
+        assert skip == int(step == 2)
+        want_x = oracle.embed_lookup(state.theta, ids.cpu().numpy(), 3.0)
+        # bf16 rounding of a table that is itself off by a few fp32 roundings of Adam
+        assert np.linalg.norm(_np(x) - want_x) <= 2.0 ** -8 * 1.01 * np.linalg.norm(want_x)
+        if step == 2:
+            for a, b in zip(params + mom, old_p + old_m):
+                assert np.array_equal(_np(a), b)
+            assert int(g.adam_step.item()) == t
+            break
+        clip = float(g.adam_norm[1].item())
+        assert clip < 1.0
+        ge = oracle.embed_grad(_np(dx), ids.cpu().numpy(), vocab, 3.0)
+        norm = np.sqrt(sum(np.linalg.norm(_np(o)) ** 2 for o in g.out) + np.linalg.norm(ge) ** 2)
+        assert abs(float(g.adam_norm[0].item()) - norm) <= 1e-4 * norm
+        (state,), t, _, _ = oracle.adam_group_step([state], [ge * clip], t, False, hpa, hpa, n_mats=0, max_norm=0.0)
+        assert np.linalg.norm(_np(table) - state.theta) <= 1e-5 * np.linalg.norm(state.theta)
+        for i in range(len(shapes)):
+            wp, wm = oracle.muon_step(old_p[i], old_m[i], _np(g.out[i]), clip, hp.lr, hp.momentum, hp.weight_decay, True, 1)
+            _check_muon(_np(params[i]), _np(mom[i]), wp, wm, old_p[i], "f32", True, hp, (step, shapes[i]))
+    g.close()
+
+
+def test_muon_step_graph_replays_match_eager():
+    import torch
+    from rank_gradient_compression_powersgd_amd import muon_hparams
+    shapes = [(130, 264), (300, 72)]
+    hp = muon_hparams(0.02, 0.9, 0.1)
+    eager, pe, me = _muon_group(shapes, "bf16", 600)
+    cap, pc, mc = _muon_group(shapes, "bf16", 600)
+    eager.attach_muon(pe, me)
+    cap.attach_muon(pc, mc)
+    warm, pw, mw = _muon_group(shapes, "bf16", 600)
+    warm.attach_muon(pw, mw)
+    warm.step_muon(hp, max_norm=3.0)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        cap.step_muon(hp, max_norm=3.0)
+    torch.cuda.synchronize()
+    rng = np.random.default_rng(9)
+    for step in range(3):
+        for a, b in zip(eager.grads, cap.grads):
+            a.copy_(torch.from_numpy(rng.standard_normal(a.shape)))
+            b.copy_(a)
+        eager.step_muon(hp, max_norm=3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(pe + me + eager.err + [eager.adam_norm], pc + mc + cap.err + [cap.adam_norm]):
+            assert torch.equal(a, b), step
+    for x in (eager, cap, warm):
+        x.close()
