@@ -12,42 +12,52 @@
 // directions it lacks, which every step then multiplies by a = 3.4 (an update of rank 112 came
 // out 3% off, against 0.06%). The accurate products use both halves of every factor
 // (hi hi + hi lo + lo hi): the result agrees with fp32 products.
+#include <type_traits>
+
 #include "ns.h"
 
 namespace psgd {
 namespace {
 
-constexpr int GM_THREADS = 256;
+constexpr int KB = 32;                         // k per stage
+constexpr int RING = 4;                        // stages in LDS
 
 typedef short i16x4 __attribute__((ext_vector_type(4)));
+#define LDS __attribute__((address_space(3)))
 __device__ __forceinline__ i16x4 lds_read_tr16(const uint16_t* p) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4*)(p));
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(p));
 }
 
-// K-outer rows (LDS row = one k): the pair of 16-byte units a transposing read touches in each of
-// the rows k = 8 g + t (g = 0, 1; t = 0..3) must land on 8 distinct 32-byte groups of the banks.
+// K-outer rows (LDS row = one k, T values): a transposing read touches one pair of 16-byte units
+// in each of the rows k = 8 g + t (+ 4); the rows of lanes 0..31 (g = 0, 1; t = 0..3), and those
+// of lanes 32..63, must land on 8 distinct 32-byte groups of the 256 bytes of banks. Rows k and
+// k + 4 share their swizzle.
 template <int T> __device__ __forceinline__ int swz_outer(int k, int q) {
   if constexpr (T == 64) return q ^ (2 * (((k >> 1) & 1) | (((k >> 3) & 1) << 1)));   // 128-byte rows
-  else return q ^ (2 * ((k & 3) | (((k >> 3) & 1) << 2)));                            // 256-byte rows
+  else return q ^ (2 * ((k & 3) | (((k >> 3) & 1) << 2)));                            // 256 or 512
 }
-// K-contiguous rows are 128 bytes: 8 consecutive rows put one logical unit on 8 distinct groups.
-__device__ __forceinline__ int swz_inner(int row, int q) { return q ^ (row & 7); }
+// K-contiguous rows are 64 bytes (4 units): 8 consecutive rows put one logical unit on the 8
+// distinct 16-byte groups of one LDS pass.
+__device__ __forceinline__ int swz_inner(int row, int q) { return q ^ ((row >> 1) & 3); }
+
+// 16 bytes per lane from base + off (bytes) straight to LDS: lane x writes at l + 16 x. As asm, since
+// with the builtin the compiler waits for every such load before each transposing LDS read; the
+// waits are written out below (wait_loads). The load has no register output.
+__device__ __forceinline__ void load_lds16(const GLOBAL uint16_t* base, uint32_t off, uint32_t l) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(l), "v"(off), "s"(base) : "m0", "memory");
+}
+
+// All but the wave's n newest loads have landed, and its LDS reads have been answered. The builtin
+// rather than asm: the compiler then knows that the fragments are there. The empty asm keeps LDS
+// reads from moving across.
+template <int N> __device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+  asm volatile("" ::: "memory");
+}
 
 __device__ __forceinline__ float h2f(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
 __device__ __forceinline__ f32x4 h2f4(u32x2 v) { return __builtin_convertvector(__builtin_bit_cast(f16x4, v), f32x4); }
 __device__ __forceinline__ u32x2 f2h4(f32x4 v) { return __builtin_bit_cast(u32x2, __builtin_convertvector(v, f16x4)); }
-
-// hi + lo of four values stored at h and (LO) l
-template <bool LO> __device__ __forceinline__ void store_split(f32x4 v, GLOBAL uint16_t* h, GLOBAL uint16_t* l) {
-  const u32x2 hi = f2h4(v);
-  *gcast<u32x2>(h) = hi;
-  if constexpr (LO) *gcast<u32x2>(l) = f2h4(v - h2f4(hi));
-}
-template <bool LO> __device__ __forceinline__ void store_split1(float v, GLOBAL uint16_t* h, GLOBAL uint16_t* l) {
-  const uint16_t hi = f16_bits((_Float16)v);
-  *h = hi;
-  if constexpr (LO) *l = f16_bits((_Float16)(v - h2f(hi)));
-}
 
 template <int OT> __device__ __forceinline__ float out_load(const void* p, int64_t i) {
   if constexpr (OT == G_F32) return gbl(static_cast<const float*>(p))[i];
@@ -60,31 +70,56 @@ template <int OT> __device__ __forceinline__ void out_store(void* p, int64_t i, 
   else gbl(static_cast<uint16_t*>(p))[i] = bf16_bits((__bf16)v);
 }
 
-// ST: stage. T: C tile side (four waves of T/2 x T/2). ACC: accurate products. OT: 0, or the
-// output type of the last update. MFMA layout: operand P gives the rows i of a C tile, Q the
-// columns j; a lane holds C[4 g .. 4 g + 3][c], four consecutive i. For the update i runs along
-// l and j along s, so those four are consecutive in memory.
+template <int OT> __device__ __forceinline__ f32x4 out_load4(const void* p, int64_t i) {
+  if constexpr (OT == G_F32) return *gcast<f32x4>(gbl(static_cast<const float*>(p)) + i);
+  else return GradIO<OT>::load4(gcast<char>(gbl(static_cast<const uint16_t*>(p)) + i));
+}
+template <int OT> __device__ __forceinline__ void out_store4(void* p, int64_t i, f32x4 v) {
+  if constexpr (OT == G_F32) *gcast<f32x4>(gbl(static_cast<float*>(p)) + i) = v;
+  else if constexpr (OT == G_F16) *gcast<u32x2>(gbl(static_cast<uint16_t*>(p)) + i) = f2h4(v);
+  else *gcast<u32x2>(gbl(static_cast<uint16_t*>(p)) + i) = __builtin_bit_cast(u32x2, __builtin_convertvector(v, bf16x4));
+}
+
+template <int T> struct Tile {
+  static constexpr int WAVES = T == 256 ? 8 : 4;
+  static constexpr int THREADS = WAVES * kWave;
+  static constexpr int WN = T == 256 ? 4 : 2;              // waves along j; 2 along i
+  static constexpr int TA = T / 32, TB = T / (16 * WN);    // 16-wide MFMA tiles per wave along i, j
+  static constexpr int BYTES = T * KB * 2;                 // one operand's stage
+  static constexpr int LOADS = 2 * BYTES / (WAVES * 1024); // 1 KB loads per wave and stage
+};
+
+// ST: stage. T: C tile side. ACC: accurate products. OT: 0, or the output type of the last update.
+// MFMA layout: operand P gives the rows i of a C tile, Q the columns j; a lane holds C[4 g .. 4 g
+// + 3][c], four consecutive i. For the update i runs along l and j along s, so those four are
+// consecutive in memory.
+//
+// Main loop. Stages of 32 k go straight from L2 to a ring of four LDS buffers (16 bytes per lane,
+// the global addresses carry the swizzle), three stages ahead of their use. While stage j is
+// multiplied out of registers, the fragments of stage j + 1 are read from LDS into the other set,
+// so the MFMAs after a barrier depend on nothing younger than it. One barrier per stage: it
+// says that stage j + 1 has landed for every wave and that every wave has read stage j out of the
+// buffer that stage j + 4 is then loaded into. Accurate products take the hi and the lo plane of
+// 32 k as two stages: hi hi in the first, lo hi + hi lo in the second.
 template <int ST, int T, bool ACC, int OT>
-__global__ __launch_bounds__(GM_THREADS, 2)
+__global__ __launch_bounds__(Tile<T>::THREADS, 2)
 void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, int step, NsArgs na)
 {
   if (na.skip && *na.skip != 0) return;
   const Work wi = work[xcd_remap(blockIdx.x, gridDim.x)];
   if (wi.mat < 0) return;
   const NsMat& d = mats[wi.mat];
+  using TL = Tile<T>;
   constexpr bool OUTER = ST == NS_UPDATE;      // P is read K-outer
-  constexpr int KS = ACC ? 32 : 64;            // k per stage: 128 bytes per row either way
-  constexpr int UN = T / 32;                   // 16-byte units per thread and operand
-  constexpr int WT = T / 32;                   // 16-row tiles per wave and side
   const int cur = step & 1;
   const int i0 = wi.a, j0 = wi.b;
-  const int lane = threadIdx.x & (kWave - 1), wv = threadIdx.x / kWave;
+  const int lane = threadIdx.x & (kWave - 1), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wv & 1, wn = wv >> 1;
+  const int wi0 = wm * (T / 2), wj0 = wn * (T / TL::WN);
   const int c = lane & 15, g = lane >> 4;
 
   const GLOBAL uint16_t *ph, *pl, *qh, *ql;
-  int64_t ldp, ldq;
-  int K;
+  int ldp, ldq, K;
   if constexpr (ST == NS_GRAM) {
     ph = qh = gbl(d.xh[cur]); pl = ql = gbl(d.xl[cur]); ldp = ldq = d.lp; K = d.l;
   } else if constexpr (ST == NS_POLY) {
@@ -93,156 +128,322 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, in
     ph = gbl(d.xh[cur]); pl = gbl(d.xl[cur]); ldp = d.lp;
     qh = gbl(d.bh); ql = gbl(d.bl); ldq = d.sp; K = d.s;
   }
-  const int nsteps = (K + KS - 1) / KS;        // the padding up to a whole tile holds zeros
+  // whole pairs of 32 k (the padding up to a tile holds zeros); accurate: two stages per 32 k
+  const int nst = 2 * ((K + 63) / 64) * (ACC ? 2 : 1);
 
-  __shared__ __attribute__((aligned(16))) uint16_t ldsP[2][T * 64], ldsQ[2][T * 64];
-  const GLOBAL uint16_t* psrc[UN];
-  const GLOBAL uint16_t* qsrc[UN];
+  __shared__ __attribute__((aligned(16))) uint16_t lds[RING][TL::BYTES];     // P, then Q
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS uint16_t*)&lds[0][0];
+  // this wave's loads of a stage: load x < PL is 1 KB of P, the others of Q
+  constexpr int PL = TL::LOADS / 2;
+  uint32_t poff[PL], qoff[PL];
+  const GLOBAL uint16_t* const pbase_h = OUTER ? ph + i0 : ph + (int64_t)i0 * ldp;
+  const GLOBAL uint16_t* const qbase_h = qh + (int64_t)j0 * ldq;
+  const GLOBAL uint16_t* const pbase_l = OUTER ? pl + i0 : pl + (int64_t)i0 * ldp;
+  const GLOBAL uint16_t* const qbase_l = ql + (int64_t)j0 * ldq;
 #pragma unroll
-  for (int j = 0; j < UN; ++j) {
-    const int e = threadIdx.x + GM_THREADS * j;
-    const int row = e >> 3, q = swz_inner(row, e & 7);
-    const GLOBAL uint16_t* qb = ACC && q >= 4 ? ql : qh;
-    qsrc[j] = qb + (int64_t)(j0 + row) * ldq + 8 * (ACC ? (q & 3) : q);
+  for (int x = 0; x < PL; ++x) {
+    const int e = (wv * PL + x) * kWave + lane;              // 16-byte slot of the operand's stage
+    qoff[x] = ((uint32_t)(e >> 2) * (uint32_t)ldq + 8u * swz_inner(e >> 2, e & 3)) * 2u;
     if constexpr (OUTER) {
-      const int k = e / (T / 8), u = swz_outer<T>(k, e % (T / 8));
-      const GLOBAL uint16_t* pb = ACC && k >= 32 ? pl : ph;
-      psrc[j] = pb + (int64_t)(ACC ? (k & 31) : k) * ldp + i0 + 8 * u;
+      const int k = e / (T / 8);
+      poff[x] = ((uint32_t)k * (uint32_t)ldp + 8u * swz_outer<T>(k, e % (T / 8))) * 2u;
     } else {
-      const GLOBAL uint16_t* pb = ACC && q >= 4 ? pl : ph;
-      psrc[j] = pb + (int64_t)(i0 + row) * ldp + 8 * (ACC ? (q & 3) : q);
+      poff[x] = ((uint32_t)(e >> 2) * (uint32_t)ldp + 8u * swz_inner(e >> 2, e & 3)) * 2u;
     }
   }
-  u32x4 rp[UN], rq[UN];
-  auto load_stage = [&](int ks) {
-    const int64_t kp = OUTER ? (int64_t)ks * KS * ldp : (int64_t)ks * KS, kq = (int64_t)ks * KS;
-#pragma unroll
-    for (int j = 0; j < UN; ++j) {
-      rp[j] = *gcast<u32x4>(psrc[j] + kp);
-      rq[j] = *gcast<u32x4>(qsrc[j] + kq);
-    }
-  };
-  auto store_stage = [&](int buf) {
-#pragma unroll
-    for (int j = 0; j < UN; ++j) {
-      const int e = threadIdx.x + GM_THREADS * j;
-      *reinterpret_cast<u32x4*>(&ldsP[buf][8 * e]) = rp[j];
-      *reinterpret_cast<u32x4*>(&ldsQ[buf][8 * e]) = rq[j];
-    }
+  // load x of stage j: P and Q in turn
+  auto load_part = [&](int j, int x) {
+    const int ks = ACC ? j >> 1 : j;
+    const uint32_t l = lds0 + (uint32_t)(j % RING) * (2 * TL::BYTES) + wv * (PL * 1024) + (x >> 1) * 1024;
+    if (x & 1) load_lds16((ACC && (j & 1) ? qbase_l : qbase_h) + (int64_t)ks * KB, qoff[x >> 1], l + TL::BYTES);
+    else load_lds16((ACC && (j & 1) ? pbase_l : pbase_h) + (OUTER ? (int64_t)ks * KB * ldp : (int64_t)ks * KB), poff[x >> 1], l);
   };
 
-  f32x4 acc[WT][WT];
+  f32x4 acc[TL::TA][TL::TB];
 #pragma unroll
-  for (int a = 0; a < WT; ++a)
+  for (int a = 0; a < TL::TA; ++a)
 #pragma unroll
-    for (int b = 0; b < WT; ++b) acc[a][b] = f32x4{0, 0, 0, 0};
+    for (int b = 0; b < TL::TB; ++b) acc[a][b] = f32x4{0, 0, 0, 0};
 
-  // fragment h (k half of a fast stage; 0 hi, 1 lo of an accurate one)
-  auto frag_inner = [&](const uint16_t* l, int row, int h) {
-    return *reinterpret_cast<const f16x8*>(&l[row * 64 + 8 * swz_inner(row, 4 * h + g)]);
-  };
-  auto frag_outer = [&](const uint16_t* l, int col, int h) {
-    const int k = 32 * h + 8 * g + (c >> 2), q = col / 8 + ((c & 3) >> 1);
-    const uint16_t* p = &l[k * T + 8 * swz_outer<T>(k, q) + 4 * (c & 1)];
-    const i16x4 x = lds_read_tr16(p), y = lds_read_tr16(p + 4 * T);
-    return __builtin_bit_cast(f16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
-  };
-  auto compute = [&](int buf) {
-    f16x8 q[2][WT];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int b = 0; b < WT; ++b) q[h][b] = frag_inner(ldsQ[buf], wn * (T / 2) + 16 * b + c, h);
-#pragma unroll
-    for (int a = 0; a < WT; ++a) {
-      f16x8 p[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = wm * (T / 2) + 16 * a;
-        if constexpr (OUTER) p[h] = frag_outer(ldsP[buf], r, h);
-        else p[h] = frag_inner(ldsP[buf], r + c, h);
-      }
-#pragma unroll
-      for (int b = 0; b < WT; ++b) {
-        acc[a][b] = mfma_f16(p[0], q[0][b], acc[a][b]);
-        if constexpr (ACC) {
-          acc[a][b] = mfma_f16(p[0], q[1][b], acc[a][b]);
-          acc[a][b] = mfma_f16(p[1], q[0][b], acc[a][b]);
-        } else {
-          acc[a][b] = mfma_f16(p[1], q[1][b], acc[a][b]);
-        }
-      }
+  struct Frag { f16x8 p[TL::TA], q[TL::TB]; };
+  auto read_p = [&](Frag& f, int j, int a) {
+    const uint16_t* lp = lds[j % RING];
+    if constexpr (OUTER) {
+      const int k = 8 * g + (c >> 2), u = (wi0 + 16 * a) / 8 + ((c & 3) >> 1);
+      const uint16_t* s = &lp[k * T + 8 * swz_outer<T>(k, u) + 4 * (c & 1)];
+      const i16x4 x = lds_read_tr16(s), y = lds_read_tr16(s + 4 * T);
+      f.p[a] = __builtin_bit_cast(f16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      const int r = wi0 + 16 * a + c;
+      f.p[a] = *reinterpret_cast<const f16x8*>(&lp[r * KB + 8 * swz_inner(r, g)]);
     }
+  };
+  auto read_q = [&](Frag& f, int j, int b) {
+    const uint16_t* lq = lds[j % RING] + TL::BYTES / 2;
+    const int r = wj0 + 16 * b + c;
+    f.q[b] = *reinterpret_cast<const f16x8*>(&lq[r * KB + 8 * swz_inner(r, g)]);
+  };
+  // One pass over the wave's MFMA tiles, row by row; `before(a)` is issued ahead of row a's MFMAs
+  // and `after(a)` behind them, so that LDS reads and stage loads trickle in between MFMAs that do
+  // not depend on them.
+  auto mul = [&](const Frag& fp, const Frag& fq, auto before, auto after) {
+#pragma unroll
+    for (int a = 0; a < TL::TA; ++a) {
+      before(a);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int b = 0; b < TL::TB; ++b) acc[a][b] = mfma_f16(fp.p[a], fq.q[b], acc[a][b]);
+      __builtin_amdgcn_sched_barrier(0);
+      after(a);
+    }
+  };
+  auto none = [](int) {};
+  // Before stage j is multiplied: stage j + 1 has landed (BEHIND later stages may still be under
+  // way) and nobody reads stage j's buffer any more.
+  auto turn = [&](auto behind) {
+    wait_loads<decltype(behind)::value * TL::LOADS>();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  Frag f0, f1;
+  // stages j (even) and j + 1; send: stages j + 4 and j + 5 are sent for; more: stage j + 2 follows
+  // and its first fragments are read
+  auto pair = [&](int j, auto behind0, auto behind1, auto send, auto more) {
+    constexpr bool SEND = decltype(send)::value, MORE = decltype(more)::value;
+    turn(behind0);
+    mul(f0, f0, [&](int a) {
+      if (a < TL::TB) read_q(f1, j + 1, a);
+      read_p(f1, j + 1, a);
+      if (SEND && a < TL::LOADS) load_part(j + RING, a);
+    }, none);
+    if constexpr (MORE) turn(behind1);
+    if constexpr (ACC) {
+      mul(f1, f0, [&](int a) { if (SEND && a < TL::LOADS) load_part(j + 1 + RING, a); }, none);
+      // f0.q is free from here on, and each f0.p[a] behind its last row
+      mul(f0, f1, [&](int a) { if (MORE && a < TL::TB) read_q(f0, j + 2, a); }, [&](int a) { if (MORE) read_p(f0, j + 2, a); });
+    } else {
+      mul(f1, f1, [&](int a) {
+        if (MORE && a < TL::TB) read_q(f0, j + 2, a);
+        if (MORE) read_p(f0, j + 2, a);
+        if (SEND && a < TL::LOADS) load_part(j + 1 + RING, a);
+      }, none);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  using N0 = std::integral_constant<int, 0>;
+  using N1 = std::integral_constant<int, 1>;
+  using N2 = std::integral_constant<int, 2>;
+  using Yes = std::true_type;
+  using No = std::false_type;
+  auto load_stage = [&](int j) {
+#pragma unroll
+    for (int x = 0; x < TL::LOADS; ++x) load_part(j, x);
   };
 
   load_stage(0);
-  store_stage(0);
-  __syncthreads();
-  for (int ks = 0; ks < nsteps; ++ks) {
-    if (ks + 1 < nsteps) load_stage(ks + 1);
-    compute(ks & 1);
-    if (ks + 1 < nsteps) store_stage((ks + 1) & 1);
-    __syncthreads();
+  load_stage(1);
+  if (nst > 2) {                               // nst is even
+    load_stage(2);
+    load_stage(3);
+    wait_loads<3 * TL::LOADS>();
+  } else {
+    wait_loads<TL::LOADS>();
   }
+  __builtin_amdgcn_s_barrier();
+#pragma unroll
+  for (int b = 0; b < TL::TB; ++b) read_q(f0, 0, b);
+#pragma unroll
+  for (int a = 0; a < TL::TA; ++a) read_p(f0, 0, a);
+  int j = 0;
+  for (; j + RING < nst; j += 2) pair(j, N2{}, N2{}, Yes{}, Yes{});
+  if (nst > 2) { pair(j, N2{}, N1{}, No{}, Yes{}); j += 2; }
+  pair(j, N0{}, N0{}, No{}, No{});
+
+  // ---- epilogue --------------------------------------------------------------------------
+  // Through this wave's own part of the ring, so that memory sees whole rows, 16 bytes a lane: a
+  // lane's accumulators are 8 bytes in each of 16 rows (stored as they lie they ran at a third of
+  // the bandwidth). 16-byte units are XOR-ed by their row, which keeps both sides conflict-free.
+  constexpr int WI = T / 2, WJ = T / TL::WN;                 // the wave's tile of C
+  __syncthreads();                                           // the ring is read out
+  uint16_t* const reg = &lds[0][0] + wv * (WI * WJ);
+  const uint32_t reg0 = lds0 + wv * (WI * WJ * 2);
+  const int ib = i0 + wi0, jb = j0 + wj0;
+
+  // rows j of WI values: a lane's four are half a unit
+  constexpr int UI = WI / 8, UJ = WJ / 8;
+  auto at_ji = [&](int a, int b) {
+    const int r = 16 * b + c, u = (2 * a + (g >> 1)) ^ (r & (UI - 1));
+    return reg + r * WI + 8 * u + 4 * (g & 1);
+  };
+  auto fetch = [&](const GLOBAL uint16_t* src, int ld) {
+#pragma unroll
+    for (int x = 0; x < WI * WJ / 512; ++x) {
+      const int e = x * kWave + lane, r = e / UI, u = (e % UI) ^ (r & (UI - 1));
+      load_lds16(src + (int64_t)jb * ld + ib, ((uint32_t)r * (uint32_t)ld + 8u * u) * 2u, reg0 + x * 1024);
+    }
+    wait_loads<0>();
+  };
+  auto add = [&](float f) {                                  // acc += f * fetched
+#pragma unroll
+    for (int a = 0; a < TL::TA; ++a)
+#pragma unroll
+      for (int b = 0; b < TL::TB; ++b) acc[a][b] += f * h2f4(*reinterpret_cast<const u32x2*>(at_ji(a, b)));
+    wait_loads<0>();
+  };
+  // the fp16 of acc (LO: of what rounding to it leaves) to rows j of dst
+  auto flush_ji = [&](GLOBAL uint16_t* dst, int ld, bool lo) {
+#pragma unroll
+    for (int a = 0; a < TL::TA; ++a)
+#pragma unroll
+      for (int b = 0; b < TL::TB; ++b) {
+        const u32x2 h = f2h4(acc[a][b]);
+        *reinterpret_cast<u32x2*>(at_ji(a, b)) = lo ? f2h4(acc[a][b] - h2f4(h)) : h;
+      }
+    GLOBAL uint16_t* o = dst + (int64_t)jb * ld + ib;
+#pragma unroll
+    for (int x = 0; x < WI * WJ / 512; ++x) {
+      const int e = x * kWave + lane, r = e / UI, u = e % UI;
+      *gcast<u32x4>(o + (int64_t)r * ld + 8 * u) = *reinterpret_cast<const u32x4*>(reg + r * WI + 8 * (u ^ (r & (UI - 1))));
+    }
+  };
+  // the same to rows i of dst
+  auto flush_ij = [&](GLOBAL uint16_t* dst, int ld, bool lo) {
+#pragma unroll
+    for (int a = 0; a < TL::TA; ++a)
+#pragma unroll
+      for (int b = 0; b < TL::TB; ++b) {
+        const u32x2 h = f2h4(acc[a][b]), v = lo ? f2h4(acc[a][b] - h2f4(h)) : h;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int r = 16 * a + 4 * g + t, u = (2 * b + (c >> 3)) ^ (r & (UJ - 1));
+          reg[r * WJ + 8 * u + (c & 7)] = (uint16_t)(v[t >> 1] >> (16 * (t & 1)));
+        }
+      }
+    GLOBAL uint16_t* o = dst + (int64_t)ib * ld + jb;
+#pragma unroll
+    for (int x = 0; x < WI * WJ / 512; ++x) {
+      const int e = x * kWave + lane, r = e / UJ, u = e % UJ;
+      *gcast<u32x4>(o + (int64_t)r * ld + 8 * u) = *reinterpret_cast<const u32x4*>(reg + r * WJ + 8 * (u ^ (r & (UJ - 1))));
+    }
+  };
+  // rows j >= s and columns i >= `imax` are padding and hold zeros, also beside NaN
+  auto mask = [&](int imax) {
+    if (ib + WI <= imax && jb + WJ <= d.s) return;
+#pragma unroll
+    for (int a = 0; a < TL::TA; ++a)
+#pragma unroll
+      for (int b = 0; b < TL::TB; ++b)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          if (ib + 16 * a + 4 * g + t >= imax || jb + 16 * b + c >= d.s) acc[a][b][t] = 0.0f;
+  };
 
   constexpr float kProd = ST == NS_GRAM ? kNsScaleA / (kNsScaleX * kNsScaleX)
                         : ST == NS_POLY ? kNsScaleB / (kNsScaleA * kNsScaleA)
                                         : 1.0f / kNsScaleB;
+  const float prod = ST == NS_POLY ? na.c * kProd : kProd;
 #pragma unroll
-  for (int a = 0; a < WT; ++a)
+  for (int a = 0; a < TL::TA; ++a)
 #pragma unroll
-    for (int b = 0; b < WT; ++b) {
-      const int i = i0 + wm * (T / 2) + 16 * a + 4 * g, j = j0 + wn * (T / 2) + 16 * b + c;
-      f32x4 v = kProd * acc[a][b];
-      if constexpr (ST != NS_UPDATE) {
-        // C[i..i+3][j]; rows and columns past s are zero
-        const int64_t ji = (int64_t)j * d.sp + i;
-        if constexpr (ST == NS_POLY) {
-          f32x4 av = h2f4(*gcast<u32x2>(gbl(d.ah) + ji));
-          if constexpr (ACC) av += h2f4(*gcast<u32x2>(gbl(d.al) + ji));
-          v = na.c * v + (na.b * kNsScaleB / kNsScaleA) * av;
-        }
-        GLOBAL uint16_t* oh = gbl(ST == NS_GRAM ? d.ah : d.bh);
-        GLOBAL uint16_t* ol = gbl(ST == NS_GRAM ? d.al : d.bl);
+    for (int b = 0; b < TL::TB; ++b) acc[a][b] *= prod;
+
+  if constexpr (ST != NS_UPDATE) {
+    if constexpr (ST == NS_POLY) {
+      fetch(gbl(d.ah), d.sp);
+      add(na.b * (kNsScaleB / kNsScaleA));
+      if constexpr (ACC) {
+        fetch(gbl(d.al), d.sp);
+        add(na.b * (kNsScaleB / kNsScaleA));
+      } else if (i0 == j0) {
+        // the fast form multiplies by a I + B: the hi half of a X comes out of the product
 #pragma unroll
-        for (int t = 0; t < 4; ++t) if (i + t >= d.s || j >= d.s) v[t] = 0.0f;
-        store_split<ACC>(v, oh + ji, ol + ji);
-        if (i0 != j0) {
+        for (int a = 0; a < TL::TA; ++a)
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int64_t ij = (int64_t)(i + t) * d.sp + j;
-            store_split1<ACC>(v[t], oh + ij, ol + ij);
-          }
-        }
-      } else {
-        // X[j][i..i+3]
-        const int64_t ji = (int64_t)j * d.lp + i;
-        v += na.a * (h2f4(*gcast<u32x2>(gbl(d.xh[cur]) + ji)) + h2f4(*gcast<u32x2>(gbl(d.xl[cur]) + ji)));
-        if constexpr (OT == 0) {
+          for (int b = 0; b < TL::TB; ++b)
 #pragma unroll
-          for (int t = 0; t < 4; ++t) if (i + t >= d.l || j >= d.s) v[t] = 0.0f;
-          store_split<true>(v, gbl(d.xh[cur ^ 1]) + ji, gbl(d.xl[cur ^ 1]) + ji);
-        } else {
-          v *= 1.0f / kNsScaleX;
+            for (int t = 0; t < 4; ++t)
+              if (ib + 16 * a + 4 * g + t == jb + 16 * b + c) acc[a][b][t] += na.a * kNsScaleB;
+      }
+    }
+    mask(d.s);
+    GLOBAL uint16_t* oh = gbl(ST == NS_GRAM ? d.ah : d.bh);
+    GLOBAL uint16_t* ol = gbl(ST == NS_GRAM ? d.al : d.bl);
+    flush_ji(oh, d.sp, false);
+    if constexpr (ACC) flush_ji(ol, d.sp, true);
+    if (i0 != j0) {
+      flush_ij(oh, d.sp, false);
+      if constexpr (ACC) flush_ij(ol, d.sp, true);
+    }
+  } else {
+    if constexpr (ACC) {
+      fetch(gbl(d.xh[cur]), d.lp);
+      add(na.a);
+    }
+    fetch(gbl(d.xl[cur]), d.lp);
+    add(na.a);
+    if constexpr (OT == 0) {
+      mask(d.l);
+      flush_ji(gbl(d.xh[cur ^ 1]), d.lp, false);
+      flush_ji(gbl(d.xl[cur ^ 1]), d.lp, true);
+    } else {
+      // half of the wave's i at a time, as fp32 rows of the output (rows i when X is transposed)
+      constexpr int HI = WI / 2;
+      float* const regf = reinterpret_cast<float*>(reg);
+      const bool vec = ((d.ld_out | d.n) & 3) == 0 && (reinterpret_cast<uintptr_t>(d.out) & (OT == G_F32 ? 15 : 7)) == 0;
+      const int cols = d.flip ? WJ : HI;
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            if (i + t >= d.l || j >= d.s) continue;
-            const int64_t o = d.flip ? (int64_t)(i + t) * d.ld_out + j : (int64_t)j * d.ld_out + i + t;
-            float x = v[t];
-            if (na.muon) {
-              const float th = out_load<OT>(d.out, o);
-              x = th - na.lr * (d.factor * x + na.weight_decay * th);
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int a = 0; a < TL::TA / 2; ++a)
+#pragma unroll
+          for (int b = 0; b < TL::TB; ++b) {
+            const f32x4 v = acc[h * (TL::TA / 2) + a][b] * (1.0f / kNsScaleX);
+            if (d.flip) {
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                const int r = 16 * a + 4 * g + t;
+                regf[r * WJ + 4 * ((4 * b + (c >> 2)) ^ (r & (WJ / 4 - 1))) + (c & 3)] = v[t];
+              }
+            } else {
+              const int r = 16 * b + c;
+              *reinterpret_cast<f32x4*>(&regf[r * HI + 4 * ((4 * a + g) ^ (r & (HI / 4 - 1)))]) = v;
             }
-            out_store<OT>(d.out, o, x);
+          }
+        const int row0 = d.flip ? ib + h * HI : jb, col0 = d.flip ? jb : ib + h * HI;
+        const int units = cols / 4;
+        for (int x = 0; x < HI * WJ / 256; ++x) {
+          const int e = x * kWave + lane, r = e / units, u = e % units;
+          const int row = row0 + r, col = col0 + 4 * u;
+          if (row >= d.m || col >= d.n) continue;
+          f32x4 v = *reinterpret_cast<const f32x4*>(&regf[r * cols + 4 * (u ^ (r & (units - 1)))]);
+          const int64_t o = (int64_t)row * d.ld_out + col;
+          if (vec) {
+            if (na.muon) {
+              const f32x4 th = out_load4<OT>(d.out, o);
+              v = th - na.lr * (d.factor * v + na.weight_decay * th);
+            }
+            out_store4<OT>(d.out, o, v);
+          } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              if (col + t >= d.n) continue;
+              float y = v[t];
+              if (na.muon) {
+                const float th = out_load<OT>(d.out, o + t);
+                y = th - na.lr * (d.factor * y + na.weight_decay * th);
+              }
+              out_store<OT>(d.out, o + t, y);
+            }
           }
         }
       }
     }
+  }
 }
 
 template <int ST, int T, bool ACC, int OT>
 void go(const NsMat* mats, const Work* work, int n_work, int step, const NsArgs& a, hipStream_t s) {
-  k_ns_gemm<ST, T, ACC, OT><<<dim3(n_work), dim3(GM_THREADS), 0, s>>>(mats, work, step, a);
+  k_ns_gemm<ST, T, ACC, OT><<<dim3(n_work), dim3(Tile<T>::THREADS), 0, s>>>(mats, work, step, a);
 }
 template <int T, bool ACC>
 hipError_t pick(NsStage st, int ot, bool last, const NsMat* mats, const Work* work, int n_work, int step,
@@ -261,6 +462,9 @@ hipError_t pick(NsStage st, int ot, bool last, const NsMat* mats, const Work* wo
 
 hipError_t launch_ns_gemm(NsStage st, int tile, bool accurate, int ot, bool last, const NsMat* mats,
                           const Work* work, int n_work, int step, const NsArgs& a, hipStream_t s) {
+  if (tile == 256)
+    return accurate ? pick<256, true>(st, ot, last, mats, work, n_work, step, a, s)
+                    : pick<256, false>(st, ot, last, mats, work, n_work, step, a, s);
   if (tile == 128)
     return accurate ? pick<128, true>(st, ot, last, mats, work, n_work, step, a, s)
                     : pick<128, false>(st, ot, last, mats, work, n_work, step, a, s);

@@ -2,6 +2,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <cstdlib>
 
 #include "ns.h"
 
@@ -61,6 +62,7 @@ hipError_t NsGroup::create(const std::vector<Item>& items, int in_type, int out_
   for (const Item& t : items)
     tiles += (rup(std::min(t.m, t.n), 128) / 128) * (rup(std::max(t.m, t.n), 128) / 128);
   tile_ = tiles >= 256 ? 128 : 64;
+  if (getenv("NS_TILE")) tile_ = atoi(getenv("NS_TILE"));
 
   std::vector<NsMat> mats(n);
   struct Off { size_t xh[2], xl[2], ah, al, bh, bl, partial; };
