@@ -357,7 +357,7 @@ typedef struct psgd_ns_hparams {
 } psgd_ns_hparams;
 
 /* One matrix of a group: in (m x n, in_dtype, read) and out (m x n, out_dtype, written), row-major
- * with any leading dimension >= n and the alignment of their element type; 1 <= m, n <= 2^28.
+ * with any leading dimension >= n and the alignment of their element type; 1 <= m, n <= 2^22.
  * out may be the same memory as in (same type and leading dimension); otherwise an out must
  * overlap no other buffer of the group. */
 typedef struct psgd_ns_matrix {

@@ -101,19 +101,27 @@ template <int T> struct Tile {
 // says that stage j + 1 has landed for every wave and that every wave has read stage j out of the
 // buffer that stage j + 4 is then loaded into. Accurate products take the hi and the lo plane of
 // 32 k as two stages: hi hi in the first, lo hi + hi lo in the second.
-template <int ST, int T, bool ACC, int OT>
-__global__ __launch_bounds__(Tile<T>::THREADS, 2)
-void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, int step, NsArgs na)
+//
+// Split items. A tile whose K is cut into wi.b & 63 parts leaves part wi.a & 63 as raw fp32
+// accumulators in slot wi.c of `partial`; the launch with REDUCE adds a tile's slots wi.c, wi.c + 1,
+// ... in order and runs the epilogue, each wave of
+// the tile as a workgroup of its own.
+template <int ST, int T, bool ACC, int OT, bool REDUCE>
+__global__ __launch_bounds__(REDUCE ? kWave : Tile<T>::THREADS, 2)
+void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, float* __restrict__ partial, int step,
+               NsArgs na)
 {
   if (na.skip && *na.skip != 0) return;
-  const Work wi = work[xcd_remap(blockIdx.x, gridDim.x)];
+  using TL = Tile<T>;
+  constexpr int PER = REDUCE ? TL::WAVES : 1;  // workgroups per item: the sums' waves are on their own
+  const int item = xcd_remap(blockIdx.x, gridDim.x);
+  const Work wi = work[item / PER];
   if (wi.mat < 0) return;
   const NsMat& d = mats[wi.mat];
-  using TL = Tile<T>;
   constexpr bool OUTER = ST == NS_UPDATE;      // P is read K-outer
   const int cur = step & 1;
-  const int i0 = wi.a, j0 = wi.b;
-  const int lane = threadIdx.x & (kWave - 1), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int i0 = wi.a & ~63, j0 = wi.b & ~63, split = wi.a & 63, splits = wi.b & 63;
+  const int lane = threadIdx.x & (kWave - 1), wv = REDUCE ? item % PER : __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wv & 1, wn = wv >> 1;
   const int wi0 = wm * (T / 2), wj0 = wn * (T / TL::WN);
   const int c = lane & 15, g = lane >> 4;
@@ -129,17 +137,24 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, in
     qh = gbl(d.bh); ql = gbl(d.bl); ldq = d.sp; K = d.s;
   }
   // whole pairs of 32 k (the padding up to a tile holds zeros); accurate: two stages per 32 k
-  const int nst = 2 * ((K + 63) / 64) * (ACC ? 2 : 1);
+  int nst = ns_stages(K, ACC);
+  int k0 = 0;                                  // first k of this part
+  if (splits > 1) {
+    const int per = ns_part(nst, splits, ACC), first = split * per;
+    nst = min(per, nst - first);
+    k0 = first * (ACC ? KB / 2 : KB);
+  }
 
-  __shared__ __attribute__((aligned(16))) uint16_t lds[RING][TL::BYTES];     // P, then Q
+  __shared__ __attribute__((aligned(16))) uint16_t lds[RING][TL::BYTES / PER];   // P, then Q
   const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS uint16_t*)&lds[0][0];
   // this wave's loads of a stage: load x < PL is 1 KB of P, the others of Q
   constexpr int PL = TL::LOADS / 2;
   uint32_t poff[PL], qoff[PL];
-  const GLOBAL uint16_t* const pbase_h = OUTER ? ph + i0 : ph + (int64_t)i0 * ldp;
-  const GLOBAL uint16_t* const qbase_h = qh + (int64_t)j0 * ldq;
-  const GLOBAL uint16_t* const pbase_l = OUTER ? pl + i0 : pl + (int64_t)i0 * ldp;
-  const GLOBAL uint16_t* const qbase_l = ql + (int64_t)j0 * ldq;
+  const int64_t pfirst = OUTER ? (int64_t)k0 * ldp + i0 : (int64_t)i0 * ldp + k0, qfirst = (int64_t)j0 * ldq + k0;
+  const GLOBAL uint16_t* const pbase_h = ph + pfirst;
+  const GLOBAL uint16_t* const qbase_h = qh + qfirst;
+  const GLOBAL uint16_t* const pbase_l = pl + pfirst;
+  const GLOBAL uint16_t* const qbase_l = ql + qfirst;
 #pragma unroll
   for (int x = 0; x < PL; ++x) {
     const int e = (wv * PL + x) * kWave + lane;              // 16-byte slot of the operand's stage
@@ -198,6 +213,21 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, in
     }
   };
   auto none = [](int) {};
+  // stage j's fragments over the first half of the rows, so that the last of them is answered before
+  // the wait; the stage loads over the second half
+  constexpr int HALF = TL::TA / 2;
+  auto read_some = [&](Frag& f, int j, int a) {
+    if (a >= HALF) return;
+#pragma unroll
+    for (int b = a * TL::TB / HALF; b < (a + 1) * TL::TB / HALF; ++b) read_q(f, j, b);
+    read_p(f, j, 2 * a);
+    read_p(f, j, 2 * a + 1);
+  };
+  auto send_some = [&](int j, int a) {
+    if (a < HALF) return;
+#pragma unroll
+    for (int x = (a - HALF) * TL::LOADS / HALF; x < (a - HALF + 1) * TL::LOADS / HALF; ++x) load_part(j, x);
+  };
   // Before stage j is multiplied: stage j + 1 has landed (BEHIND later stages may still be under
   // way) and nobody reads stage j's buffer any more.
   auto turn = [&](auto behind) {
@@ -212,20 +242,18 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, in
     constexpr bool SEND = decltype(send)::value, MORE = decltype(more)::value;
     turn(behind0);
     mul(f0, f0, [&](int a) {
-      if (a < TL::TB) read_q(f1, j + 1, a);
-      read_p(f1, j + 1, a);
-      if (SEND && a < TL::LOADS) load_part(j + RING, a);
+      read_some(f1, j + 1, a);
+      if (SEND) send_some(j + RING, a);
     }, none);
     if constexpr (MORE) turn(behind1);
     if constexpr (ACC) {
-      mul(f1, f0, [&](int a) { if (SEND && a < TL::LOADS) load_part(j + 1 + RING, a); }, none);
+      mul(f1, f0, [&](int a) { if (SEND) send_some(j + 1 + RING, a); }, none);
       // f0.q is free from here on, and each f0.p[a] behind its last row
       mul(f0, f1, [&](int a) { if (MORE && a < TL::TB) read_q(f0, j + 2, a); }, [&](int a) { if (MORE) read_p(f0, j + 2, a); });
     } else {
       mul(f1, f1, [&](int a) {
-        if (MORE && a < TL::TB) read_q(f0, j + 2, a);
-        if (MORE) read_p(f0, j + 2, a);
-        if (SEND && a < TL::LOADS) load_part(j + 1 + RING, a);
+        if (MORE) read_some(f0, j + 2, a);
+        if (SEND) send_some(j + 1 + RING, a);
       }, none);
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -240,24 +268,98 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, in
     for (int x = 0; x < TL::LOADS; ++x) load_part(j, x);
   };
 
-  load_stage(0);
-  load_stage(1);
-  if (nst > 2) {                               // nst is even
-    load_stage(2);
-    load_stage(3);
-    wait_loads<3 * TL::LOADS>();
+  if constexpr (REDUCE) {
+    const GLOBAL f32x4* s = gcast<f32x4>(gbl(partial)) + (int64_t)wi.c * (T * T / 4) + wv * (TL::TA * TL::TB * kWave) + lane;
+    for (int x = 0; x < splits; ++x, s += T * T / 4)
+#pragma unroll
+      for (int a = 0; a < TL::TA; ++a)
+#pragma unroll
+        for (int b = 0; b < TL::TB; ++b) acc[a][b] += s[(a * TL::TB + b) * kWave];
+  } else if constexpr (T == 256) {
+    static_assert(!ACC, "128-wide tiles at most: both halves' fragments beside 128 accumulators do not fit");
+    // Two waves per SIMD take turns: while waves 0..3 multiply, waves 4..7 read their fragments and
+    // send for loads, and the other way round, a barrier between the phases. Each phase's MFMAs
+    // find their operands in registers, so the matrix pipe of every SIMD passes from one wave to the
+    // other without a gap to fill. Stage j is read in one phase by each half; after both, its
+    // buffer is free: stage j + 3 is sent for while stage j is read.
+    const bool second = wv >= TL::WAVES / 2;
+    auto read_all = [&](Frag& f, int j) {
+#pragma unroll
+      for (int b = 0; b < TL::TB; ++b) read_q(f, j, b);
+#pragma unroll
+      for (int a = 0; a < TL::TA; ++a) read_p(f, j, a);
+    };
+    auto none1 = [](int) {};
+    auto phase_read = [&](Frag& f, int j, auto behind, auto send) {
+      read_all(f, j);
+      if constexpr (decltype(send)::value) load_stage(j + RING - 1);
+      wait_loads<decltype(behind)::value * TL::LOADS>();
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto phase_end = [&] {
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto two = [&](int j, auto behind0, auto behind1, auto send0, auto send1) {   // stages j (even), j + 1
+      phase_read(f0, j, behind0, send0);
+      mul(f0, f0, none1, none1);
+      phase_end();
+      phase_read(f0, j + 1, behind1, send1);
+      mul(f0, f0, none1, none1);
+      phase_end();
+    };
+    load_stage(0);
+    load_stage(1);
+    if (nst > 2) {
+      load_stage(2);
+      wait_loads<2 * TL::LOADS>();
+    } else {
+      wait_loads<TL::LOADS>();
+    }
+    __builtin_amdgcn_s_barrier();
+    if (second) __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    int j = 0;
+    for (; j + 4 < nst; j += 2) two(j, N2{}, N2{}, Yes{}, Yes{});
+    if (nst > 2) {                             // four stages left, the last of them to be sent for
+      two(j, N2{}, N1{}, Yes{}, No{});
+      j += 2;
+    }
+    two(j, N0{}, N0{}, No{}, No{});
+    if (!second) __builtin_amdgcn_s_barrier();
   } else {
-    wait_loads<TL::LOADS>();
+    load_stage(0);
+    load_stage(1);
+    if (nst > 2) {                               // nst is even
+      load_stage(2);
+      load_stage(3);
+      wait_loads<3 * TL::LOADS>();
+    } else {
+      wait_loads<TL::LOADS>();
+    }
+    __builtin_amdgcn_s_barrier();
+#pragma unroll
+    for (int b = 0; b < TL::TB; ++b) read_q(f0, 0, b);
+#pragma unroll
+    for (int a = 0; a < TL::TA; ++a) read_p(f0, 0, a);
+    int j = 0;
+    for (; j + RING < nst; j += 2) pair(j, N2{}, N2{}, Yes{}, Yes{});
+    if (nst > 2) { pair(j, N2{}, N1{}, No{}, Yes{}); j += 2; }
+    pair(j, N0{}, N0{}, No{}, No{});
   }
-  __builtin_amdgcn_s_barrier();
+
+  if constexpr (!REDUCE && ST != NS_UPDATE) {
+    if (splits > 1) {
+      GLOBAL f32x4* s = gcast<f32x4>(gbl(partial)) + (int64_t)wi.c * (T * T / 4) + wv * (TL::TA * TL::TB * kWave) + lane;
 #pragma unroll
-  for (int b = 0; b < TL::TB; ++b) read_q(f0, 0, b);
+      for (int a = 0; a < TL::TA; ++a)
 #pragma unroll
-  for (int a = 0; a < TL::TA; ++a) read_p(f0, 0, a);
-  int j = 0;
-  for (; j + RING < nst; j += 2) pair(j, N2{}, N2{}, Yes{}, Yes{});
-  if (nst > 2) { pair(j, N2{}, N1{}, No{}, Yes{}); j += 2; }
-  pair(j, N0{}, N0{}, No{}, No{});
+        for (int b = 0; b < TL::TB; ++b) s[(a * TL::TB + b) * kWave] = acc[a][b];
+      return;
+    }
+  }
 
   // ---- epilogue --------------------------------------------------------------------------
   // Through this wave's own part of the ring, so that memory sees whole rows, 16 bytes a lane: a
@@ -265,8 +367,9 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, in
   // the bandwidth). 16-byte units are XOR-ed by their row, which keeps both sides conflict-free.
   constexpr int WI = T / 2, WJ = T / TL::WN;                 // the wave's tile of C
   __syncthreads();                                           // the ring is read out
-  uint16_t* const reg = &lds[0][0] + wv * (WI * WJ);
-  const uint32_t reg0 = lds0 + wv * (WI * WJ * 2);
+  const int part = REDUCE ? 0 : wv * (WI * WJ);
+  uint16_t* const reg = &lds[0][0] + part;
+  const uint32_t reg0 = lds0 + 2 * part;
   const int ib = i0 + wi0, jb = j0 + wj0;
 
   // rows j of WI values: a lane's four are half a unit
@@ -379,12 +482,15 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, in
       fetch(gbl(d.xh[cur]), d.lp);
       add(na.a);
     }
-    fetch(gbl(d.xl[cur]), d.lp);
-    add(na.a);
+    // The fast form needs no lo in the last step: nothing multiplies that rounding again.
+    if constexpr (ACC || OT == 0) {
+      fetch(gbl(d.xl[cur]), d.lp);
+      add(na.a);
+    }
     if constexpr (OT == 0) {
       mask(d.l);
       flush_ji(gbl(d.xh[cur ^ 1]), d.lp, false);
-      flush_ji(gbl(d.xl[cur ^ 1]), d.lp, true);
+      if (ACC || step + 2 < na.steps) flush_ji(gbl(d.xl[cur ^ 1]), d.lp, true);
     } else {
       // half of the wave's i at a time, as fp32 rows of the output (rows i when X is transposed)
       constexpr int HI = WI / 2;
@@ -441,35 +547,37 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, in
   }
 }
 
-template <int ST, int T, bool ACC, int OT>
-void go(const NsMat* mats, const Work* work, int n_work, int step, const NsArgs& a, hipStream_t s) {
-  k_ns_gemm<ST, T, ACC, OT><<<dim3(n_work), dim3(Tile<T>::THREADS), 0, s>>>(mats, work, step, a);
+template <int ST, int T, bool ACC, int OT, bool REDUCE = false>
+void go(const NsList& l, const NsMat* mats, int step, const NsArgs& a, hipStream_t s) {
+  k_ns_gemm<ST, T, ACC, OT, REDUCE><<<dim3(REDUCE ? l.n_reduce * Tile<T>::WAVES : l.n_work), dim3(REDUCE ? kWave : Tile<T>::THREADS), 0, s>>>(
+      mats, REDUCE ? l.reduce : l.work, l.partial, step, a);
+}
+template <int ST, int T, bool ACC>
+void go_split(const NsList& l, const NsMat* mats, int step, const NsArgs& a, hipStream_t s) {
+  go<ST, T, ACC, 0>(l, mats, step, a, s);
+  if (l.n_reduce > 0) go<ST, T, ACC, 0, true>(l, mats, step, a, s);
 }
 template <int T, bool ACC>
-hipError_t pick(NsStage st, int ot, bool last, const NsMat* mats, const Work* work, int n_work, int step,
-                const NsArgs& a, hipStream_t s) {
-  if (st == NS_GRAM) go<NS_GRAM, T, ACC, 0>(mats, work, n_work, step, a, s);
-  else if (st == NS_POLY) go<NS_POLY, T, ACC, 0>(mats, work, n_work, step, a, s);
-  else if (!last) go<NS_UPDATE, T, ACC, 0>(mats, work, n_work, step, a, s);
-  else if (ot == G_F32) go<NS_UPDATE, T, ACC, G_F32>(mats, work, n_work, step, a, s);
-  else if (ot == G_F16) go<NS_UPDATE, T, ACC, G_F16>(mats, work, n_work, step, a, s);
-  else if (ot == G_BF16) go<NS_UPDATE, T, ACC, G_BF16>(mats, work, n_work, step, a, s);
+hipError_t pick(NsStage st, int ot, bool last, const NsList& l, const NsMat* mats, int step, const NsArgs& a, hipStream_t s) {
+  if (st == NS_GRAM) go_split<NS_GRAM, T, ACC>(l, mats, step, a, s);
+  else if (st == NS_POLY) go_split<NS_POLY, T, ACC>(l, mats, step, a, s);
+  else if (!last) go<NS_UPDATE, T, ACC, 0>(l, mats, step, a, s);
+  else if (ot == G_F32) go<NS_UPDATE, T, ACC, G_F32>(l, mats, step, a, s);
+  else if (ot == G_F16) go<NS_UPDATE, T, ACC, G_F16>(l, mats, step, a, s);
+  else if (ot == G_BF16) go<NS_UPDATE, T, ACC, G_BF16>(l, mats, step, a, s);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_ns_gemm(NsStage st, int tile, bool accurate, int ot, bool last, const NsMat* mats,
-                          const Work* work, int n_work, int step, const NsArgs& a, hipStream_t s) {
-  if (tile == 256)
-    return accurate ? pick<256, true>(st, ot, last, mats, work, n_work, step, a, s)
-                    : pick<256, false>(st, ot, last, mats, work, n_work, step, a, s);
-  if (tile == 128)
-    return accurate ? pick<128, true>(st, ot, last, mats, work, n_work, step, a, s)
-                    : pick<128, false>(st, ot, last, mats, work, n_work, step, a, s);
-  return accurate ? pick<64, true>(st, ot, last, mats, work, n_work, step, a, s)
-                  : pick<64, false>(st, ot, last, mats, work, n_work, step, a, s);
+hipError_t launch_ns_gemm(NsStage st, bool accurate, int ot, bool last, const NsList& l, const NsMat* mats, int step,
+                          const NsArgs& a, hipStream_t s) {
+  if (l.tile == 256)
+    return accurate ? hipErrorInvalidValue : pick<256, false>(st, ot, last, l, mats, step, a, s);
+  if (l.tile == 128)
+    return accurate ? pick<128, true>(st, ot, last, l, mats, step, a, s) : pick<128, false>(st, ot, last, l, mats, step, a, s);
+  return accurate ? pick<64, true>(st, ot, last, l, mats, step, a, s) : pick<64, false>(st, ot, last, l, mats, step, a, s);
 }
 
 }  // namespace psgd

@@ -50,9 +50,25 @@ enum NsStage : int { NS_GRAM = 0, NS_POLY = 1, NS_UPDATE = 2 };
 
 hipError_t launch_ns_norm(int it, const NsMat* mats, const Work* work, int n_work, const NsArgs& a, hipStream_t s);
 hipError_t launch_ns_x0(int it, const NsMat* mats, const Work* work, int n_work, const NsArgs& a, hipStream_t s);
-// One product stage of step `step` (0-based) over a tile list; `last` writes the caller's output.
-hipError_t launch_ns_gemm(NsStage st, int tile, bool accurate, int ot, bool last, const NsMat* mats,
-                          const Work* work, int n_work, int step, const NsArgs& a, hipStream_t s);
+// One product stage's tiles: (matrix, first row, first column, partial slot), padded for
+// xcd_remap. Tiles are multiples of 64 wide, so the low 6 bits of the row and the column carry the
+// part of a tile whose K is split and the number of parts (0: not split).
+struct NsList {
+  int tile = 0;
+  const Work* work = nullptr;   int n_work = 0;
+  const Work* reduce = nullptr; int n_reduce = 0;    // the split tiles, with their first slot
+  float* partial = nullptr;                          // tile * tile floats per slot
+};
+// Stages of 32 k a product over K takes (accurate: the hi and the lo plane each), always even, and
+// the stages of one of `splits` parts (whole k and an even number).
+__host__ __device__ inline int ns_stages(int K, bool accurate) { return 2 * ((K + 63) / 64) * (accurate ? 2 : 1); }
+__host__ __device__ inline int ns_part(int stages, int splits, bool accurate) {
+  const int unit = accurate ? 4 : 2;
+  return ((stages + splits - 1) / splits + unit - 1) / unit * unit;
+}
+// One product stage of step `step` (0-based); `last` writes the caller's output.
+hipError_t launch_ns_gemm(NsStage st, bool accurate, int ot, bool last, const NsList& l, const NsMat* mats, int step,
+                          const NsArgs& a, hipStream_t s);
 
 // A group of matrices orthogonalised together: validated by the caller, laid out and allocated
 // here. One instance serves one call at a time.
@@ -73,8 +89,9 @@ class NsGroup {
   size_t bytes_ = 0;
   NsMat* d_mats_[2] = {nullptr, nullptr};
   Work* d_work_ = nullptr;
-  List norm_, x0_, gram_, poly_, update_;
-  int it_ = 0, ot_ = 0, tile_ = 128;
+  List norm_, x0_;
+  NsList gram_, poly_, update_;
+  int it_ = 0, ot_ = 0;
   bool accurate_ = false;
 };
 

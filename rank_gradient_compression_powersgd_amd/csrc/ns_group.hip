@@ -2,7 +2,8 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
-#include <cstdlib>
+#include <functional>
+#include <queue>
 
 #include "ns.h"
 
@@ -13,38 +14,161 @@ namespace {
 
 inline int64_t rup(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
-// Spread a tile list over the XCDs (xcd_remap: XCD x walks the x-th eighth of the list). Groups
-// of `gsize` consecutive items share an operand panel and stay on one XCD, longest group first
-// to the XCD with the least work so far; short lists are dealt out item by item, since a shared
-// panel is worth less than an idle XCD.
-void balance(std::vector<Work>& w, std::vector<int64_t>& cost, const std::vector<int>& group) {
-  const int n = (int)w.size();
-  const bool single = n <= 512;
-  struct G { int beg, end; int64_t c; };
-  std::vector<G> gs;
-  for (int i = 0; i < n;) {
-    int j = i;
-    int64_t c = 0;
-    while (j < n && (single ? j == i : group[j] == group[i])) c += cost[j++];
-    gs.push_back({i, j, c});
-    i = j;
+constexpr int kCus = 256;
+
+// One candidate item of a tile list.
+struct Item {
+  Work w;
+  double cost;                           // microseconds on a CU of its own
+};
+
+// Cost model of a product list, in microseconds, from runs of lists of one tile width.
+//   stage   one stage of 32 k of a tile that has its CU to itself
+//   full    the same on a full chip, which runs at its power limit
+//   fixed, fixed_update  what a tile costs beside its stages (the update reads and writes X)
+// 256-wide tiles do 1.9 times the work per microsecond of 128-wide ones and three times that of
+// 64-wide ones once the CUs are full; below that the narrow ones finish first (an update of 496 x
+// 3968: 8 us in 64-wide tiles, 14 in 128-wide ones, 26 in 256-wide ones; four resblocks: 794, 499 and
+// 391 us). Accurate products (two stages per 32 k, three products for two stages' loads) run at the
+// MFMA's pace from 128-wide tiles on; 256-wide ones would not hold both halves in registers.
+struct TileCost { int tile; double stage, full, fixed, fixed_update; };
+constexpr TileCost kFast[] = {{64, 0.14, 0.16, 1.5, 2.5}, {128, 0.29, 0.36, 2.5, 7.0}, {256, 0.75, 0.85, 7.0, 15.0}};
+constexpr TileCost kAccurate[] = {{64, 0.17, 0.19, 1.5, 3.0}, {128, 0.33, 0.37, 2.5, 8.0}};
+constexpr double kLaunch = 4.0;              // a second, dependent launch
+constexpr double kMemory = 4.0e6;            // bytes per microsecond of partial sums
+
+// Time of a list whose items go, longest first, to the CU with the least work.
+double makespan(std::vector<double> cost) {
+  std::sort(cost.begin(), cost.end(), std::greater<double>());
+  std::vector<double> start(kCus, 0.0);
+  std::priority_queue<double, std::vector<double>, std::greater<double>> cus(std::greater<double>(), std::move(start));
+  double last = 0.0;
+  for (double c : cost) {
+    const double t = cus.top() + c;
+    cus.pop();
+    cus.push(t);
+    last = std::max(last, t);
   }
-  std::stable_sort(gs.begin(), gs.end(), [](const G& a, const G& b) { return a.c > b.c; });
+  return last;
+}
+
+// The list in the order xcd_remap deals it out: XCD x walks the x-th eighth, padded to the longest.
+// Items of one cost are dealt to the XCDs in contiguous runs, since neighbours share operand rows in
+// an XCD's L2, as many to each as evens out the XCDs' work; longer items come first. (Four
+// resblocks' A: runs 192 us, item by item to the first free CU 222 us, where half of the XCDs had
+// all of the second round.)
+std::vector<Work> spread(const std::vector<Item>& items) {
+  std::vector<int> idx(items.size());
+  for (size_t i = 0; i < idx.size(); ++i) idx[i] = (int)i;
+  std::stable_sort(idx.begin(), idx.end(), [&](int a, int b) { return items[a].cost > items[b].cost; });
   std::vector<std::vector<Work>> seg(kXcds);
-  int64_t load[kXcds] = {};
-  for (const G& g : gs) {
-    int x = 0;
-    for (int y = 1; y < kXcds; ++y) if (load[y] < load[x]) x = y;
-    load[x] += g.c;
-    for (int i = g.beg; i < g.end; ++i) seg[x].push_back(w[i]);
+  double load[kXcds] = {};
+  for (size_t beg = 0; beg < idx.size();) {
+    size_t end = beg;
+    while (end < idx.size() && items[idx[end]].cost == items[idx[beg]].cost) ++end;
+    int quota[kXcds] = {};
+    for (size_t i = beg; i < end; ++i) {
+      int x = 0;
+      for (int y = 1; y < kXcds; ++y) if (load[y] < load[x]) x = y;
+      load[x] += items[idx[i]].cost;
+      ++quota[x];
+    }
+    for (int x = 0; x < kXcds; ++x)
+      for (int k = 0; k < quota[x]; ++k) seg[x].push_back(items[idx[beg++]].w);
   }
   size_t per = 0;
   for (const auto& s : seg) per = std::max(per, s.size());
-  w.clear();
+  std::vector<Work> out;
   for (auto& s : seg) {
     s.resize(per, Work{-1, 0, 0, 0});
-    w.insert(w.end(), s.begin(), s.end());
+    out.insert(out.end(), s.begin(), s.end());
   }
+  return out;
+}
+
+struct Planned {
+  int tile = 0;
+  std::vector<Work> work, reduce;
+  int64_t slots = 0;
+  double time = 0.0;
+};
+
+// The tiles of one product stage, `tile` wide, in an order in which neighbours share operands:
+// blocks of up to 8 x 8 tiles of the lower triangle (A and B), or the row tiles over one column panel
+// of X (the update).
+std::vector<Work> tiles_of(const std::vector<NsMat>& mats, NsStage st, int tile) {
+  std::vector<Work> w;
+  for (int i = 0; i < (int)mats.size(); ++i) {
+    const int ns = (mats[i].s + tile - 1) / tile, nl = (mats[i].l + tile - 1) / tile;
+    if (st == NS_UPDATE) {
+      for (int a = 0; a < nl; ++a)
+        for (int b = 0; b < ns; ++b) w.push_back(Work{i, a * tile, b * tile, -1});
+      continue;
+    }
+    const int side = ns <= 8 ? ns : 4;
+    for (int a0 = 0; a0 < ns; a0 += side)
+      for (int b0 = 0; b0 <= a0; b0 += side)
+        for (int a = a0; a < std::min(ns, a0 + side); ++a)
+          for (int b = b0; b < std::min(a + 1, b0 + side); ++b) w.push_back(Work{i, a * tile, b * tile, -1});
+  }
+  return w;
+}
+
+// Choose the tile width and the split of K that the cost model expects to finish first. Splitting
+// gives a list of few long tiles (A is s x s over K = l) enough items to fill the CUs, or evens out
+// a last round that would fill part of them; it costs the partial sums' way through memory and a
+// second launch.
+Planned plan_list(const std::vector<NsMat>& mats, NsStage st, bool accurate) {
+  Planned best;
+  const int kinds = accurate ? 2 : 3;
+  for (int kind = 0; kind < kinds; ++kind) {
+    const TileCost& tc = accurate ? kAccurate[kind] : kFast[kind];
+    const std::vector<Work> w = tiles_of(mats, st, tc.tile);
+    const int n = (int)w.size();
+    if (kind + 1 < kinds && n > 64 * kCus) continue;        // far past what narrow tiles are for
+    const double fixed = st == NS_UPDATE ? tc.fixed_update : tc.fixed;
+    const double tile_bytes = 4.0 * tc.tile * tc.tile;
+    auto stages = [&](const Work& x) { return ns_stages(st == NS_GRAM ? mats[x.mat].l : mats[x.mat].s, accurate); };
+    double total = 0.0;
+    for (const Work& x : w) total += stages(x);
+    // tiles of more than `limit` stages are split, but for the first `whole` of the list
+    auto consider = [&](double limit, int whole) {
+      std::vector<Item> items;
+      std::vector<Work> reduce;
+      std::vector<double> cost;
+      int64_t slots = 0;
+      for (int i = 0; i < n; ++i) {
+        const int ks = stages(w[i]), want = i < whole ? 1 : (int)std::min(16.0, std::ceil(ks / limit));
+        const int per = ns_part(ks, want, accurate), parts = (ks + per - 1) / per;
+        if (parts <= 1) {
+          items.push_back({w[i], ks * tc.stage + fixed});
+        } else {
+          reduce.push_back(Work{w[i].mat, w[i].a, w[i].b | parts, (int)slots});
+          for (int p = 0; p < parts; ++p, ++slots)
+            items.push_back({Work{w[i].mat, w[i].a | p, w[i].b | parts, (int)slots}, std::min(per, ks - p * per) * tc.stage + fixed});
+        }
+      }
+      for (const Item& x : items) cost.push_back(x.cost);
+      double time = std::max(makespan(cost), total * tc.full / kCus);
+      if (slots) time += kLaunch + (2.0 * slots + reduce.size()) * tile_bytes / kMemory;
+      // a split has to promise a twentieth: the model is no better than that
+      if (best.tile && time >= (slots ? 0.95 : 1.0) * best.time) return;
+      best.tile = tc.tile;
+      best.time = time;
+      best.slots = slots;
+      best.work = spread(items);
+      best.reduce = reduce;
+      while (best.reduce.size() % kXcds) best.reduce.push_back(Work{-1, 0, 0, 0});
+    };
+    consider(1.0, n);
+    if (st == NS_UPDATE || n > 8 * kCus) continue;
+    for (double share : {1.0, 0.75, 0.5, 0.34, 0.25}) {      // of a CU's share of the list
+      const double limit = std::max(4.0, share * total / kCus);
+      consider(limit, 0);
+      if (n > kCus) consider(limit, n / kCus * kCus);
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -56,14 +180,6 @@ hipError_t NsGroup::create(const std::vector<Item>& items, int in_type, int out_
   ot_ = out_type;
   accurate_ = accurate;
   const int n = (int)items.size();
-  // 128-wide tiles reuse each staged value twice as often; 64-wide ones fill the chip when the
-  // group is small
-  int64_t tiles = 0;
-  for (const Item& t : items)
-    tiles += (rup(std::min(t.m, t.n), 128) / 128) * (rup(std::max(t.m, t.n), 128) / 128);
-  tile_ = tiles >= 256 ? 128 : 64;
-  if (getenv("NS_TILE")) tile_ = atoi(getenv("NS_TILE"));
-
   std::vector<NsMat> mats(n);
   struct Off { size_t xh[2], xl[2], ah, al, bh, bl, partial; };
   std::vector<Off> offs(n);
@@ -77,10 +193,18 @@ hipError_t NsGroup::create(const std::vector<Item>& items, int in_type, int out_
     d.m = (int)t.m; d.n = (int)t.n;
     d.flip = t.m > t.n;
     d.s = std::min(d.m, d.n); d.l = std::max(d.m, d.n);
-    d.sp = (int)rup(d.s, tile_); d.lp = (int)rup(d.l, tile_);
     // parts of at least 8192 elements, at most 1024 of them (every X0 workgroup adds them up)
     d.part_rows = (int)std::max<int64_t>((8192 + t.n - 1) / t.n, (t.m + 1023) / 1024);
     d.parts = (d.m + d.part_rows - 1) / d.part_rows;
+  }
+  const Planned plan[3] = {plan_list(mats, NS_GRAM, accurate), plan_list(mats, NS_POLY, accurate),
+                           plan_list(mats, NS_UPDATE, accurate)};
+  const int square = std::max(plan[0].tile, plan[1].tile), pad_s = std::max(square, plan[2].tile);
+  const int64_t slots = std::max(plan[0].slots * plan[0].tile * plan[0].tile, plan[1].slots * plan[1].tile * plan[1].tile);
+  for (int i = 0; i < n; ++i) {
+    NsMat& d = mats[i];
+    d.sp = (int)rup(d.s, pad_s);
+    d.lp = (int)rup(d.l, plan[2].tile);
     const size_t x = (size_t)d.sp * d.lp * 2, a = (size_t)d.sp * d.sp * 2;
     Off& o = offs[i];
     for (int k = 0; k < 2; ++k) { o.xh[k] = take(x); o.xl[k] = take(x); }
@@ -90,6 +214,7 @@ hipError_t NsGroup::create(const std::vector<Item>& items, int in_type, int out_
     o.bl = accurate ? take(a) : 0;
     o.partial = take((size_t)d.parts * 8);
   }
+  const size_t slots_off = take((size_t)slots * 4);
 
   std::vector<Work> all;
   auto add = [&](List& l, const std::vector<Work>& w) {
@@ -98,41 +223,20 @@ hipError_t NsGroup::create(const std::vector<Item>& items, int in_type, int out_
     all.insert(all.end(), w.begin(), w.end());
   };
   std::vector<Work> w;
-  std::vector<int64_t> cost;
-  std::vector<int> group;
-  auto clear = [&] { w.clear(); cost.clear(); group.clear(); };
   for (int i = 0; i < n; ++i)
     for (int p = 0; p < mats[i].parts; ++p) w.push_back(Work{i, p * mats[i].part_rows, p, 0});
   add(norm_, w);
-  clear();
+  w.clear();
   const int xt = ns_x0_tile();
   for (int i = 0; i < n; ++i)
     for (int a = 0; a < mats[i].sp; a += xt)
       for (int b = 0; b < mats[i].lp; b += xt) w.push_back(Work{i, a, b, 0});
   add(x0_, w);
-  int gid = 0;
-  for (int st = 0; st < 2; ++st) {         // A, then B: tiles on and below the diagonal
-    clear();
-    for (int i = 0; i < n; ++i)
-      for (int a = 0; a < mats[i].sp; a += tile_, ++gid)
-        for (int b = 0; b <= a; b += tile_) {
-          w.push_back(Work{i, a, b, 0});
-          cost.push_back(st == 0 ? mats[i].l : mats[i].s);
-          group.push_back(gid);
-        }
-    balance(w, cost, group);
-    add(st == 0 ? gram_ : poly_, w);
+  List lists[3], reduces[3];
+  for (int k = 0; k < 3; ++k) {
+    add(lists[k], plan[k].work);
+    add(reduces[k], plan[k].reduce);
   }
-  clear();
-  for (int i = 0; i < n; ++i)              // X: the row tiles over one column panel share it
-    for (int a = 0; a < mats[i].lp; a += tile_, ++gid)
-      for (int b = 0; b < mats[i].sp; b += tile_) {
-        w.push_back(Work{i, a, b, 0});
-        cost.push_back(mats[i].s);
-        group.push_back(gid);
-      }
-  balance(w, cost, group);
-  add(update_, w);
 
   const size_t mat_bytes = (sizeof(NsMat) * n + 255) / 256 * 256;
   const size_t work_off = ws + 2 * mat_bytes;
@@ -141,6 +245,15 @@ hipError_t NsGroup::create(const std::vector<Item>& items, int in_type, int out_
   if (e != hipSuccess) { buf_ = nullptr; return hipErrorOutOfMemory; }
   char* base = static_cast<char*>(buf_);
   d_work_ = reinterpret_cast<Work*>(base + work_off);
+  NsList* const out[3] = {&gram_, &poly_, &update_};
+  for (int k = 0; k < 3; ++k) {
+    out[k]->tile = plan[k].tile;
+    out[k]->work = d_work_ + lists[k].off;
+    out[k]->n_work = lists[k].cnt;
+    out[k]->reduce = d_work_ + reduces[k].off;
+    out[k]->n_reduce = reduces[k].cnt;
+    out[k]->partial = reinterpret_cast<float*>(base + slots_off);
+  }
   for (int adj = 0; adj < 2; ++adj) {
     d_mats_[adj] = reinterpret_cast<NsMat*>(base + ws + adj * mat_bytes);
     for (int i = 0; i < n; ++i) {
@@ -170,9 +283,9 @@ hipError_t NsGroup::run(const NsArgs& a, int adjust, hipStream_t s) {
   hipError_t e = launch_ns_norm(it_, dm, W(norm_), norm_.cnt, a, s);
   if (e == hipSuccess) e = launch_ns_x0(it_, dm, W(x0_), x0_.cnt, a, s);
   for (int k = 0; k < a.steps && e == hipSuccess; ++k) {
-    e = launch_ns_gemm(NS_GRAM, tile_, accurate_, ot_, false, dm, W(gram_), gram_.cnt, k, a, s);
-    if (e == hipSuccess) e = launch_ns_gemm(NS_POLY, tile_, accurate_, ot_, false, dm, W(poly_), poly_.cnt, k, a, s);
-    if (e == hipSuccess) e = launch_ns_gemm(NS_UPDATE, tile_, accurate_, ot_, k + 1 == a.steps, dm, W(update_), update_.cnt, k, a, s);
+    e = launch_ns_gemm(NS_GRAM, accurate_, ot_, false, gram_, dm, k, a, s);
+    if (e == hipSuccess) e = launch_ns_gemm(NS_POLY, accurate_, ot_, false, poly_, dm, k, a, s);
+    if (e == hipSuccess) e = launch_ns_gemm(NS_UPDATE, accurate_, ot_, k + 1 == a.steps, update_, dm, k, a, s);
   }
   return e;
 }

@@ -1041,6 +1041,8 @@ psgd_status psgd_adam_update(psgd_ctx* ctx, const psgd_adam_tensor* pass, int n_
 // ------------------------------------------------------------------------------------------
 namespace {
 
+constexpr int64_t kMaxNsDim = 1 << 22;   // rows of a tile are addressed by 32-bit byte offsets
+
 // Makes a context's device current for one call and gives the caller's back.
 struct DeviceGuard {
   int prev = -1;
@@ -1116,7 +1118,7 @@ psgd_status psgd_ns_plan_create(psgd_ctx* ctx, const psgd_ns_matrix* mats, int n
   for (int i = 0; i < n_mats; ++i) {
     const psgd_ns_matrix& a = mats[i];
     if (!a.in || !a.out) return fail(ctx, PSGD_EINVAL, "matrix %d: in and out are required", i);
-    if (a.m < 1 || a.n < 1 || a.m > (1 << 28) || a.n > (1 << 28))
+    if (a.m < 1 || a.n < 1 || a.m > kMaxNsDim || a.n > kMaxNsDim)
       return fail(ctx, PSGD_EINVAL, "matrix %d: bad shape %lld x %lld", i, (long long)a.m, (long long)a.n);
     if (a.ld_in < a.n || a.ld_out < a.n) return fail(ctx, PSGD_EINVAL, "matrix %d: leading dimensions must be >= n", i);
     if (!aligned_to(a.in, type_size(it)) || !aligned_to(a.out, type_size(ot)))
@@ -1168,6 +1170,8 @@ psgd_status psgd_muon_attach(psgd_ctx* ctx, psgd_plan* plan, const psgd_muon_mat
   for (int i = 0; i < plan->n_mats; ++i) {
     const DevMat& d = plan->mats[i];
     const psgd_muon_matrix& a = opt[i];
+    if (d.m > kMaxNsDim || d.n > kMaxNsDim)
+      return fail(ctx, PSGD_EINVAL, "matrix %d: %d x %d is too large for Newton-Schulz", i, d.m, d.n);
     if (!d.out) return fail(ctx, PSGD_EINVAL, "matrix %d: Muon reads the decompressed gradient, the matrix has no out buffer", i);
     if (!a.param || !a.momentum) return fail(ctx, PSGD_EINVAL, "matrix %d: param and momentum are required", i);
     if (a.ld_param < d.n) return fail(ctx, PSGD_EINVAL, "matrix %d: ld_param must be >= n", i);

@@ -114,7 +114,7 @@ def test_c_refusals():
     _raises(B.PSGD_EDTYPE, lambda: create([good], i=9))
     _raises(B.PSGD_EDTYPE, lambda: create([good], o=0))
     _raises(B.PSGD_EINVAL, lambda: create([good], p=2))
-    for change in (dict(m=0), dict(n=0), dict(ld_in=15), dict(ld_out=15), dict(out=None), dict(m=2 ** 28 + 1),
+    for change in (dict(m=0), dict(n=0), dict(ld_in=15), dict(ld_out=15), dict(out=None), dict(m=2 ** 22 + 1),
                    {"in": x.data_ptr() + 2}):
         bad = B.make_ns_matrix(x, x)
         for k, v in change.items():
