@@ -180,6 +180,20 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
 #pragma unroll
     for (int b = 0; b < TL::TB; ++b) acc[a][b] = f32x4{0, 0, 0, 0};
 
+  // hi lo + lo hi: on their own in 64-wide tiles, where the accumulators are few and K short, so that
+  // they are not cut to the size of hi hi
+  constexpr bool CROSS = ACC && T == 64;
+  f32x4 own[CROSS ? TL::TA : 1][CROSS ? TL::TB : 1];
+  f32x4 (&cross)[TL::TA][TL::TB] = [&]() -> f32x4 (&)[TL::TA][TL::TB] {
+    if constexpr (CROSS) return own; else return acc;
+  }();
+  if constexpr (CROSS) {
+#pragma unroll
+    for (int a = 0; a < TL::TA; ++a)
+#pragma unroll
+      for (int b = 0; b < TL::TB; ++b) own[a][b] = f32x4{0, 0, 0, 0};
+  }
+
   struct Frag { f16x8 p[TL::TA], q[TL::TB]; };
   auto read_p = [&](Frag& f, int j, int a) {
     const uint16_t* lp = lds[j % RING];
@@ -201,17 +215,18 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
   // One pass over the wave's MFMA tiles, row by row; `before(a)` is issued ahead of row a's MFMAs
   // and `after(a)` behind them, so that LDS reads and stage loads trickle in between MFMAs that do
   // not depend on them.
-  auto mul = [&](const Frag& fp, const Frag& fq, auto before, auto after) {
+  auto mul_to = [&](f32x4 (&to)[TL::TA][TL::TB], const Frag& fp, const Frag& fq, auto before, auto after) {
 #pragma unroll
     for (int a = 0; a < TL::TA; ++a) {
       before(a);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int b = 0; b < TL::TB; ++b) acc[a][b] = mfma_f16(fp.p[a], fq.q[b], acc[a][b]);
+      for (int b = 0; b < TL::TB; ++b) to[a][b] = mfma_f16(fp.p[a], fq.q[b], to[a][b]);
       __builtin_amdgcn_sched_barrier(0);
       after(a);
     }
   };
+  auto mul = [&](const Frag& fp, const Frag& fq, auto before, auto after) { mul_to(acc, fp, fq, before, after); };
   auto none = [](int) {};
   // stage j's fragments over the first half of the rows, so that the last of them is answered before
   // the wait; the stage loads over the second half
@@ -247,9 +262,9 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
     }, none);
     if constexpr (MORE) turn(behind1);
     if constexpr (ACC) {
-      mul(f1, f0, [&](int a) { if (SEND) send_some(j + 1 + RING, a); }, none);
+      mul_to(cross, f1, f0, [&](int a) { if (SEND) send_some(j + 1 + RING, a); }, none);
       // f0.q is free from here on, and each f0.p[a] behind its last row
-      mul(f0, f1, [&](int a) { if (MORE && a < TL::TB) read_q(f0, j + 2, a); }, [&](int a) { if (MORE) read_p(f0, j + 2, a); });
+      mul_to(cross, f0, f1, [&](int a) { if (MORE && a < TL::TB) read_q(f0, j + 2, a); }, [&](int a) { if (MORE) read_p(f0, j + 2, a); });
     } else {
       mul(f1, f1, [&](int a) {
         if (MORE) read_some(f0, j + 2, a);
@@ -345,9 +360,47 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
 #pragma unroll
     for (int a = 0; a < TL::TA; ++a) read_p(f0, 0, a);
     int j = 0;
-    for (; j + RING < nst; j += 2) pair(j, N2{}, N2{}, Yes{}, Yes{});
-    if (nst > 2) { pair(j, N2{}, N1{}, No{}, Yes{}); j += 2; }
-    pair(j, N0{}, N0{}, No{}, No{});
+    if constexpr (ACC) {
+      // An MFMA adds to its accumulator by truncation, so a long chain drifts by half a step an
+      // instruction: every 128 k the chain's sum moves to a rounded one (a product over 1474 k came
+      // out 3.4e-6 off instead of 0.9e-6).
+      f32x4 sum[TL::TA][TL::TB];
+#pragma unroll
+      for (int a = 0; a < TL::TA; ++a)
+#pragma unroll
+        for (int b = 0; b < TL::TB; ++b) sum[a][b] = f32x4{0, 0, 0, 0};
+      for (int n = 1; j + RING < nst; j += 2, ++n) {
+        pair(j, N2{}, N2{}, Yes{}, Yes{});
+        if ((n & 3) == 0) {
+#pragma unroll
+          for (int a = 0; a < TL::TA; ++a)
+#pragma unroll
+            for (int b = 0; b < TL::TB; ++b) {
+              sum[a][b] += acc[a][b];
+              acc[a][b] = f32x4{0, 0, 0, 0};
+            }
+        }
+      }
+      if (nst > 2) {
+        pair(j, N2{}, N1{}, No{}, Yes{});
+        j += 2;
+      }
+      pair(j, N0{}, N0{}, No{}, No{});
+#pragma unroll
+      for (int a = 0; a < TL::TA; ++a)
+#pragma unroll
+        for (int b = 0; b < TL::TB; ++b) {
+          acc[a][b] += sum[a][b];
+          if constexpr (CROSS) acc[a][b] += own[a][b];
+        }
+    } else {
+      for (; j + RING < nst; j += 2) pair(j, N2{}, N2{}, Yes{}, Yes{});
+      if (nst > 2) {
+        pair(j, N2{}, N1{}, No{}, Yes{});
+        j += 2;
+      }
+      pair(j, N0{}, N0{}, No{}, No{});
+    }
   }
 
   if constexpr (!REDUCE && ST != NS_UPDATE) {
