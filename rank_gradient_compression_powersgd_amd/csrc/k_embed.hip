@@ -88,26 +88,108 @@ void k_embed_lookup(EmbedLookup a)
 }
 
 // ---- the tokens sorted ---------------------------------------------------------------------
+// A stable sort by id in ranges of `range` ids: first the ranges in order, each with its tokens in
+// batch order (`list`), then each range by id (`sorted`, with the first place of every id in `seg`).
+// A token's place is its key's first place, plus the tokens of that key in earlier waves, plus
+// those before it in its own wave: stable, and free of atomics' order.
 constexpr int SO_THREADS = 1024, SO_WAVES = SO_THREADS / kWave, SO_UNROLL = 8;
 
-// One workgroup per range of `range` ids. Every workgroup reads all tokens (a few bytes each,
-// from L2): it counts those below its range, which is where its part of the sorted order
-// begins, so no workgroup waits for another and one launch sorts. Each wave keeps one contiguous
-// share of the batch; a token's place is its id's first place, plus the tokens of that id in
-// earlier waves, plus those before it in its own wave: stable, and free of atomics' order.
+__device__ __forceinline__ int prefix(uint64_t mask, int lane) { return __popcll(mask & ((1ull << lane) - 1)); }
+
+// lanes that hold the same key, among those of `has`
+template <int BITS> __device__ __forceinline__ uint64_t same_key(uint32_t key, bool has) {
+  uint64_t same = __builtin_amdgcn_ballot_w64(has);
+#pragma unroll
+  for (int bit = 0; bit < BITS; ++bit) {
+    const bool set = (key >> bit) & 1;
+    const uint64_t one = __builtin_amdgcn_ballot_w64(set);
+    same &= set ? one : ~one;
+  }
+  return same;
+}
+constexpr int bits_of(int n) { return n <= 1 ? 0 : 1 + bits_of((n + 1) / 2); }
+
+// place of this lane's key: lanes with the same key take consecutive places from at[key], which the
+// last of them moves on
+template <int BITS> __device__ __forceinline__ int32_t take_place(int32_t* at, uint32_t key, bool has, int lane) {
+  const uint64_t same = same_key<BITS>(key, has);
+  int32_t p = 0;
+  if (has) p = at[key] + prefix(same, lane);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  if (has && (same >> lane) == 1) at[key] = p + 1;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  return p;
+}
+
+// Exclusive sum over the workgroup's threads; `sums` holds a word per wave.
+__device__ __forceinline__ int32_t block_exclusive(int32_t v, int32_t* sums) {
+  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+  int32_t inc = v;
+  for (int o = 1; o < kWave; o <<= 1) { const int32_t u = __shfl_up(inc, o); if (lane >= o) inc += u; }
+  if (lane == kWave - 1) sums[w] = inc;
+  __syncthreads();
+  for (int i = 0; i < w; ++i) inc += sums[i];
+  __syncthreads();
+  return inc - v;
+}
+
+// hist[w][k] (tokens of key k in wave w's share) becomes the first place of key k in wave w, the
+// keys in order from `base`; returns the first place of key threadIdx.x.
+template <int N> __device__ __forceinline__ int32_t places(int32_t (*hist)[N], int n, int32_t base, int32_t* sums) {
+  int32_t cnt = 0;
+  if ((int)threadIdx.x < n)
+    for (int i = 0; i < SO_WAVES; ++i) cnt += hist[i][threadIdx.x];
+  const int32_t first = base + block_exclusive(cnt, sums);
+  if ((int)threadIdx.x < n) {
+    int32_t at = first;
+    for (int i = 0; i < SO_WAVES; ++i) { const int32_t h = hist[i][threadIdx.x]; hist[i][threadIdx.x] = at; at += h; }
+  }
+  __syncthreads();
+  return first;
+}
+
+// The tokens of range `lo`.., which stand in `list` in batch order (n of them from `base`), sorted by
+// id. The waves take contiguous shares.
+struct SortMem {
+  int32_t hist[SO_WAVES][kEmbedRange];
+  int32_t sums[SO_WAVES];
+};
+__device__ __forceinline__ void sort_range(const EmbedGrad& a, SortMem& m, int64_t lo, int nr, int32_t base, int32_t n) {
+  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+  const int32_t share = (n + SO_THREADS - 1) / SO_THREADS * kWave;
+  const int32_t b0 = min(w * share, n), b1 = min(b0 + share, n);
+  const GLOBAL uint64_t* list = gbl((const uint64_t*)a.list) + base;
+  for (int i = threadIdx.x; i < SO_WAVES * kEmbedRange; i += SO_THREADS) (&m.hist[0][0])[i] = 0;
+  __syncthreads();
+  for (int32_t b = b0 + lane; b < b1; b += kWave) atomicAdd(&m.hist[w][(uint32_t)(list[b] >> 32)], 1);
+  __syncthreads();
+  const int32_t first = places(m.hist, nr, base, m.sums);
+  if ((int)threadIdx.x < nr) gbl(a.seg)[lo + threadIdx.x] = first;
+  if (lo + nr == a.vocab && threadIdx.x == 0) gbl(a.seg)[a.vocab] = base + n;
+  for (int32_t b = b0; b < b1; b += kWave) {
+    const bool has = b + lane < b1;
+    const uint64_t e = has ? list[b + lane] : ~0ull;
+    const int32_t at = take_place<bits_of(kEmbedRange)>(m.hist[w], (uint32_t)(e >> 32), has, lane);
+    if (has) gbl(a.sorted)[at] = ((uint64_t)(lo + (e >> 32)) << 32) | (uint32_t)e;
+  }
+}
+
+// Short batches, one launch: the workgroup of a range reads all tokens (a few bytes each, from L2),
+// counts those below its range, which is where its part of the order begins, and keeps its own.
+// No workgroup waits for another. The time grows with n for every workgroup: 14 us at 20480 tokens
+// and 34 at 65537, where the three launches below take 15 and 17.
 template <int ID>
 __global__ __launch_bounds__(SO_THREADS)
 void k_embed_sort(EmbedGrad a)
 {
-  __shared__ int32_t hist[SO_WAVES][kEmbedRange];       // tokens of an id per wave, then places
-  __shared__ int32_t below_w[SO_WAVES], in_w[SO_WAVES], scan_w[SO_WAVES];
+  __shared__ SortMem m;
+  __shared__ int32_t below_w[SO_WAVES], in_w[SO_WAVES];
   const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
   const int64_t lo = (int64_t)blockIdx.x * a.range, hi = min(lo + a.range, a.vocab);
-  const int nr = (int)(hi - lo);
-  const int64_t share = (a.n + SO_WAVES * kWave - 1) / (SO_WAVES * kWave) * kWave;
+  const int64_t share = (a.n + SO_THREADS - 1) / SO_THREADS * kWave;
   const int64_t b0 = min(w * share, a.n), b1 = min(b0 + share, a.n);
-  for (int i = threadIdx.x; i < SO_WAVES * kEmbedRange; i += SO_THREADS) (&hist[0][0])[i] = 0;
-
   int32_t below = 0, in = 0;
   for (int64_t b = b0; b < b1; b += SO_UNROLL * kWave) {
     int64_t id[SO_UNROLL];
@@ -126,9 +208,7 @@ void k_embed_sort(EmbedGrad a)
   __syncthreads();
   int32_t base = 0, mine = 0, total = 0;
   for (int i = 0; i < SO_WAVES; ++i) { base += below_w[i]; mine += i < w ? in_w[i] : 0; total += in_w[i]; }
-
-  // the range's tokens, in batch order, each wave's share contiguous
-  uint64_t* __restrict__ list = a.list + base + mine;
+  GLOBAL uint64_t* list = gbl(a.list) + base + mine;
   int32_t put = 0;
   if (in > 0)
     for (int64_t b = b0; b < b1; b += SO_UNROLL * kWave) {
@@ -142,114 +222,161 @@ void k_embed_sort(EmbedGrad a)
       for (int u = 0; u < SO_UNROLL; ++u) {
         const bool mineid = id[u] >= lo && id[u] < hi;
         const uint64_t bal = __builtin_amdgcn_ballot_w64(mineid);
-        if (mineid) {
-          const int32_t key = (int32_t)(id[u] - lo);
-          list[put + __popcll(bal & ((1ull << lane) - 1))] = ((uint64_t)key << 32) | (uint32_t)(b + u * kWave + lane);
-          atomicAdd(&hist[w][key], 1);
-        }
+        if (mineid) list[put + prefix(bal, lane)] = ((uint64_t)(id[u] - lo) << 32) | (uint32_t)(b + u * kWave + lane);
         put += __popcll(bal);
       }
     }
   __syncthreads();
+  sort_range(a, m, lo, (int)(hi - lo), base, total);
+}
 
-  // first place of every id (exclusive sums over ids, then over waves within an id)
-  int32_t cnt = 0;
-  if ((int)threadIdx.x < nr)
-    for (int i = 0; i < SO_WAVES; ++i) cnt += hist[i][threadIdx.x];
-  int32_t inc = cnt;
-  for (int o = 1; o < kWave; o <<= 1) { const int32_t v = __shfl_up(inc, o); if (lane >= o) inc += v; }
-  if (lane == kWave - 1) scan_w[w] = inc;
+// Long batches, three launches. Tokens are dealt to workgroups in contiguous shares of `tokens`.
+// 1: tokens of every range in each share.
+template <int ID>
+__global__ __launch_bounds__(SO_THREADS)
+void k_embed_count(EmbedGrad a)
+{
+  __shared__ int32_t hist[kEmbedRanges];
+  const int nb = (int)((a.vocab + a.range - 1) / a.range);
+  for (int i = threadIdx.x; i < nb; i += SO_THREADS) hist[i] = 0;
   __syncthreads();
-  int32_t first = base + inc - cnt;
-  for (int i = 0; i < w; ++i) first += scan_w[i];
-  if ((int)threadIdx.x < nr) {
-    gbl(a.seg)[lo + threadIdx.x] = first;
-    for (int i = 0; i < SO_WAVES; ++i) { const int32_t h = hist[i][threadIdx.x]; hist[i][threadIdx.x] = first; first += h; }
+  const int64_t b0 = (int64_t)blockIdx.x * a.tokens, b1 = min(b0 + a.tokens, a.n);
+  for (int64_t t = b0 + threadIdx.x; t < b1; t += SO_THREADS) {
+    const int64_t id = load_id<ID>(a.ids, t);
+    if (id >= 0 && id < a.vocab) atomicAdd(&hist[(uint32_t)id / (uint32_t)a.range], 1);
   }
-  if (hi == a.vocab && threadIdx.x == 0) gbl(a.seg)[a.vocab] = base + total;
   __syncthreads();
+  for (int i = threadIdx.x; i < nb; i += SO_THREADS) gbl(a.count)[(int64_t)blockIdx.x * nb + i] = hist[i];
+}
 
-  // stable placement: 64 tokens of the wave's list at a time. Lanes with the same id take
-  // consecutive places; the last of them moves the id's place on.
-  for (int32_t i0 = 0; i0 < in; i0 += kWave) {
-    const bool has = i0 + lane < in;
-    const uint64_t e = has ? list[i0 + lane] : ~0ull;
-    const uint32_t key = (uint32_t)(e >> 32);
-    uint64_t same = __builtin_amdgcn_ballot_w64(has);
-    for (int bit = 0; bit < 32 - __builtin_clz(kEmbedRange - 1); ++bit) {
-      const uint64_t one = __builtin_amdgcn_ballot_w64((key >> bit) & 1);
-      same &= ((key >> bit) & 1) ? one : ~one;
+// 2: every share's tokens to their range's part of `list`. A range begins behind all tokens of the
+// ranges before it, a share's part of it behind those of the shares before.
+template <int ID>
+__global__ __launch_bounds__(SO_THREADS)
+void k_embed_deal(EmbedGrad a)
+{
+  __shared__ int32_t hist[SO_WAVES][kEmbedRanges];
+  __shared__ int32_t sums[SO_WAVES];
+  const int nb = (int)((a.vocab + a.range - 1) / a.range);
+  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave, r = threadIdx.x;
+  for (int i = threadIdx.x; i < SO_WAVES * kEmbedRanges; i += SO_THREADS) (&hist[0][0])[i] = 0;
+  int32_t total = 0, before = 0;
+  for (int g0 = 0; r < nb && g0 < (int)gridDim.x; g0 += 16) {
+    int32_t c[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) c[u] = g0 + u < (int)gridDim.x ? gbl((const int32_t*)a.count)[(int64_t)(g0 + u) * nb + r] : 0;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+      total += c[u];
+      before += g0 + u < (int)blockIdx.x ? c[u] : 0;
     }
-    int32_t at = 0;
-    if (has) at = hist[w][key] + __popcll(same & ((1ull << lane) - 1));
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    if (has) {
-      if ((same >> lane) == 1) hist[w][key] = at + 1;
-      gbl(a.sorted)[at] = ((uint64_t)(lo + key) << 32) | (uint32_t)e;
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+  }
+  const int32_t start = block_exclusive(total, sums);
+  if (blockIdx.x == 0 && r < nb) gbl(a.start)[r] = start;
+  if (blockIdx.x == 0 && r == nb - 1) gbl(a.start)[nb] = start + total;
+  const int64_t share = (a.tokens + SO_THREADS - 1) / SO_THREADS * kWave;
+  const int64_t g0 = (int64_t)blockIdx.x * a.tokens, g1 = min(g0 + a.tokens, a.n);
+  const int64_t b0 = min(g0 + w * share, g1), b1 = min(b0 + share, g1);
+  for (int64_t t = b0 + lane; t < b1; t += kWave) {
+    const int64_t id = load_id<ID>(a.ids, t);
+    if (id >= 0 && id < a.vocab) atomicAdd(&hist[w][(uint32_t)id / (uint32_t)a.range], 1);
+  }
+  __syncthreads();
+  if (r < nb) {
+    int32_t at = start + before;
+    for (int i = 0; i < SO_WAVES; ++i) { const int32_t h = hist[i][r]; hist[i][r] = at; at += h; }
+  }
+  __syncthreads();
+  for (int64_t b = b0; b < b1; b += kWave) {
+    const int64_t t = b + lane, id = t < b1 ? load_id<ID>(a.ids, t) : -1;
+    const bool has = id >= 0 && id < a.vocab;
+    const uint32_t bucket = has ? (uint32_t)id / (uint32_t)a.range : 0;
+    const int32_t at = take_place<bits_of(kEmbedRanges)>(hist[w], bucket, has, lane);
+    if (has) gbl(a.list)[at] = ((uint64_t)((uint32_t)id - bucket * (uint32_t)a.range) << 32) | (uint32_t)t;
   }
 }
 
-// ---- the sums ------------------------------------------------------------------------------
-constexpr int SU_THREADS = 256, SU_UNROLL = 8;
+// 3: every range by id.
+__global__ __launch_bounds__(SO_THREADS)
+void k_embed_order(EmbedGrad a)
+{
+  __shared__ SortMem m;
+  const int64_t lo = (int64_t)blockIdx.x * a.range;
+  const int32_t base = gbl((const int32_t*)a.start)[blockIdx.x], end = gbl((const int32_t*)a.start)[blockIdx.x + 1];
+  sort_range(a, m, lo, (int)min(a.range, a.vocab - lo), base, end - base);
+}
 
-// blockIdx.x < chunks: one chunk of the sorted order, 256 V columns. A token whose tokens all
-// lie in the chunk is finished here; a token that goes on into the next chunk or comes from the
-// one before leaves a partial row: slot 2 j + 1 where it begins in chunk j, 2 j where it does
-// not. The remaining workgroups write the zero rows of absent tokens.
-template <int T, int V>
+// ---- the sums ------------------------------------------------------------------------------
+constexpr int SU_THREADS = 256, SU_UNROLL = 8, JO_UNROLL = 16;
+
+// blockIdx.x < chunks: one chunk of the sorted order; blockIdx.y: blockDim.x V columns. A token
+// whose tokens all lie in the chunk is finished here; a token that goes on into the next chunk or
+// comes from the one before leaves a partial row: slot 2 j + 1 where it begins in chunk j, 2 j
+// where it does not. Where a run begins and ends is read off the neighbours in the sorted order, so
+// nothing but the rows themselves is waited for. The remaining workgroups write the zero rows of
+// absent tokens.
+template <int T, int V, bool ADD>
 __global__ __launch_bounds__(SU_THREADS)
 void k_embed_sum(EmbedGrad a)
 {
   typedef typename Vec<T, V>::f vf;
-  const int64_t col = ((int64_t)blockIdx.y * SU_THREADS + threadIdx.x) * V;
+  __shared__ uint64_t ent[kEmbedChunk + 2];      // the chunk's entries, and one before and behind
+  const int64_t col = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * V;
   const int64_t vocab = a.vocab;
   if ((int64_t)blockIdx.x >= a.chunks) {
     const int64_t v0 = ((int64_t)blockIdx.x - a.chunks) * kEmbedZeroRows;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int32_t s = gbl((const int32_t*)a.seg)[min(v0 + min(lane, kEmbedZeroRows), vocab)];
+    const int32_t next = __shfl_down(s, 1);      // by every lane, also those that ask for no row
+    uint64_t gone = __builtin_amdgcn_ballot_w64(lane < kEmbedZeroRows && v0 + lane < vocab && s == next);
     if (col >= a.dim) return;
-    for (int64_t v = v0; v < min(v0 + kEmbedZeroRows, vocab); ++v)
-      if (gbl(a.seg)[v] == gbl(a.seg)[v + 1]) Vec<G_F32, V>::store(a.dtable, v * a.ld_dtable + col, vf(0.0f));
+    for (; gone; gone &= gone - 1) Vec<G_F32, V>::store(a.dtable, (v0 + __builtin_ctzll(gone)) * a.ld_dtable + col, vf(0.0f));
     return;
   }
-  const int32_t total = gbl(a.seg)[vocab];
+  const int32_t total = gbl((const int32_t*)a.seg)[vocab];
   const int64_t p0 = (int64_t)blockIdx.x * a.chunk;
-  if (p0 >= total || col >= a.dim) return;
+  if (p0 >= total) return;
   const int cnt = (int)min((int64_t)a.chunk, total - p0);
-  const GLOBAL uint64_t* sorted = gbl(a.sorted) + p0;
+  for (int i = threadIdx.x; i < cnt + 2; i += blockDim.x) {
+    const int64_t p = p0 - 1 + i;
+    ent[i] = p >= 0 && p < total ? gbl((const uint64_t*)a.sorted)[p] : ~0ull;
+  }
+  __syncthreads();
+  if (col >= a.dim) return;
+  auto id_of = [&](int i) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)(ent[i + 1] >> 32)); };   // -1: before
+  auto pos_of = [&](int i) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)ent[i + 1]); };
   vf acc = 0.0f;
-  int run = 0;                                   // first position of the running token
+  bool begins = id_of(-1) != id_of(0);
   for (int i0 = 0; i0 < cnt; i0 += SU_UNROLL) {
-    uint64_t e[SU_UNROLL + 1];
-    vf x[SU_UNROLL];
+    vf x[SU_UNROLL], old[ADD ? SU_UNROLL : 1];
 #pragma unroll
     for (int u = 0; u < SU_UNROLL; ++u) {
-      e[u] = i0 + u < cnt ? sorted[i0 + u] : ~0ull;
-      x[u] = 0.0f;
-      if (i0 + u < cnt) x[u] = Vec<T, V>::load(a.dx, (int64_t)(uint32_t)e[u] * a.ld_dx + col);
+      // past the chunk its last row again: without a branch the loads of a batch are under way
+      // together
+      const int i = min(i0 + u, cnt - 1);
+      x[u] = Vec<T, V>::load(a.dx, (int64_t)pos_of(i) * a.ld_dx + col);
+      // the row to add to, where a token may end (one that leaves a partial row after all only
+      // reads it for nothing)
+      if (ADD && id_of(i) != id_of(i + 1)) old[ADD ? u : 0] = Vec<G_F32, V>::load(a.dtable, (int64_t)id_of(i) * a.ld_dtable + col);
     }
-    e[SU_UNROLL] = i0 + SU_UNROLL < cnt ? sorted[i0 + SU_UNROLL] : ~0ull;
+    __builtin_amdgcn_sched_barrier(0);           // or the loads sink to their uses
 #pragma unroll
     for (int u = 0; u < SU_UNROLL; ++u) {
-      if (i0 + u >= cnt) break;
+      const int i = i0 + u;
+      if (i >= cnt) break;
       acc += x[u];
-      const uint32_t v = (uint32_t)(e[u] >> 32);
-      if (i0 + u + 1 < cnt && (uint32_t)(e[u + 1] >> 32) == v) continue;
-      // the token's run in this chunk ends here
-      const int32_t s0 = gbl(a.seg)[v], s1 = gbl(a.seg)[(int64_t)v + 1];
-      const bool begins = s0 == p0 + run, ends = s1 == p0 + i0 + u + 1;
+      const uint32_t v = id_of(i);
+      const bool ends = id_of(i + 1) != v;
+      if (!ends && i + 1 < cnt) continue;
       if (begins && ends) {
-        const int64_t o = (int64_t)v * a.ld_dtable + col;
         vf r = a.scale * acc;
-        if (a.accumulate) r = Vec<G_F32, V>::load(a.dtable, o) + r;
-        Vec<G_F32, V>::store(a.dtable, o, r);
+        if constexpr (ADD) r = old[u] + r;
+        Vec<G_F32, V>::store(a.dtable, (int64_t)v * a.ld_dtable + col, r);
       } else {
         Vec<G_F32, V>::store(a.partial, (2 * (int64_t)blockIdx.x + (begins ? 1 : 0)) * a.ld_partial + col, acc);
       }
       acc = 0.0f;
-      run = i0 + u + 1;
+      begins = true;
     }
   }
 }
@@ -266,12 +393,20 @@ void k_embed_join(EmbedGrad a)
   const uint32_t v = (uint32_t)(gbl(a.sorted)[p1 - 1] >> 32);
   const int32_t s0 = gbl(a.seg)[v], s1 = gbl(a.seg)[(int64_t)v + 1];
   if (s0 < p0 || s1 <= p1) return;
-  const int64_t col = ((int64_t)blockIdx.y * SU_THREADS + threadIdx.x) * V;
+  const int64_t col = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * V;
   if (col >= a.dim) return;
   vf acc = Vec<G_F32, V>::load(a.partial, (2 * j + 1) * a.ld_partial + col);
   const int64_t je = (s1 - 1) / a.chunk;
-#pragma unroll 8
-  for (int64_t k = j + 1; k <= je; ++k) acc += Vec<G_F32, V>::load(a.partial, 2 * k * a.ld_partial + col);
+  for (int64_t k0 = j + 1; k0 <= je; k0 += JO_UNROLL) {       // a batch of loads at a time, the last one too
+    vf x[JO_UNROLL];
+#pragma unroll
+    for (int u = 0; u < JO_UNROLL; ++u) {
+      x[u] = 0.0f;
+      if (k0 + u <= je) x[u] = Vec<G_F32, V>::load(a.partial, 2 * (k0 + u) * a.ld_partial + col);
+    }
+#pragma unroll
+    for (int u = 0; u < JO_UNROLL; ++u) acc += x[u];
+  }
   const int64_t o = (int64_t)v * a.ld_dtable + col;
   vf r = a.scale * acc;
   if (a.accumulate) r = Vec<G_F32, V>::load(a.dtable, o) + r;
@@ -304,17 +439,27 @@ template <int T> hipError_t lookup_out(const EmbedLookup& a, int ot, int id_byte
   return hipGetLastError();
 }
 
+// Columns of V values over workgroups of whole waves, evenly.
+struct Cols { unsigned blocks, threads; };
+Cols cols_of(int64_t dim, int v) {
+  const int64_t vecs = (dim + v - 1) / v, blocks = (vecs + SU_THREADS - 1) / SU_THREADS;
+  return {(unsigned)blocks, (unsigned)(((vecs + blocks - 1) / blocks + kWave - 1) / kWave * kWave)};
+}
 template <int T, int V> hipError_t grad_sum(const EmbedGrad& a, hipStream_t s) {
-  const unsigned cols = (unsigned)((a.dim + SU_THREADS * V - 1) / (SU_THREADS * V));
+  const Cols c = cols_of(a.dim, V);
   const int64_t zero = a.accumulate ? 0 : (a.vocab + kEmbedZeroRows - 1) / kEmbedZeroRows;
-  if (a.chunks + zero > 0) k_embed_sum<T, V><<<dim3((unsigned)(a.chunks + zero), cols), dim3(SU_THREADS), 0, s>>>(a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.chunks < 2) return e;
-  k_embed_join<V><<<dim3((unsigned)(a.chunks - 1), cols), dim3(SU_THREADS), 0, s>>>(a);
+  const dim3 grid((unsigned)(a.chunks + zero), c.blocks), block(c.threads);
+  if (a.accumulate && a.chunks > 0) k_embed_sum<T, V, true><<<grid, block, 0, s>>>(a);
+  else if (!a.accumulate) k_embed_sum<T, V, false><<<grid, block, 0, s>>>(a);
+  if (const hipError_t e = hipGetLastError(); e != hipSuccess || a.chunks < 2) return e;
+  constexpr int VJ = V == 1 ? 1 : 4;
+  const Cols j = cols_of(a.dim, VJ);
+  k_embed_join<VJ><<<dim3((unsigned)(a.chunks - 1), j.blocks), dim3(j.threads), 0, s>>>(a);
   return hipGetLastError();
 }
 template <int T> hipError_t grad_vec(const EmbedGrad& a, hipStream_t s) {
-  if (a.dim % 4 == 0 && aligned(a.dx, a.ld_dx, T == G_F32 ? 4 : 2, 4) && aligned(a.dtable, a.ld_dtable, 4, 4)) return grad_sum<T, 4>(a, s);
+  constexpr int V = T == G_F32 ? 4 : 8, size = T == G_F32 ? 4 : 2;
+  if (a.dim % V == 0 && aligned(a.dx, a.ld_dx, size, V) && aligned(a.dtable, a.ld_dtable, 4, V)) return grad_sum<T, V>(a, s);
   return grad_sum<T, 1>(a, s);
 }
 
@@ -331,9 +476,21 @@ hipError_t launch_embed_lookup(const EmbedLookup& a, int tt, int ot, int id_byte
 }
 
 hipError_t launch_embed_grad(const EmbedGrad& a, int dt, int id_bytes, hipStream_t s) {
-  const dim3 grid((unsigned)((a.vocab + a.range - 1) / a.range)), block(SO_THREADS);
-  if (id_bytes == 4) k_embed_sort<4><<<grid, block, 0, s>>>(a);
-  else k_embed_sort<8><<<grid, block, 0, s>>>(a);
+  const dim3 ranges((unsigned)((a.vocab + a.range - 1) / a.range)), block(SO_THREADS);
+  if (a.tokens == 0) {
+    if (id_bytes == 4) k_embed_sort<4><<<ranges, block, 0, s>>>(a);
+    else k_embed_sort<8><<<ranges, block, 0, s>>>(a);
+  } else {
+    const dim3 shares((unsigned)((a.n + a.tokens - 1) / a.tokens));
+    if (id_bytes == 4) {
+      k_embed_count<4><<<shares, block, 0, s>>>(a);
+      k_embed_deal<4><<<shares, block, 0, s>>>(a);
+    } else {
+      k_embed_count<8><<<shares, block, 0, s>>>(a);
+      k_embed_deal<8><<<shares, block, 0, s>>>(a);
+    }
+    k_embed_order<<<ranges, block, 0, s>>>(a);
+  }
   if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   switch (dt) {
     case G_F32: return grad_vec<G_F32>(a, s);
@@ -348,6 +505,13 @@ int64_t embed_range(int64_t vocab) {
   const int64_t r = (vocab + 255) / 256;
   return r < 16 ? 16 : r > kEmbedRange ? kEmbedRange : r;
 }
-int embed_chunk(int64_t, int64_t) { return 32; }
+// Tokens per workgroup of the three-launch sort (at most 128 workgroups, since each adds up the
+// counts of all), or 0: one launch. That one takes any vocabulary.
+int64_t embed_tokens(int64_t n, int64_t vocab) {
+  const int64_t ranges = (vocab + embed_range(vocab) - 1) / embed_range(vocab);
+  if (n <= kEmbedShort || ranges > kEmbedRanges) return 0;
+  const int64_t t = (n + 127) / 128;
+  return t < 2048 ? 2048 : t;
+}
 
 }  // namespace psgd

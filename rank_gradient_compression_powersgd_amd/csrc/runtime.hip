@@ -1242,15 +1242,18 @@ psgd_status check_embed(psgd_ctx* ctx, const void* ids, psgd_itype it, int64_t n
   if (!std::isfinite(scale)) return fail(ctx, PSGD_EINVAL, "scale must be finite");
   return PSGD_OK;
 }
-struct EmbedLayout { int64_t chunk, chunks, list, sorted, seg, partial, ld_partial, bytes; };
+struct EmbedLayout { int64_t chunks, tokens, list, sorted, seg, count, start, partial, ld_partial, bytes; };
 EmbedLayout embed_layout(int64_t n, int64_t vocab, int64_t dim) {
   EmbedLayout L{};
-  L.chunk = psgd::embed_chunk(n, dim);
-  L.chunks = (n + L.chunk - 1) / L.chunk;
+  L.chunks = (n + psgd::kEmbedChunk - 1) / psgd::kEmbedChunk;
+  L.tokens = psgd::embed_tokens(n, vocab);
+  const int64_t range = psgd::embed_range(vocab), ranges = (vocab + range - 1) / range;
   L.list = 0;
   L.sorted = L.list + rup(8 * n, 256);
   L.seg = L.sorted + rup(8 * n, 256);
-  L.partial = L.seg + rup(4 * (vocab + 1), 256);
+  L.count = L.seg + rup(4 * (vocab + 1), 256);
+  L.start = L.count + (L.tokens ? rup(4 * ranges * ((n + L.tokens - 1) / L.tokens), 256) : 0);
+  L.partial = L.start + (L.tokens ? rup(4 * (ranges + 1), 256) : 0);
   L.ld_partial = rup(dim, 4);
   L.bytes = L.partial + 8 * L.chunks * L.ld_partial;
   return L;
@@ -1305,10 +1308,13 @@ psgd_status psgd_embed_grad(psgd_ctx* ctx, const void* dx, int64_t ld_dx, psgd_d
   a.dx = dx; a.ld_dx = ld_dx; a.ids = ids; a.n = n; a.vocab = vocab; a.dim = dim;
   a.dtable = dtable; a.ld_dtable = ld_dtable; a.scale = scale; a.accumulate = accumulate != 0;
   a.range = psgd::embed_range(vocab);
-  a.chunk = (int32_t)L.chunk; a.chunks = L.chunks;
+  a.chunk = psgd::kEmbedChunk; a.chunks = L.chunks;
+  a.tokens = L.tokens;
   a.list = reinterpret_cast<uint64_t*>(ws + L.list);
   a.sorted = reinterpret_cast<uint64_t*>(ws + L.sorted);
   a.seg = reinterpret_cast<int32_t*>(ws + L.seg);
+  a.count = reinterpret_cast<int32_t*>(ws + L.count);
+  a.start = reinterpret_cast<int32_t*>(ws + L.start);
   a.partial = reinterpret_cast<float*>(ws + L.partial);
   a.ld_partial = L.ld_partial;
   HIPCHK(ctx, psgd::launch_embed_grad(a, dt, (int)id_type, stream), "embedding gradient");

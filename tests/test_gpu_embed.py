@@ -231,3 +231,14 @@ def test_two_calls_at_once_and_graph_replays(ctx):
         psgd_embed_grad(ctx, xr, ids[0], got[1], workspace=ws[1])
         torch.cuda.synchronize()
         assert torch.equal(x, xr) and torch.equal(got[0], got[1]), t
+
+
+@pytest.mark.parametrize("n,vocab", [(16385, 3000), (24576, 3000), (24577, 3000), (40001, 9000), (300000, 130), (30000, 300001)])
+def test_grad_long_batches(ctx, n, vocab):
+    """Both sides of the length from which tokens are dealt to ranges by several workgroups, shares of
+    several sizes, and a vocabulary of more ranges than they deal to; half of the tokens are one."""
+    rng = np.random.default_rng(n)
+    ids = rng.integers(-1, vocab + 1, n)
+    ids[rng.random(n) < 0.5] = vocab // 2
+    _grad_case(ctx, n, vocab, 8, "f32", "i64", 1.0, False, ids)
+    _grad_case(ctx, n, vocab, 8, "bf16", "i32", 0.5, True, ids)
