@@ -574,7 +574,9 @@ def psgd_embed_grad(ctx: int, dx, ids, dtable, scale: float = 1.0, accumulate: b
             workspace = torch.empty(need, dtype=torch.uint8, device=dtable.device)
         else:
             # allocated on the stream that uses it, so that its memory is not handed out earlier
-            s = torch.cuda.ExternalStream(stream, dtable.device) if isinstance(stream, int) else stream
+            s = stream
+            if isinstance(stream, int):
+                s = torch.cuda.ExternalStream(stream, dtable.device) if stream else torch.cuda.default_stream(dtable.device)
             with torch.cuda.stream(s):
                 workspace = torch.empty(need, dtype=torch.uint8, device=dtable.device)
     elif not workspace.is_contiguous():

@@ -138,7 +138,7 @@ Planned plan_list(const std::vector<NsMat>& mats, NsStage st, bool accurate) {
       std::vector<double> cost;
       int64_t slots = 0;
       for (int i = 0; i < n; ++i) {
-        const int ks = stages(w[i]), want = i < whole ? 1 : (int)std::min(16.0, std::ceil(ks / limit));
+        const int ks = stages(w[i]), want = i < whole ? 1 : (int)std::min(32.0, std::ceil(ks / limit));
         const int per = ns_part(ks, want, accurate), parts = (ks + per - 1) / per;
         if (parts <= 1) {
           items.push_back({w[i], ks * tc.stage + fixed});

@@ -215,6 +215,12 @@ def test_two_calls_at_once_and_graph_replays(ctx):
     torch.cuda.synchronize()
     for a, b in zip(ref, got):
         assert torch.equal(a, b)
+    for i, stream in enumerate((0, streams[1].cuda_stream)):    # raw stream handles
+        got[i].zero_()
+        torch.cuda.synchronize()
+        psgd_embed_grad(ctx, dx[i], ids[i], got[i], stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(ref[i], got[i])
     need = psgd_embed_grad_workspace(n, vocab, dim)
     ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)]
     x, xr = torch.empty(n, dim, device="cuda"), torch.empty(n, dim, device="cuda")

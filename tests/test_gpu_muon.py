@@ -93,6 +93,48 @@ def test_larger_groups_and_low_rank(shapes, accurate):
     g.close()
 
 
+def _direct(u, coef=oracle.muon.QUINTIC, steps=5):
+    """The iteration itself in float64 on the device, for sizes whose SVD takes too long."""
+    import torch
+    x = u.double()
+    x = x / torch.linalg.vector_norm(x)
+    x = x.t().contiguous() if x.shape[0] > x.shape[1] else x
+    for _ in range(steps):
+        a = x @ x.t().contiguous()
+        x = coef[0] * x + (coef[1] * a + coef[2] * (a @ a)) @ x
+    return x.t() if u.shape[0] > u.shape[1] else x
+
+
+@pytest.mark.parametrize("accurate", [True, False])
+@pytest.mark.parametrize("shapes", [[(1030, 2049)] * 16, [(3000, 1111)] + [(530, 4100), (4100, 530)] * 9, [(40, 20000), (20000, 33)]])
+def test_groups_that_fill_the_chip(shapes, accurate):
+    """Enough work for the widest tiles, uneven lists whose longest products are split, and a few rows
+    over a long K; every matrix against float64, and each alone within a group of equals."""
+    import torch
+    from rank_gradient_compression_powersgd_amd import NewtonSchulzGroup
+    gen = torch.Generator(device="cuda").manual_seed(len(shapes))
+    ups = [torch.randn(m, n, device="cuda", generator=gen) * torch.rand(m, 1, device="cuda", generator=gen) for m, n in shapes]
+    outs = [torch.empty_like(u) for u in ups]
+    log(f"newton-schulz, {len(shapes)} matrices from {shapes[0]}, accurate={accurate}")
+    g = NewtonSchulzGroup(ups, outs, accurate)
+    g.run()
+    torch.cuda.synchronize()
+    for i, (u, o) in enumerate(zip(ups, outs)):
+        want = _direct(u)
+        norm = float(torch.linalg.vector_norm(want))
+        err = float(torch.linalg.vector_norm(o.double() - want))
+        tol = ((ACC_TOL if accurate else FAST_TOL) + EPS2["f32"]) * norm
+        if i < 3:
+            log(f"  {tuple(u.shape)}: {err / norm:.2e}")
+        assert err <= tol, (i, tuple(u.shape), err, tol)
+    first = [o.clone() for o in outs]
+    g.run()
+    torch.cuda.synchronize()
+    for a, b in zip(first, outs):
+        assert torch.equal(a, b)
+    g.close()
+
+
 @pytest.mark.parametrize("steps,coef", [(1, oracle.muon.QUINTIC), (2, oracle.muon.QUINTIC), (12, (1.5, -0.5, 0.0))])
 def test_steps_and_coefficients(steps, coef):
     import torch
