@@ -15,6 +15,7 @@ namespace psgd {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int BATCH = 4;                  // vectors a thread loads together
 constexpr int XT = 64;                    // X0 tile: XT x XT elements
 
 template <int IT> __device__ __forceinline__ float load1(const void* p, int64_t i) {
@@ -43,32 +44,55 @@ void k_ns_norm(const NsMat* __restrict__ mats, const Work* __restrict__ work, Ns
   const int n = d.n, r0 = wi.a, rows = min(d.part_rows, d.m - r0);
   const float clip = a.norm ? a.norm[1] : 1.0f;
   double acc = 0.0;
+  // a part holds fewer than 2^32 elements (a matrix that fits the memory has at most 1024 parts)
   if (vec4_ok<IT>(d)) {
     const uint32_t n4 = (uint32_t)n >> 2, total = (uint32_t)rows * n4;
-    for (uint32_t e = threadIdx.x; e < total; e += kThreads) {
-      const uint32_t r = e / n4, cidx = (e - r * n4) << 2;
-      f32x4 u = load4<IT>(d.in, (int64_t)(r0 + (int)r) * d.ld_in + cidx);
-      if (a.muon) {
-        GLOBAL f32x4* pm = gcast<f32x4>(gbl(d.mom) + (int64_t)(r0 + (int)r) * n + cidx);
-        const f32x4 g = clip * u, mo = a.mu * *pm + g;
-        *pm = mo;
-        u = a.nesterov ? g + a.mu * mo : mo;
+    for (uint32_t e0 = threadIdx.x; e0 < total; e0 += BATCH * kThreads) {
+      f32x4 u[BATCH], mo[BATCH];
+      int64_t at[BATCH];
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {        // past the end the last element again, not counted
+        const uint32_t e = min(e0 + k * kThreads, total - 1), r = e / n4, col = (e - r * n4) << 2;
+        u[k] = load4<IT>(d.in, (int64_t)(r0 + (int)r) * d.ld_in + col);
+        at[k] = (int64_t)(r0 + (int)r) * n + col;
+        if (a.muon) mo[k] = *gcast<f32x4>(gbl(d.mom) + at[k]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc += (double)u[i] * (double)u[i];
+      for (int k = 0; k < BATCH; ++k) {
+        if (e0 + k * kThreads >= total) break;
+        f32x4 x = u[k];
+        if (a.muon) {
+          const f32x4 g = clip * x, m1 = a.mu * mo[k] + g;
+          *gcast<f32x4>(gbl(d.mom) + at[k]) = m1;
+          x = a.nesterov ? g + a.mu * m1 : m1;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc += (double)x[i] * (double)x[i];
+      }
     }
   } else {
-    const uint64_t total = (uint64_t)rows * (uint32_t)n;
-    for (uint64_t e = threadIdx.x; e < total; e += kThreads) {
-      const uint32_t r = (uint32_t)(e / (uint32_t)n), cidx = (uint32_t)(e - (uint64_t)r * (uint32_t)n);
-      float u = load1<IT>(d.in, (int64_t)(r0 + (int)r) * d.ld_in + cidx);
-      if (a.muon) {
-        GLOBAL float* pm = gbl(d.mom) + (int64_t)(r0 + (int)r) * n + cidx;
-        const float g = clip * u, mo = a.mu * *pm + g;
-        *pm = mo;
-        u = a.nesterov ? g + a.mu * mo : mo;
+    const uint32_t total = (uint32_t)rows * (uint32_t)n;
+    for (uint32_t e0 = threadIdx.x; e0 < total; e0 += 2 * BATCH * kThreads) {
+      float u[2 * BATCH], mo[2 * BATCH];
+      int64_t at[2 * BATCH];
+#pragma unroll
+      for (int k = 0; k < 2 * BATCH; ++k) {
+        const uint32_t e = min(e0 + k * kThreads, total - 1), r = e / (uint32_t)n, col = e - r * (uint32_t)n;
+        u[k] = load1<IT>(d.in, (int64_t)(r0 + (int)r) * d.ld_in + col);
+        at[k] = (int64_t)(r0 + (int)r) * n + col;
+        if (a.muon) mo[k] = gbl(d.mom)[at[k]];
       }
-      acc += (double)u * (double)u;
+#pragma unroll
+      for (int k = 0; k < 2 * BATCH; ++k) {
+        if (e0 + k * kThreads >= total) break;
+        float x = u[k];
+        if (a.muon) {
+          const float g = clip * x, m1 = a.mu * mo[k] + g;
+          gbl(d.mom)[at[k]] = m1;
+          x = a.nesterov ? g + a.mu * m1 : m1;
+        }
+        acc += (double)x * (double)x;
+      }
     }
   }
   __shared__ double red[kThreads];
@@ -99,6 +123,38 @@ void k_ns_x0(const NsMat* __restrict__ mats, const Work* __restrict__ work, NsAr
   const NsMat& d = mats[wi.mat];
   __shared__ double red[kThreads];
   __shared__ float tile[XT][XT + 1];
+  const float clip = a.norm ? a.norm[1] : 1.0f;
+  const int i0 = wi.a, j0 = wi.b;
+  // rows and columns of the update under this tile, loaded before the norm is added up
+  const int r0 = d.flip ? j0 : i0, c0 = d.flip ? i0 : j0;
+  const bool v4 = vec4_ok<IT>(d);
+  constexpr int PER = XT * XT / 4 / kThreads;
+  f32x4 u[PER];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int e = threadIdx.x + k * kThreads, row = r0 + (e >> 4), col = c0 + ((e & 15) << 2);
+    u[k] = f32x4{0, 0, 0, 0};
+    if (row < d.m && col < d.n) {
+      if (v4) {
+        u[k] = load4<IT>(d.in, (int64_t)row * d.ld_in + col);
+        if (a.muon) {
+          const f32x4 mo = *gcast<f32x4>(gbl(d.mom) + (int64_t)row * d.n + col);
+          u[k] = a.nesterov ? clip * u[k] + a.mu * mo : mo;
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          if (col + t < d.n) {
+            float x = load1<IT>(d.in, (int64_t)row * d.ld_in + col + t);
+            if (a.muon) {
+              const float mo = gbl(d.mom)[(int64_t)row * d.n + col + t];
+              x = a.nesterov ? clip * x + a.mu * mo : mo;
+            }
+            u[k][t] = x;
+          }
+      }
+    }
+  }
   double acc = 0.0;
   for (int i = threadIdx.x; i < d.parts; i += kThreads) acc += gbl(d.partial)[i];
   red[threadIdx.x] = acc;
@@ -110,36 +166,11 @@ void k_ns_x0(const NsMat* __restrict__ mats, const Work* __restrict__ work, NsAr
   const double norm = sqrt(red[0]);
   // a norm that is NaN stays NaN (max would drop it)
   const double inv = (double)kNsScaleX / (norm < a.eps ? a.eps : norm);
-  const float clip = a.norm ? a.norm[1] : 1.0f;
-  const int i0 = wi.a, j0 = wi.b;
-  // rows and columns of the update under this tile
-  const int r0 = d.flip ? j0 : i0, c0 = d.flip ? i0 : j0;
-  const bool v4 = vec4_ok<IT>(d);
-  for (int e = threadIdx.x; e < XT * XT / 4; e += kThreads) {
-    const int r = e >> 4, c = (e & 15) << 2, row = r0 + r, col = c0 + c;
-    f32x4 u = {0, 0, 0, 0};
-    if (row < d.m && col < d.n) {
-      if (v4) {
-        u = load4<IT>(d.in, (int64_t)row * d.ld_in + col);
-        if (a.muon) {
-          const f32x4 mo = *gcast<f32x4>(gbl(d.mom) + (int64_t)row * d.n + col);
-          u = a.nesterov ? clip * u + a.mu * mo : mo;
-        }
-      } else {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          if (col + t < d.n) {
-            float x = load1<IT>(d.in, (int64_t)row * d.ld_in + col + t);
-            if (a.muon) {
-              const float mo = gbl(d.mom)[(int64_t)row * d.n + col + t];
-              x = a.nesterov ? clip * x + a.mu * mo : mo;
-            }
-            u[t] = x;
-          }
-      }
-    }
+  for (int k = 0; k < PER; ++k) {
+    const int e = threadIdx.x + k * kThreads, r = e >> 4, c = (e & 15) << 2;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) tile[r][c + t] = (float)((double)u[t] * inv);
+    for (int t = 0; t < 4; ++t) tile[r][c + t] = (float)((double)u[k][t] * inv);
   }
   __syncthreads();
   GLOBAL uint16_t* xh = gbl(d.xh[0]);

@@ -193,8 +193,8 @@ hipError_t NsGroup::create(const std::vector<Item>& items, int in_type, int out_
     d.m = (int)t.m; d.n = (int)t.n;
     d.flip = t.m > t.n;
     d.s = std::min(d.m, d.n); d.l = std::max(d.m, d.n);
-    // parts of at least 8192 elements, at most 1024 of them (every X0 workgroup adds them up)
-    d.part_rows = (int)std::max<int64_t>((8192 + t.n - 1) / t.n, (t.m + 1023) / 1024);
+    // parts of at least 4096 elements, at most 1024 of them (every X0 workgroup adds them up)
+    d.part_rows = (int)std::max<int64_t>((4096 + t.n - 1) / t.n, (t.m + 1023) / 1024);
     d.parts = (d.m + d.part_rows - 1) / d.part_rows;
   }
   const Planned plan[3] = {plan_list(mats, NS_GRAM, accurate), plan_list(mats, NS_POLY, accurate),
