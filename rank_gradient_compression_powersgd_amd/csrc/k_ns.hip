@@ -184,7 +184,7 @@ void k_ns_x0(const NsMat* __restrict__ mats, const Work* __restrict__ work, NsAr
       const bool in = i0 + i < d.s && j0 + j + t < d.l;
       split16(in ? (d.flip ? tile[j + t][i] : tile[i][j + t]) : 0.0f, h[t], l[t]);
     }
-    const int64_t off = (int64_t)(i0 + i) * d.lp + j0 + j;
+    const int64_t off = ((int64_t)((j0 + j) >> 5) * d.sp + i0 + i) * 32 + (j & 31);      // ns.h: panels of 32 columns
     *gcast<u32x2>(xh + off) = u32x2{(uint32_t)h[0] | ((uint32_t)h[1] << 16), (uint32_t)h[2] | ((uint32_t)h[3] << 16)};
     *gcast<u32x2>(xl + off) = u32x2{(uint32_t)l[0] | ((uint32_t)l[1] << 16), (uint32_t)l[2] | ((uint32_t)l[3] << 16)};
   }

@@ -28,14 +28,11 @@ __device__ __forceinline__ i16x4 lds_read_tr16(const uint16_t* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(p));
 }
 
-// K-outer rows (LDS row = one k, T values): a transposing read touches one pair of 16-byte units
-// in each of the rows k = 8 g + t (+ 4); the rows of lanes 0..31 (g = 0, 1; t = 0..3), and those
-// of lanes 32..63, must land on 8 distinct 32-byte groups of the 256 bytes of banks. Rows k and
-// k + 4 share their swizzle.
-template <int T> __device__ __forceinline__ int swz_outer(int k, int q) {
-  if constexpr (T == 64) return q ^ (2 * (((k >> 1) & 1) | (((k >> 3) & 1) << 1)));   // 128-byte rows
-  else return q ^ (2 * ((k & 3) | (((k >> 3) & 1) << 2)));                            // 256 or 512
-}
+// A stage of P read K-outer is 32 x 32 blocks, 64 bytes per k. A transposing read touches 32 bytes
+// in each of the rows k = 8 g + t (+ 4): the rows of lanes 0..31 (g = 0, 1; t = 0..3) and those of
+// lanes 32..63 each have to land on 8 distinct 32-byte groups of the 256 bytes of banks, so the two
+// 32-byte halves of a row change places with every 8 k.
+__device__ __forceinline__ int swz_outer(int k, int q) { return q ^ (((k >> 3) & 1) << 1); }
 // K-contiguous rows are 64 bytes (4 units): 8 consecutive rows put one logical unit on the 8
 // distinct 16-byte groups of one LDS pass.
 __device__ __forceinline__ int swz_inner(int row, int q) { return q ^ ((row >> 1) & 3); }
@@ -127,15 +124,16 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
   const int c = lane & 15, g = lane >> 4;
 
   const GLOBAL uint16_t *ph, *pl, *qh, *ql;
-  int ldp, ldq, K;
   if constexpr (ST == NS_GRAM) {
-    ph = qh = gbl(d.xh[cur]); pl = ql = gbl(d.xl[cur]); ldp = ldq = d.lp; K = d.l;
+    ph = qh = gbl(d.xh[cur]); pl = ql = gbl(d.xl[cur]);
   } else if constexpr (ST == NS_POLY) {
-    ph = qh = gbl(d.ah); pl = ql = gbl(d.al); ldp = ldq = d.sp; K = d.s;
+    ph = qh = gbl(d.ah); pl = ql = gbl(d.al);
   } else {
-    ph = gbl(d.xh[cur]); pl = gbl(d.xl[cur]); ldp = d.lp;
-    qh = gbl(d.bh); ql = gbl(d.bl); ldq = d.sp; K = d.s;
+    ph = gbl(d.xh[cur]); pl = gbl(d.xl[cur]);
+    qh = gbl(d.bh); ql = gbl(d.bl);
   }
+  const int K = ST == NS_GRAM ? d.l : d.s;
+  const int64_t panel = (int64_t)d.sp * KB;    // elements from one panel of 32 columns to the next
   // whole pairs of 32 k (the padding up to a tile holds zeros); accurate: two stages per 32 k
   int nst = ns_stages(K, ACC);
   int k0 = 0;                                  // first k of this part
@@ -150,7 +148,8 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
   // this wave's loads of a stage: load x < PL is 1 KB of P, the others of Q
   constexpr int PL = TL::LOADS / 2;
   uint32_t poff[PL], qoff[PL];
-  const int64_t pfirst = OUTER ? (int64_t)k0 * ldp + i0 : (int64_t)i0 * ldp + k0, qfirst = (int64_t)j0 * ldq + k0;
+  const int64_t pfirst = OUTER ? i0 / KB * panel + k0 * KB : k0 / KB * panel + i0 * KB, qfirst = k0 / KB * panel + j0 * KB;
+  const int64_t pstage = OUTER ? KB * KB : panel;             // elements from stage to stage
   const GLOBAL uint16_t* const pbase_h = ph + pfirst;
   const GLOBAL uint16_t* const qbase_h = qh + qfirst;
   const GLOBAL uint16_t* const pbase_l = pl + pfirst;
@@ -158,20 +157,17 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
 #pragma unroll
   for (int x = 0; x < PL; ++x) {
     const int e = (wv * PL + x) * kWave + lane;              // 16-byte slot of the operand's stage
-    qoff[x] = ((uint32_t)(e >> 2) * (uint32_t)ldq + 8u * swz_inner(e >> 2, e & 3)) * 2u;
-    if constexpr (OUTER) {
-      const int k = e / (T / 8);
-      poff[x] = ((uint32_t)k * (uint32_t)ldp + 8u * swz_outer<T>(k, e % (T / 8))) * 2u;
-    } else {
-      poff[x] = ((uint32_t)(e >> 2) * (uint32_t)ldp + 8u * swz_inner(e >> 2, e & 3)) * 2u;
-    }
+    const int r = e >> 2;                                    // its row: 64 bytes, contiguous with the next
+    qoff[x] = (uint32_t)(r * KB + 8 * swz_inner(r, e & 3)) * 2u;
+    if constexpr (OUTER) poff[x] = (uint32_t)((r / KB) * panel + (r % KB) * KB + 8 * swz_outer(r % KB, e & 3)) * 2u;
+    else poff[x] = qoff[x];
   }
   // load x of stage j: P and Q in turn
   auto load_part = [&](int j, int x) {
     const int ks = ACC ? j >> 1 : j;
     const uint32_t l = lds0 + (uint32_t)(j % RING) * (2 * TL::BYTES) + wv * (PL * 1024) + (x >> 1) * 1024;
-    if (x & 1) load_lds16((ACC && (j & 1) ? qbase_l : qbase_h) + (int64_t)ks * KB, qoff[x >> 1], l + TL::BYTES);
-    else load_lds16((ACC && (j & 1) ? pbase_l : pbase_h) + (OUTER ? (int64_t)ks * KB * ldp : (int64_t)ks * KB), poff[x >> 1], l);
+    if (x & 1) load_lds16((ACC && (j & 1) ? qbase_l : qbase_h) + ks * panel, qoff[x >> 1], l + TL::BYTES);
+    else load_lds16((ACC && (j & 1) ? pbase_l : pbase_h) + ks * pstage, poff[x >> 1], l);
   };
 
   f32x4 acc[TL::TA][TL::TB];
@@ -198,9 +194,9 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
   auto read_p = [&](Frag& f, int j, int a) {
     const uint16_t* lp = lds[j % RING];
     if constexpr (OUTER) {
-      const int k = 8 * g + (c >> 2), u = (wi0 + 16 * a) / 8 + ((c & 3) >> 1);
-      const uint16_t* s = &lp[k * T + 8 * swz_outer<T>(k, u) + 4 * (c & 1)];
-      const i16x4 x = lds_read_tr16(s), y = lds_read_tr16(s + 4 * T);
+      const int k = 8 * g + (c >> 2), col = wi0 + 16 * a, u = 2 * ((col / 16) & 1) + ((c & 3) >> 1);
+      const uint16_t* s = &lp[col / KB * (KB * KB) + k * KB + 8 * swz_outer(k, u) + 4 * (c & 1)];
+      const i16x4 x = lds_read_tr16(s), y = lds_read_tr16(s + 4 * KB);
       f.p[a] = __builtin_bit_cast(f16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
       const int r = wi0 + 16 * a + c;
@@ -425,17 +421,20 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
   const uint32_t reg0 = lds0 + 2 * part;
   const int ib = i0 + wi0, jb = j0 + wj0;
 
-  // rows j of WI values: a lane's four are half a unit
-  constexpr int UI = WI / 8, UJ = WJ / 8;
+  // In the workspace's layout: panels of 32 columns, 64 bytes per row, so a wave's tile is a
+  // contiguous block per panel.
+  auto swz_out = [](int r, int u) { return u ^ ((r >> 2) & 3); };
+  // rows j, columns i: a lane's four values are half a unit
   auto at_ji = [&](int a, int b) {
-    const int r = 16 * b + c, u = (2 * a + (g >> 1)) ^ (r & (UI - 1));
-    return reg + r * WI + 8 * u + 4 * (g & 1);
+    const int r = 16 * b + c, u = 2 * (a & 1) + (g >> 1);
+    return reg + (a >> 1) * (WJ * KB) + r * KB + 8 * swz_out(r, u) + 4 * (g & 1);
   };
-  auto fetch = [&](const GLOBAL uint16_t* src, int ld) {
+  auto fetch = [&](const GLOBAL uint16_t* src) {
+    const GLOBAL uint16_t* s = src + ib / KB * panel + jb * KB;
 #pragma unroll
     for (int x = 0; x < WI * WJ / 512; ++x) {
-      const int e = x * kWave + lane, r = e / UI, u = (e % UI) ^ (r & (UI - 1));
-      load_lds16(src + (int64_t)jb * ld + ib, ((uint32_t)r * (uint32_t)ld + 8u * u) * 2u, reg0 + x * 1024);
+      const int e = x * kWave + lane, r = (e >> 2) % WJ;
+      load_lds16(s + x * 512 / (WJ * KB) * panel, (uint32_t)(r * KB + 8 * swz_out(r, e & 3)) * 2u, reg0 + x * 1024);
     }
     wait_loads<0>();
   };
@@ -446,8 +445,19 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
       for (int b = 0; b < TL::TB; ++b) acc[a][b] += f * h2f4(*reinterpret_cast<const u32x2*>(at_ji(a, b)));
     wait_loads<0>();
   };
+  // what stands in `reg`, panels of R rows, to rows row.. of the panels from `col` on
+  auto send_out = [&](GLOBAL uint16_t* dst, int row, int col, auto rows) {
+    constexpr int R = decltype(rows)::value;
+    GLOBAL uint16_t* o = dst + col / KB * panel + row * KB;
+#pragma unroll
+    for (int x = 0; x < WI * WJ / 512; ++x) {
+      const int e = x * kWave + lane, r = (e >> 2) % R;
+      *gcast<u32x4>(o + x * 512 / (R * KB) * panel + r * KB + 8 * (e & 3)) =
+          *reinterpret_cast<const u32x4*>(reg + x * 512 / (R * KB) * (R * KB) + r * KB + 8 * swz_out(r, e & 3));
+    }
+  };
   // the fp16 of acc (LO: of what rounding to it leaves) to rows j of dst
-  auto flush_ji = [&](GLOBAL uint16_t* dst, int ld, bool lo) {
+  auto flush_ji = [&](GLOBAL uint16_t* dst, bool lo) {
 #pragma unroll
     for (int a = 0; a < TL::TA; ++a)
 #pragma unroll
@@ -455,15 +465,10 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
         const u32x2 h = f2h4(acc[a][b]);
         *reinterpret_cast<u32x2*>(at_ji(a, b)) = lo ? f2h4(acc[a][b] - h2f4(h)) : h;
       }
-    GLOBAL uint16_t* o = dst + (int64_t)jb * ld + ib;
-#pragma unroll
-    for (int x = 0; x < WI * WJ / 512; ++x) {
-      const int e = x * kWave + lane, r = e / UI, u = e % UI;
-      *gcast<u32x4>(o + (int64_t)r * ld + 8 * u) = *reinterpret_cast<const u32x4*>(reg + r * WI + 8 * (u ^ (r & (UI - 1))));
-    }
+    send_out(dst, jb, ib, std::integral_constant<int, WJ>{});
   };
   // the same to rows i of dst
-  auto flush_ij = [&](GLOBAL uint16_t* dst, int ld, bool lo) {
+  auto flush_ij = [&](GLOBAL uint16_t* dst, bool lo) {
 #pragma unroll
     for (int a = 0; a < TL::TA; ++a)
 #pragma unroll
@@ -471,16 +476,11 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
         const u32x2 h = f2h4(acc[a][b]), v = lo ? f2h4(acc[a][b] - h2f4(h)) : h;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const int r = 16 * a + 4 * g + t, u = (2 * b + (c >> 3)) ^ (r & (UJ - 1));
-          reg[r * WJ + 8 * u + (c & 7)] = (uint16_t)(v[t >> 1] >> (16 * (t & 1)));
+          const int r = 16 * a + 4 * g + t, u = 2 * (b & 1) + (c >> 3);
+          reg[(b >> 1) * (WI * KB) + r * KB + 8 * swz_out(r, u) + (c & 7)] = (uint16_t)(v[t >> 1] >> (16 * (t & 1)));
         }
       }
-    GLOBAL uint16_t* o = dst + (int64_t)ib * ld + jb;
-#pragma unroll
-    for (int x = 0; x < WI * WJ / 512; ++x) {
-      const int e = x * kWave + lane, r = e / UJ, u = e % UJ;
-      *gcast<u32x4>(o + (int64_t)r * ld + 8 * u) = *reinterpret_cast<const u32x4*>(reg + r * WJ + 8 * (u ^ (r & (UJ - 1))));
-    }
+    send_out(dst, ib, jb, std::integral_constant<int, WI>{});
   };
   // rows j >= s and columns i >= `imax` are padding and hold zeros, also beside NaN
   auto mask = [&](int imax) {
@@ -505,10 +505,10 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
 
   if constexpr (ST != NS_UPDATE) {
     if constexpr (ST == NS_POLY) {
-      fetch(gbl(d.ah), d.sp);
+      fetch(gbl(d.ah));
       add(na.b * (kNsScaleB / kNsScaleA));
       if constexpr (ACC) {
-        fetch(gbl(d.al), d.sp);
+        fetch(gbl(d.al));
         add(na.b * (kNsScaleB / kNsScaleA));
       } else if (i0 == j0) {
         // the fast form multiplies by a I + B: the hi half of a X comes out of the product
@@ -524,26 +524,26 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
     mask(d.s);
     GLOBAL uint16_t* oh = gbl(ST == NS_GRAM ? d.ah : d.bh);
     GLOBAL uint16_t* ol = gbl(ST == NS_GRAM ? d.al : d.bl);
-    flush_ji(oh, d.sp, false);
-    if constexpr (ACC) flush_ji(ol, d.sp, true);
+    flush_ji(oh, false);
+    if constexpr (ACC) flush_ji(ol, true);
     if (i0 != j0) {
-      flush_ij(oh, d.sp, false);
-      if constexpr (ACC) flush_ij(ol, d.sp, true);
+      flush_ij(oh, false);
+      if constexpr (ACC) flush_ij(ol, true);
     }
   } else {
     if constexpr (ACC) {
-      fetch(gbl(d.xh[cur]), d.lp);
+      fetch(gbl(d.xh[cur]));
       add(na.a);
     }
     // The fast form needs no lo in the last step: nothing multiplies that rounding again.
     if constexpr (ACC || OT == 0) {
-      fetch(gbl(d.xl[cur]), d.lp);
+      fetch(gbl(d.xl[cur]));
       add(na.a);
     }
     if constexpr (OT == 0) {
       mask(d.l);
-      flush_ji(gbl(d.xh[cur ^ 1]), d.lp, false);
-      if (ACC || step + 2 < na.steps) flush_ji(gbl(d.xl[cur ^ 1]), d.lp, true);
+      flush_ji(gbl(d.xh[cur ^ 1]), false);
+      if (ACC || step + 2 < na.steps) flush_ji(gbl(d.xl[cur ^ 1]), true);
     } else {
       // half of the wave's i at a time, as fp32 rows of the output (rows i when X is transposed)
       constexpr int HI = WI / 2;

@@ -14,6 +14,9 @@ namespace psgd {
 //   X  (sp x lp)  as hi + lo, X * 2^14 = hi + lo to 2^-22: singular values stay below 4
 //   A  (sp x sp)  X X^T, times 2^14 (entries bounded by the squared singular values)
 //   B  (sp x sp)  b A + c A A, times 2^10
+// All of them are stored as panels of 32 columns, one after another, 64 bytes per row within a panel:
+// what a product stage of 32 k loads of a tile's rows (and, read the other way round, of its columns)
+// is then contiguous. Row by row the 64-byte pieces kept a CU's loads to half of their rate.
 // A and B are symmetric: only the tiles on and below the diagonal are computed, and each is
 // stored twice.
 constexpr float kNsScaleX = 16384.0f, kNsScaleA = 16384.0f, kNsScaleB = 1024.0f;
