@@ -438,11 +438,14 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
     }
     wait_loads<0>();
   };
-  auto add = [&](float f) {                                  // acc += f * fetched
+  auto add = [&](float f) {                                  // acc += f * fetched, few at a time: no registers to spare
 #pragma unroll
     for (int a = 0; a < TL::TA; ++a)
 #pragma unroll
-      for (int b = 0; b < TL::TB; ++b) acc[a][b] += f * h2f4(*reinterpret_cast<const u32x2*>(at_ji(a, b)));
+      for (int b = 0; b < TL::TB; ++b) {
+        __builtin_amdgcn_sched_barrier(0);
+        acc[a][b] += f * h2f4(*reinterpret_cast<const u32x2*>(at_ji(a, b)));
+      }
     wait_loads<0>();
   };
   // what stands in `reg`, panels of R rows, to rows row.. of the panels from `col` on
@@ -482,17 +485,9 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
       }
     send_out(dst, ib, jb, std::integral_constant<int, WI>{});
   };
-  // rows j >= s and columns i >= `imax` are padding and hold zeros, also beside NaN
-  auto mask = [&](int imax) {
-    if (ib + WI <= imax && jb + WJ <= d.s) return;
-#pragma unroll
-    for (int a = 0; a < TL::TA; ++a)
-#pragma unroll
-      for (int b = 0; b < TL::TB; ++b)
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          if (ib + 16 * a + 4 * g + t >= imax || jb + 16 * b + c >= d.s) acc[a][b][t] = 0.0f;
-  };
+  // Nothing masks the padding, rows j >= s and columns i >= s or l: its products are of X0's zeros.
+  // A NaN in X is in all of X by way of the norm, so the padding may be NaN beside it; the next
+  // call writes every element anew.
 
   constexpr float kProd = ST == NS_GRAM ? kNsScaleA / (kNsScaleX * kNsScaleX)
                         : ST == NS_POLY ? kNsScaleB / (kNsScaleA * kNsScaleA)
@@ -521,7 +516,6 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
               if (ib + 16 * a + 4 * g + t == jb + 16 * b + c) acc[a][b][t] += na.a * kNsScaleB;
       }
     }
-    mask(d.s);
     GLOBAL uint16_t* oh = gbl(ST == NS_GRAM ? d.ah : d.bh);
     GLOBAL uint16_t* ol = gbl(ST == NS_GRAM ? d.al : d.bl);
     flush_ji(oh, false);
@@ -541,7 +535,6 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
       add(na.a);
     }
     if constexpr (OT == 0) {
-      mask(d.l);
       flush_ji(gbl(d.xh[cur ^ 1]), false);
       if (ACC || step + 2 < na.steps) flush_ji(gbl(d.xl[cur ^ 1]), true);
     } else {
