@@ -22,18 +22,20 @@ struct Item {
   double cost;                           // microseconds on a CU of its own
 };
 
-// Cost model of a product list, in microseconds, from runs of lists of one tile width.
-//   stage   one stage of 32 k of a tile that has its CU to itself
-//   full    the same on a full chip, which runs at its power limit
+// Cost model of a product list, in microseconds, fitted to runs of 13 groups in each tile width.
+//   stage   one stage of 32 k of a tile, on a chip that is idle but for it
+//   full    the same on a full chip, which runs at its power limit; in between by the share of CUs
+//           that have an item
 //   fixed, fixed_update  what a tile costs beside its stages (the update reads and writes X)
-// 256-wide tiles do 1.9 times the work per microsecond of 128-wide ones and three times that of
-// 64-wide ones once the CUs are full; below that the narrow ones finish first (an update of 496 x
-// 3968: 8 us in 64-wide tiles, 14 in 128-wide ones, 26 in 256-wide ones; four resblocks: 794, 499 and
-// 391 us). Accurate products (two stages per 32 k, three products for two stages' loads) run at the
-// MFMA's pace from 128-wide tiles on; 256-wide ones would not hold both halves in registers.
+// On a full chip 256-wide tiles do 1.6 times the work per microsecond of 128-wide ones and 2.4 times
+// that of 64-wide ones (A of four 2480 x 2480 in 61, 72 and 100 us); where there are few tiles the
+// narrow ones finish first (A of 496 x 3968, unsplit: 62, 27 and 18 us; its update 16, 9.1 and 8.7).
+// Accurate products (two stages per 32 k, three products for two stages' loads) run at the MFMA's
+// pace from 128-wide tiles on (the same A: 221 and 252 us); 256-wide ones would not hold both halves
+// in registers.
 struct TileCost { int tile; double stage, full, fixed, fixed_update; };
-constexpr TileCost kFast[] = {{64, 0.14, 0.16, 1.5, 2.5}, {128, 0.29, 0.36, 2.5, 7.0}, {256, 0.75, 0.85, 7.0, 15.0}};
-constexpr TileCost kAccurate[] = {{64, 0.17, 0.19, 1.5, 3.0}, {128, 0.33, 0.37, 2.5, 8.0}};
+constexpr TileCost kFast[] = {{64, 0.12, 0.11, 0.7, 0.8}, {128, 0.18, 0.29, 1.5, 2.5}, {256, 0.43, 0.75, 6.0, 7.0}};
+constexpr TileCost kAccurate[] = {{64, 0.145, 0.14, 0.7, 1.0}, {128, 0.29, 0.37, 3.0, 4.0}};
 constexpr double kLaunch = 4.0;              // a second, dependent launch
 constexpr double kMemory = 4.0e6;            // bytes per microsecond of partial sums
 
@@ -141,14 +143,15 @@ Planned plan_list(const std::vector<NsMat>& mats, NsStage st, bool accurate) {
         const int ks = stages(w[i]), want = i < whole ? 1 : (int)std::min(32.0, std::ceil(ks / limit));
         const int per = ns_part(ks, want, accurate), parts = (ks + per - 1) / per;
         if (parts <= 1) {
-          items.push_back({w[i], ks * tc.stage + fixed});
+          items.push_back({w[i], (double)ks});
         } else {
           reduce.push_back(Work{w[i].mat, w[i].a, w[i].b | parts, (int)slots});
           for (int p = 0; p < parts; ++p, ++slots)
-            items.push_back({Work{w[i].mat, w[i].a | p, w[i].b | parts, (int)slots}, std::min(per, ks - p * per) * tc.stage + fixed});
+            items.push_back({Work{w[i].mat, w[i].a | p, w[i].b | parts, (int)slots}, (double)std::min(per, ks - p * per)});
         }
       }
-      for (const Item& x : items) cost.push_back(x.cost);
+      const double stage = tc.stage + (tc.full - tc.stage) * std::min(1.0, (double)items.size() / kCus);
+      for (Item& x : items) cost.push_back(x.cost = x.cost * stage + fixed);
       double time = std::max(makespan(cost), total * tc.full / kCus);
       if (slots) time += kLaunch + (2.0 * slots + reduce.size()) * tile_bytes / kMemory;
       // a split has to promise a twentieth: the model is no better than that
