@@ -10,7 +10,7 @@
 // in 22 bits is what keeps the fast form usable: the rounding of a factor of B X or X X^T only
 // reaches directions the update already has, while a rounded X itself would put noise into the
 // directions it lacks, which every step then multiplies by a = 3.4 (an update of rank 112 came
-// out 3% off, against 0.06%). The accurate products use both halves of every factor
+// out 3% off, against 0.15%). The accurate products use both halves of every factor
 // (hi hi + hi lo + lo hi): the result agrees with fp32 products.
 #include <type_traits>
 
@@ -101,8 +101,7 @@ template <int T> struct Tile {
 //
 // Split items. A tile whose K is cut into wi.b & 63 parts leaves part wi.a & 63 as raw fp32
 // accumulators in slot wi.c of `partial`; the launch with REDUCE adds a tile's slots wi.c, wi.c + 1,
-// ... in order and runs the epilogue, each wave of
-// the tile as a workgroup of its own.
+// ... in order and runs the epilogue, each wave of the tile as a workgroup of its own.
 template <int ST, int T, bool ACC, int OT, bool REDUCE>
 __global__ __launch_bounds__(REDUCE ? kWave : Tile<T>::THREADS, 2)
 void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, float* __restrict__ partial, int step,
@@ -281,11 +280,28 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
 
   if constexpr (REDUCE) {
     const GLOBAL f32x4* s = gcast<f32x4>(gbl(partial)) + (int64_t)wi.c * (T * T / 4) + wv * (TL::TA * TL::TB * kWave) + lane;
-    for (int x = 0; x < splits; ++x, s += T * T / 4)
+    auto add_slots = [&](auto count) {                        // loads of several slots at once, added in order
+      constexpr int N = decltype(count)::value;
+      f32x4 v[N][TL::TA][TL::TB];
 #pragma unroll
-      for (int a = 0; a < TL::TA; ++a)
+      for (int x = 0; x < N; ++x)
 #pragma unroll
-        for (int b = 0; b < TL::TB; ++b) acc[a][b] += s[(a * TL::TB + b) * kWave];
+        for (int a = 0; a < TL::TA; ++a)
+#pragma unroll
+          for (int b = 0; b < TL::TB; ++b) v[x][a][b] = s[x * (T * T / 4) + (a * TL::TB + b) * kWave];
+#pragma unroll
+      for (int x = 0; x < N; ++x)
+#pragma unroll
+        for (int a = 0; a < TL::TA; ++a)
+#pragma unroll
+          for (int b = 0; b < TL::TB; ++b) acc[a][b] += v[x][a][b];
+      s += N * (T * T / 4);
+    };
+    int x = 0;
+    constexpr int GO = T == 64 ? 4 : T == 128 ? 2 : 1;
+    for (; x + GO <= splits; x += GO) add_slots(std::integral_constant<int, GO>{});
+    if constexpr (GO > 1)
+      for (; x < splits; ++x) add_slots(N1{});
   } else if constexpr (T == 256) {
     static_assert(!ACC, "128-wide tiles at most: both halves' fragments beside 128 accumulators do not fit");
     // Two waves per SIMD take turns: while waves 0..3 multiply, waves 4..7 read their fragments and
@@ -412,8 +428,7 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
 
   // ---- epilogue --------------------------------------------------------------------------
   // Through this wave's own part of the ring, so that memory sees whole rows, 16 bytes a lane: a
-  // lane's accumulators are 8 bytes in each of 16 rows (stored as they lie they ran at a third of
-  // the bandwidth). 16-byte units are XOR-ed by their row, which keeps both sides conflict-free.
+  // lane's accumulators are 8 bytes in each of 16 rows. 16-byte units are XOR-ed by their row, which keeps both sides conflict-free.
   constexpr int WI = T / 2, WJ = T / TL::WN;                 // the wave's tile of C
   __syncthreads();                                           // the ring is read out
   const int part = REDUCE ? 0 : wv * (WI * WJ);
@@ -563,28 +578,42 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
           }
         const int row0 = d.flip ? ib + h * HI : jb, col0 = d.flip ? jb : ib + h * HI;
         const int units = cols / 4;
-        for (int x = 0; x < HI * WJ / 256; ++x) {
-          const int e = x * kWave + lane, r = e / units, u = e % units;
-          const int row = row0 + r, col = col0 + 4 * u;
-          if (row >= d.m || col >= d.n) continue;
-          f32x4 v = *reinterpret_cast<const f32x4*>(&regf[r * cols + 4 * (u ^ (r & (units - 1)))]);
-          const int64_t o = (int64_t)row * d.ld_out + col;
-          if (vec) {
-            if (na.muon) {
-              const f32x4 th = out_load4<OT>(d.out, o);
-              v = th - na.lr * (d.factor * v + na.weight_decay * th);
-            }
-            out_store4<OT>(d.out, o, v);
-          } else {
+        // A batch of loads before the first is waited for (one at a time: four resblocks' last update
+        // 448 us, so 391). Their addresses are clamped into the parameter, nothing is stored past it.
+        constexpr int BATCH = 8;
+        static_assert(HI * WJ / 256 % BATCH == 0 || HI * WJ / 256 < BATCH);
+        constexpr int PASS = HI * WJ / 256 < BATCH ? HI * WJ / 256 : BATCH;
+        for (int x0 = 0; x0 < HI * WJ / 256; x0 += PASS) {
+          f32x4 th[PASS];
+          if (vec && na.muon) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              if (col + t >= d.n) continue;
-              float y = v[t];
-              if (na.muon) {
-                const float th = out_load<OT>(d.out, o + t);
-                y = th - na.lr * (d.factor * y + na.weight_decay * th);
+            for (int y = 0; y < PASS; ++y) {
+              const int e = (x0 + y) * kWave + lane;
+              const int row = min(row0 + e / units, d.m - 1), col = min(col0 + 4 * (e % units), d.n - 4);
+              th[y] = out_load4<OT>(d.out, (int64_t)row * d.ld_out + col);
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < PASS; ++y) {
+            const int e = (x0 + y) * kWave + lane, r = e / units, u = e % units;
+            const int row = row0 + r, col = col0 + 4 * u;
+            if (row >= d.m || col >= d.n) continue;
+            f32x4 v = *reinterpret_cast<const f32x4*>(&regf[r * cols + 4 * (u ^ (r & (units - 1)))]);
+            const int64_t o = (int64_t)row * d.ld_out + col;
+            if (vec) {
+              if (na.muon) v = th[y] - na.lr * (d.factor * v + na.weight_decay * th[y]);
+              out_store4<OT>(d.out, o, v);
+            } else {
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                if (col + t >= d.n) continue;
+                float w = v[t];
+                if (na.muon) {
+                  const float one = out_load<OT>(d.out, o + t);
+                  w = one - na.lr * (d.factor * w + na.weight_decay * one);
+                }
+                out_store<OT>(d.out, o + t, w);
               }
-              out_store<OT>(d.out, o + t, y);
             }
           }
         }
