@@ -345,8 +345,9 @@ psgd_status psgd_adam_update(psgd_ctx* ctx, const psgd_adam_tensor* pass, int n_
  * rounding of a bf16 output. PSGD_NS_ACCURATE multiplies fp16 halves hi + lo (three products),
  * as close to the exact result as fp32 products, at about a third of the speed.
  *
- * Coefficients: the singular values entering each step must stay below 1.97 and |b x^2 + c x^4|
- * below 60 (checked on the host by following the polynomial from [0, 1]); others are rejected with PSGD_EUNSUPPORTED. The usual (3.4445, -4.7750, 2.0315) and (1.5, -0.5, 0) pass.
+ * Coefficients: the singular values entering each step must stay below 1.97, |b x^2 + c x^4| and
+ * |a + b x^2 + c x^4| at most 60 (checked on the host by following the polynomial from [0, 1]);
+ * others are rejected with PSGD_EUNSUPPORTED. (3.4445, -4.7750, 2.0315) and (1.5, -0.5, 0) pass.
  */
 typedef enum psgd_ns_precision { PSGD_NS_FAST = 0, PSGD_NS_ACCURATE = 1 } psgd_ns_precision;
 

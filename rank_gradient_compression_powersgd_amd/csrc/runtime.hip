@@ -1072,14 +1072,14 @@ psgd_status check_ns(psgd_ctx* ctx, const psgd_ns_hparams& h) {
   if (!(h.eps > 0.0f) || !std::isfinite(h.eps)) return fail(ctx, PSGD_EINVAL, "eps must be finite and > 0");
   if (h.steps < 1 || h.steps > 32) return fail(ctx, PSGD_EINVAL, "steps must lie in [1, 32], got %d", h.steps);
   // Follow the largest singular value the polynomial can produce from [0, hi]: fp16 holds
-  // 2^14 X, 2^14 X X^T and 2^10 B.
+  // 2^14 X, 2^14 X X^T and 2^10 B, or 2^10 (a I + B) in the fast form.
   const double a = h.a, b = h.b, c = h.c;
   double hi = 1.0;
   for (int k = 0; k < h.steps; ++k) {
     double next = 0.0;
     for (int i = 0; i <= 512; ++i) {
       const double x = hi * i / 512, x2 = x * x, p = b * x2 + c * x2 * x2;
-      if (std::fabs(p) > 60.0)
+      if (std::fabs(p) > 60.0 || std::fabs(a + p) > 60.0)
         return fail(ctx, PSGD_EUNSUPPORTED, "the Newton-Schulz coefficients leave the fp16 range of B at step %d", k);
       next = std::max(next, std::fabs(x * (a + p)));
     }

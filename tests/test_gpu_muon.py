@@ -148,6 +148,23 @@ def test_steps_and_coefficients(steps, coef):
     g.close()
 
 
+@pytest.mark.parametrize("a", [59.0, -59.0])
+@pytest.mark.parametrize("accurate", [True, False])
+def test_largest_linear_coefficient(a, accurate):
+    """One step of X <- a X: 2^10 a = 60416 is an fp16 number, so what is left of the fast form is
+    the rounding of X to fp16, 2^-11 of each element at most, and the output's 2^-24."""
+    import torch
+    from rank_gradient_compression_powersgd_amd import NewtonSchulzGroup, ns_hparams
+    u = torch.from_numpy(_update(90, 200, 5)).float().cuda()
+    out = torch.empty_like(u)
+    g = NewtonSchulzGroup([u], [out], accurate=accurate)
+    g.run(ns_hparams(a=a, b=0.0, c=0.0, steps=1))
+    torch.cuda.synchronize()
+    want = a * _np(u) / np.linalg.norm(_np(u))
+    assert np.linalg.norm(_np(out) - want) <= (2.0 ** -11 + 2.0 ** -22) * np.linalg.norm(want)
+    g.close()
+
+
 def test_strides_alignment_in_place_and_untouched_memory():
     import torch
     from rank_gradient_compression_powersgd_amd import NewtonSchulzGroup

@@ -123,7 +123,8 @@ def test_c_refusals():
     g = NewtonSchulzGroup([x], [torch.empty_like(x)])
     for bad, status in ((ns_hparams(steps=0), B.PSGD_EINVAL), (ns_hparams(steps=33), B.PSGD_EINVAL), (ns_hparams(eps=0.0), B.PSGD_EINVAL),
                         (ns_hparams(a=float("nan")), B.PSGD_EINVAL), (ns_hparams(a=5.0, b=0.0, c=0.0), B.PSGD_EUNSUPPORTED),
-                        (ns_hparams(c=100.0), B.PSGD_EUNSUPPORTED)):
+                        (ns_hparams(c=100.0), B.PSGD_EUNSUPPORTED), (ns_hparams(a=61.0, b=0.0, c=0.0, steps=1), B.PSGD_EUNSUPPORTED),
+                        (ns_hparams(a=-61.0, b=1.0, c=0.0, steps=1), B.PSGD_EUNSUPPORTED)):
         _raises(status, lambda: g.run(bad))
     _raises(B.PSGD_EINVAL, lambda: B.psgd_newton_schulz(ctx, g.plan), "context")
     g.close()
