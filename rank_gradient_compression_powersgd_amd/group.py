@@ -116,21 +116,23 @@ class PowerSGDGroup:
         m x n (fp16, bf16 or fp32), momentum m x n fp32. The group needs its out buffers
         (write_out). accurate: products as exact as fp32 ones; default: for fp32 parameters,
         whose rounding the fast products' 2e-3 of the update would exceed."""
-        torch = self.torch
-        self.muon_params, self.momentum = list(params), list(momentum)
-        if accurate is None:
-            accurate = self.muon_params[0].dtype == torch.float32
-        if any(p.dtype != self.muon_params[0].dtype for p in self.muon_params):
-            raise B.PsgdError("psgd_muon_attach", B.PSGD_EDTYPE, "parameters must have one dtype")
-        if len(self.muon_params) != len(self.err) or len(self.momentum) != len(self.err):
-            raise B.PsgdError("psgd_muon_attach", B.PSGD_EINVAL, "one param and one momentum per matrix")
-        for p, e in zip(self.muon_params, self.err):
+        torch, call = self.torch, "psgd_muon_attach"
+        params, momentum = list(params), list(momentum)
+        if len(params) != len(self.err) or len(momentum) != len(self.err):
+            raise B.PsgdError(call, B.PSGD_EINVAL, "one param and one momentum per matrix")
+        if any(p.dtype != params[0].dtype for p in params):
+            raise B.PsgdError(call, B.PSGD_EDTYPE, "parameters must have one dtype")
+        for p, e in zip(params, self.err):
             if tuple(p.shape) != tuple(e.shape):
-                raise B.PsgdError("psgd_muon_attach", B.PSGD_EINVAL, "param and matrix shapes differ")
-        B._same_device("psgd_muon_attach", self.flags, *self.muon_params, *self.momentum)
-        opt = [B.make_muon_matrix(p, m) for p, m in zip(self.muon_params, self.momentum)]
-        B.psgd_muon_attach(self.ctx, self.plan, opt, B._dtype(self.muon_params[0], "psgd_muon_attach"),
+                raise B.PsgdError(call, B.PSGD_EINVAL, "param and matrix shapes differ")
+        B._same_device(call, self.flags, *params, *momentum)
+        if accurate is None:
+            accurate = params[0].dtype == torch.float32
+        opt = [B.make_muon_matrix(p, m) for p, m in zip(params, momentum)]
+        B.psgd_muon_attach(self.ctx, self.plan, opt, B._dtype(params[0], call),
                            B.PSGD_NS_ACCURATE if accurate else B.PSGD_NS_FAST)
+        # only now: a refused call leaves the attached tensors alive
+        self.muon_params, self.momentum = params, momentum
         if not hasattr(self, "adam_step"):
             dev = self.flags.device
             self.adam_step = torch.zeros(1, dtype=torch.int32, device=dev)
@@ -142,6 +144,8 @@ class PowerSGDGroup:
         decompression, momentum and orthogonalised update, fp32 Adam (hp_pass) on the
         pass-through tensors. passthrough: (param, m1, m2, grad) fp32 tensors, e.g. an embedding
         with its psgd_embed_grad gradient."""
+        if not hasattr(self, "muon_params"):
+            raise B.PsgdError("psgd_muon_update", B.PSGD_EINVAL, "no Muon state attached (attach_muon)")
         if passthrough and hp_pass is None:
             raise ValueError("pass-through tensors need their Adam hyperparameters (hp_pass)")
         self.compress(stream)

@@ -151,7 +151,13 @@ def test_c_refusals():
     _raises(B.PSGD_EINVAL, lambda: B.psgd_muon_update(grp.ctx, grp.plan, grp.skip, None, muon_hparams(0.1)), "psgd_muon_attach")
     _raises(B.PSGD_EINVAL, lambda: grp.attach_muon([x], []))
     _raises(B.PSGD_EINVAL, lambda: grp.attach_muon([torch.zeros(8, 16, device="cuda")], [torch.zeros(8, 16, device="cuda")]))
+    _raises(B.PSGD_EINVAL, lambda: grp.step_muon(muon_hparams(0.1)), "attach_muon")
     grp.attach_muon([x], [x.clone()])
+    kept = grp.muon_params[0], grp.momentum[0]
+    _raises(B.PSGD_EINVAL, lambda: grp.attach_muon([], []))
+    _raises(B.PSGD_EDTYPE, lambda: grp.attach_muon([x.double()], [x.clone()]))
+    _raises(B.PSGD_EDTYPE, lambda: grp.attach_muon([x.clone()], [x.half()]))
+    assert grp.muon_params[0] is kept[0] and grp.momentum[0] is kept[1]        # the library still points to them
     for bad in (muon_hparams(-1.0), muon_hparams(0.1, momentum=1.0), muon_hparams(0.1, weight_decay=float("inf")),
                 muon_hparams(0.1, adjust=2), muon_hparams(0.1, steps=0)):
         _raises(B.PSGD_EINVAL, lambda: B.psgd_muon_update(grp.ctx, grp.plan, grp.skip, None, bad))
