@@ -429,8 +429,9 @@ psgd_status psgd_muon_update(psgd_ctx* ctx, psgd_plan* plan, const int32_t* skip
  *     touched. Ids outside [0, vocab) are ignored. Non-finite dx values end up in dtable.
  * table, dx and out: fp16, bf16 or fp32, row-major, any leading dimension >= dim, aligned to their
  * element type. ids: n int32 (PSGD_I32) or int64 (PSGD_I64) on the device. dtable: fp32.
- * 0 <= n < 2^31 (0: lookup does nothing, gradient clears dtable unless accumulating),
- * 1 <= vocab < 2^31, 1 <= dim <= 2^23. Outputs must not overlap inputs.
+ * 0 <= n <= 2^25 (0: lookup does nothing, gradient clears dtable unless accumulating),
+ * 1 <= vocab < 2^31 in the lookup and <= 2^20 in the gradient, 1 <= dim <= 2^23. Outputs must not
+ * overlap inputs.
  *   workspace: psgd_embed_grad_workspace(n, vocab, dim) bytes of device memory, 16-byte aligned,
  *     contents ignored and overwritten; calls that may overlap need one each.
  * Asynchronous on stream; no plan involved, no allocation.

@@ -500,9 +500,10 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
       }
     send_out(dst, ib, jb, std::integral_constant<int, WI>{});
   };
-  // Nothing masks the padding, rows j >= s and columns i >= s or l: its products are of X0's zeros.
-  // A NaN in X is in all of X by way of the norm, so the padding may be NaN beside it; the next
-  // call writes every element anew.
+  // Nothing masks the padding. Sums run over whole pairs of 32 k: up to there rows and columns past s
+  // and l are products of X0's zeros. What lies further out, up to the wider of two products' tiles,
+  // may never have been written and only reaches elements as far out. A NaN in X is in all of X by
+  // way of the norm, so the padding may be NaN beside it; the next call writes all of it anew.
 
   constexpr float kProd = ST == NS_GRAM ? kNsScaleA / (kNsScaleX * kNsScaleX)
                         : ST == NS_POLY ? kNsScaleB / (kNsScaleA * kNsScaleA)

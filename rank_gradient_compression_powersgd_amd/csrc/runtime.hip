@@ -1233,10 +1233,15 @@ psgd_status psgd_muon_update(psgd_ctx* ctx, psgd_plan* plan, const int32_t* skip
 }
 
 namespace {
-psgd_status check_embed(psgd_ctx* ctx, const void* ids, psgd_itype it, int64_t n, int64_t vocab, int64_t dim, float scale) {
+// A launch is at most 2^32 threads long: 64 per token in the lookup. The gradient's vocabulary is
+// bounded for its time, since past 2^18 ids its sort reads every id once per 512 of them.
+constexpr int64_t kMaxTokens = 1 << 25, kMaxGradVocab = 1 << 20;
+
+psgd_status check_embed(psgd_ctx* ctx, const void* ids, psgd_itype it, int64_t n, int64_t vocab, int64_t max_vocab, int64_t dim, float scale) {
   if (it != PSGD_I32 && it != PSGD_I64) return fail(ctx, PSGD_EDTYPE, "ids must be int32 or int64");
-  if (n < 0 || n > 0x7fffffffll) return fail(ctx, PSGD_EINVAL, "n = %lld outside [0, 2^31)", (long long)n);
-  if (vocab < 1 || vocab > 0x7fffffffll) return fail(ctx, PSGD_EINVAL, "vocab = %lld outside [1, 2^31)", (long long)vocab);
+  if (n < 0 || n > kMaxTokens) return fail(ctx, PSGD_EINVAL, "n = %lld outside [0, %lld]", (long long)n, (long long)kMaxTokens);
+  if (vocab < 1 || vocab > max_vocab)
+    return fail(ctx, PSGD_EINVAL, "vocab = %lld outside [1, %lld]", (long long)vocab, (long long)max_vocab);
   if (dim < 1 || dim > (1 << 23)) return fail(ctx, PSGD_EINVAL, "dim = %lld outside [1, 2^23]", (long long)dim);
   if (n > 0 && (!ids || !aligned_to(ids, (int)it))) return fail(ctx, PSGD_EINVAL, "ids must be a pointer aligned to its element type");
   if (!std::isfinite(scale)) return fail(ctx, PSGD_EINVAL, "scale must be finite");
@@ -1267,7 +1272,7 @@ psgd_status psgd_embed_lookup(psgd_ctx* ctx, const void* table, int64_t ld_table
   ctx->err.clear();
   const int tt = grad_type(table_dtype), ot = grad_type(out_dtype);
   if (!tt || !ot) return fail(ctx, PSGD_EDTYPE, "unknown table or output dtype");
-  if (psgd_status st = check_embed(ctx, ids, id_type, n, vocab, dim, scale); st != PSGD_OK) return st;
+  if (psgd_status st = check_embed(ctx, ids, id_type, n, vocab, 0x7fffffffll, dim, scale); st != PSGD_OK) return st;
   if (ld_table < dim || ld_out < dim) return fail(ctx, PSGD_EINVAL, "leading dimensions must be >= dim");
   if (n == 0) return PSGD_OK;
   if (!table || !out || !aligned_to(table, type_size(tt)) || !aligned_to(out, type_size(ot)))
@@ -1280,7 +1285,8 @@ psgd_status psgd_embed_lookup(psgd_ctx* ctx, const void* table, int64_t ld_table
 }
 
 psgd_status psgd_embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim, int64_t* bytes) {
-  if (!bytes || check_embed(nullptr, reinterpret_cast<const void*>(8), PSGD_I64, n, vocab, dim, 1.0f) != PSGD_OK) return PSGD_EINVAL;
+  if (!bytes || check_embed(nullptr, reinterpret_cast<const void*>(8), PSGD_I64, n, vocab, kMaxGradVocab, dim, 1.0f) != PSGD_OK)
+    return PSGD_EINVAL;
   *bytes = embed_layout(n, vocab, dim).bytes;
   return PSGD_OK;
 }
@@ -1293,7 +1299,7 @@ psgd_status psgd_embed_grad(psgd_ctx* ctx, const void* dx, int64_t ld_dx, psgd_d
   ctx->err.clear();
   const int dt = grad_type(dx_dtype);
   if (!dt) return fail(ctx, PSGD_EDTYPE, "unknown gradient dtype %d", (int)dx_dtype);
-  if (psgd_status st = check_embed(ctx, ids, id_type, n, vocab, dim, scale); st != PSGD_OK) return st;
+  if (psgd_status st = check_embed(ctx, ids, id_type, n, vocab, kMaxGradVocab, dim, scale); st != PSGD_OK) return st;
   if (ld_dx < dim || ld_dtable < dim) return fail(ctx, PSGD_EINVAL, "leading dimensions must be >= dim");
   if (!dtable || !aligned_to(dtable, 4)) return fail(ctx, PSGD_EINVAL, "dtable must be a pointer aligned to its element type");
   if (n > 0 && (!dx || !aligned_to(dx, type_size(dt)))) return fail(ctx, PSGD_EINVAL, "dx must be a pointer aligned to its element type");

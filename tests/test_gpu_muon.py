@@ -222,6 +222,33 @@ def test_zero_tiny_huge_and_non_finite_updates():
     g.close()
 
 
+@pytest.mark.parametrize("accurate", [True, False])
+@pytest.mark.parametrize("shapes", [[(33, 65)], [(40, 20000), (300, 64)], [(1100, 130)] * 3, [(700, 1500)] * 9])
+def test_nothing_of_a_nan_is_left(shapes, accurate):
+    """A call on NaN leaves NaN in all of the workspace; the next call's result is a fresh plan's,
+    bit for bit, whatever tile widths the three products take."""
+    import torch
+    from rank_gradient_compression_powersgd_amd import NewtonSchulzGroup
+    good = [torch.from_numpy(_update(m, n, 70 + i)).float().cuda() for i, (m, n) in enumerate(shapes)]
+    ups = [torch.full_like(x, float("nan")) for x in good]
+    outs, fresh = [torch.empty_like(x) for x in good], [torch.empty_like(x) for x in good]
+    g = NewtonSchulzGroup(ups, outs, accurate=accurate)
+    g.run()
+    torch.cuda.synchronize()
+    assert all(bool(o.isnan().all()) for o in outs)
+    for u, x in zip(ups, good):
+        u.copy_(x)
+    g.run()
+    h = NewtonSchulzGroup(good, fresh, accurate=accurate)
+    h.run()
+    torch.cuda.synchronize()
+    for i, (a, b) in enumerate(zip(outs, fresh)):
+        assert torch.equal(a, b), i
+        _check(_np(a), oracle.newton_schulz(_np(good[i])), "f32", accurate, f"{shapes[i]} after NaN")
+    g.close()
+    h.close()
+
+
 def test_other_stream_and_graph_replays():
     import torch
     from rank_gradient_compression_powersgd_amd import NewtonSchulzGroup

@@ -52,13 +52,13 @@ def test_calls_without_a_context():
     assert lib.psgd_embed_lookup(None, None, 1, 1, 1, 3, None, 8, 1, 1.0, None, 1, 3, None) == B.PSGD_EINVAL
     assert lib.psgd_embed_grad(None, None, 1, 3, None, 8, 1, 1, 1, 1.0, None, 1, 0, None, 0, None) == B.PSGD_EINVAL
     assert lib.psgd_embed_grad_workspace(1, 1, 1, None) == B.PSGD_EINVAL
-    for bad in ((-1, 1, 1), (2 ** 31, 1, 1), (1, 0, 1), (1, 2 ** 31, 1), (1, 1, 0), (1, 1, 2 ** 23 + 1)):
+    for bad in ((-1, 1, 1), (2 ** 25 + 1, 1, 1), (2 ** 31, 1, 1), (1, 0, 1), (1, 2 ** 20 + 1, 1), (1, 1, 0), (1, 1, 2 ** 23 + 1)):
         assert lib.psgd_embed_grad_workspace(*bad, ctypes.byref(n)) == B.PSGD_EINVAL
     assert lib.psgd_embed_grad_workspace(0, 1, 1, ctypes.byref(n)) == B.PSGD_OK and n.value > 0
 
 
 def test_workspace_grows_past_32_bits():
-    assert B.psgd_embed_grad_workspace(2 ** 31 - 1, 2 ** 31 - 1, 1) > 2 ** 35
+    assert B.psgd_embed_grad_workspace(2 ** 25, 2 ** 20, 2 ** 14) > 2 ** 36
 
 
 def test_newton_schulz_binding_checks():
@@ -131,7 +131,7 @@ def test_c_refusals():
     lib, null = B.load_library(), None
     look = lambda **k: lib.psgd_embed_lookup(ctx, *{**dict(t=x.data_ptr(), lt=16, v=16, d=16, td=3, i=x.data_ptr(), it=8, n=2, s=1.0,  # noqa: E731
                                                            o=x.data_ptr(), lo=16, od=3, st=None), **k}.values())
-    for k in (dict(t=null), dict(o=null), dict(i=null), dict(lt=15), dict(lo=15), dict(n=-1), dict(v=0), dict(d=0), dict(s=float("inf")),
+    for k in (dict(t=null), dict(o=null), dict(i=null), dict(lt=15), dict(lo=15), dict(n=-1), dict(v=0), dict(d=0), dict(s=float("inf")), dict(n=2 ** 25 + 1), dict(v=2 ** 31),
               dict(i=x.data_ptr() + 4), dict(t=x.data_ptr() + 2)):
         assert look(**k) == B.PSGD_EINVAL, k
     for k in (dict(td=7), dict(od=0), dict(it=3)):
