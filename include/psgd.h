@@ -341,9 +341,9 @@ psgd_status psgd_adam_update(psgd_ctx* ctx, const psgd_adam_tensor* pass, int n_
  * and leaves the others alone.
  *
  * Products. PSGD_NS_FAST multiplies factors rounded to fp16 (2^-12 each) with fp32 sums and
- * carries X itself in 22 bits: the result is within about 2e-3 of its Frobenius norm, the
- * rounding of a bf16 output. PSGD_NS_ACCURATE multiplies fp16 halves hi + lo (three products),
- * as close to the exact result as fp32 products, at about a third of the speed.
+ * carries X itself in 22 bits: the result is within about 2e-3 of its Frobenius norm (4e-3 for a
+ * few rows of equal singular values), the rounding of a bf16 output. PSGD_NS_ACCURATE multiplies fp16 halves hi + lo (three products),
+ * as close to the exact result as fp32 products, at a third to a half of the speed.
  *
  * Coefficients: the singular values entering each step must stay below 1.97, |b x^2 + c x^4| and
  * |a + b x^2 + c x^4| at most 60 (checked on the host by following the polynomial from [0, 1]);
@@ -370,8 +370,8 @@ typedef struct psgd_ns_matrix {
 typedef struct psgd_ns_plan psgd_ns_plan;
 
 /* Describe a group orthogonalised in grouped launches. Allocates the plan's workspace (8 bytes per
- * element of the matrices padded to whole tiles plus 4 per element of s x s, 8 when accurate) and
- * uploads the tables (synchronously). The pointers are captured. One plan runs one call at a time. */
+ * element of the matrices padded to whole tiles, 4 per element of s x s, 8 when accurate, and the
+ * partial sums of products that are split) and uploads the tables (synchronously). The pointers are captured. One plan runs one call at a time. */
 psgd_status psgd_ns_plan_create(psgd_ctx* ctx, const psgd_ns_matrix* mats, int n_mats, psgd_dtype in_dtype,
                                 psgd_dtype out_dtype, psgd_ns_precision precision, psgd_ns_plan** plan);
 

@@ -179,7 +179,7 @@ __device__ __forceinline__ void sort_range(const EmbedGrad& a, SortMem& m, int64
 // Short batches, one launch: the workgroup of a range reads all tokens (a few bytes each, from L2),
 // counts those below its range, which is where its part of the order begins, and keeps its own.
 // No workgroup waits for another. The time grows with n for every workgroup: 14 us at 20480 tokens
-// and 34 at 65537, where the three launches below take 15 and 17.
+// and 34 at 65537, where the three launches below take 17 and 20.
 template <int ID>
 __global__ __launch_bounds__(SO_THREADS)
 void k_embed_sort(EmbedGrad a)

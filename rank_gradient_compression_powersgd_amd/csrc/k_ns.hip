@@ -8,7 +8,7 @@
 //
 // Both are bound by HBM: fp32 Muon reads 8 and writes 4 bytes per element, then reads 8 and
 // writes 4. A second pass over U is what the norm costs: no scale is known before the whole
-// matrix has been read.
+// matrix has been read. Four resblock shards (9.4e7 elements): 208 us and 246 us, 5.4 and 4.6 TB/s.
 #include "ns.h"
 
 namespace psgd {

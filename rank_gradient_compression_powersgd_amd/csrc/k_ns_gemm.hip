@@ -12,6 +12,12 @@
 // directions it lacks, which every step then multiplies by a = 3.4 (an update of rank 112 came
 // out 3% off, against 0.15%). The accurate products use both halves of every factor
 // (hi hi + hi lo + lo hi): the result agrees with fp32 products.
+//
+// Measured. Four resblock shards (s 496..1984, l 3968), fast: A 181 us, B 106, update 350; the
+// unsharded resblock (s 3968, l up to 15872): A 596, B 243, update 1256, 1.2 PFLOP/s.
+// One resblock shard, accurate: A 135, B 75, update 255. Large groups run at the chip's power limit,
+// 82% of what a large library product reaches; small ones (496 x 3968: 5 to 8 us a launch) wait for
+// their first loads.
 #include <type_traits>
 
 #include "ns.h"

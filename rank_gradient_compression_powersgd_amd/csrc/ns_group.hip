@@ -57,7 +57,7 @@ double makespan(std::vector<double> cost) {
 // The list in the order xcd_remap deals it out: XCD x walks the x-th eighth, padded to the longest.
 // Items of one cost are dealt to the XCDs in contiguous runs, since neighbours share operand rows in
 // an XCD's L2, as many to each as evens out the XCDs' work; longer items come first. (Four
-// resblocks' A: runs 192 us, item by item to the first free CU 222 us, where half of the XCDs had
+// resblocks' A, row-major: runs 192 us, item by item to the first free CU 222 us, where half of the XCDs had
 // all of the second round.)
 std::vector<Work> spread(const std::vector<Item>& items) {
   std::vector<int> idx(items.size());
