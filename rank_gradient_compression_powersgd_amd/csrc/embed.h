@@ -8,7 +8,7 @@ namespace psgd {
 constexpr int kEmbedRange = 512;        // most ids one sorting workgroup takes
 constexpr int kEmbedRanges = 512;       // most ranges the three-launch sort deals tokens to
 constexpr int64_t kEmbedShort = 24576;  // longest batch sorted by one launch
-constexpr int kEmbedChunk = 32;         // sorted tokens per summing workgroup
+constexpr int kEmbedChunk = 32;         // sorted tokens per summing workgroup, at most
 constexpr int kEmbedZeroRows = 16;      // table rows per workgroup that clears absent tokens
 
 struct EmbedLookup {
@@ -36,6 +36,7 @@ struct EmbedGrad {
   float* partial; int64_t ld_partial;   // 2 chunks rows of partial sums
 };
 
+int embed_chunk(int64_t n, int64_t dim);
 int64_t embed_range(int64_t vocab);
 int64_t embed_tokens(int64_t n, int64_t vocab);
 hipError_t launch_embed_lookup(const EmbedLookup& a, int tt, int ot, int id_bytes, hipStream_t s);

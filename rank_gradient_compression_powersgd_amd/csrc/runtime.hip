@@ -1250,7 +1250,8 @@ psgd_status check_embed(psgd_ctx* ctx, const void* ids, psgd_itype it, int64_t n
 struct EmbedLayout { int64_t chunks, tokens, list, sorted, seg, count, start, partial, ld_partial, bytes; };
 EmbedLayout embed_layout(int64_t n, int64_t vocab, int64_t dim) {
   EmbedLayout L{};
-  L.chunks = (n + psgd::kEmbedChunk - 1) / psgd::kEmbedChunk;
+  const int chunk = psgd::embed_chunk(n, dim);
+  L.chunks = (n + chunk - 1) / chunk;
   L.tokens = psgd::embed_tokens(n, vocab);
   const int64_t range = psgd::embed_range(vocab), ranges = (vocab + range - 1) / range;
   L.list = 0;
@@ -1314,7 +1315,7 @@ psgd_status psgd_embed_grad(psgd_ctx* ctx, const void* dx, int64_t ld_dx, psgd_d
   a.dx = dx; a.ld_dx = ld_dx; a.ids = ids; a.n = n; a.vocab = vocab; a.dim = dim;
   a.dtable = dtable; a.ld_dtable = ld_dtable; a.scale = scale; a.accumulate = accumulate != 0;
   a.range = psgd::embed_range(vocab);
-  a.chunk = psgd::kEmbedChunk; a.chunks = L.chunks;
+  a.chunk = psgd::embed_chunk(n, dim); a.chunks = L.chunks;
   a.tokens = L.tokens;
   a.list = reinterpret_cast<uint64_t*>(ws + L.list);
   a.sorted = reinterpret_cast<uint64_t*>(ws + L.sorted);
