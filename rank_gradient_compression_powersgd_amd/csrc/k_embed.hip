@@ -307,7 +307,7 @@ void k_embed_order(EmbedGrad a)
 }
 
 // ---- the sums ------------------------------------------------------------------------------
-constexpr int SU_THREADS = 256, SU_UNROLL = 8, JO_UNROLL = 16;
+constexpr int SU_THREADS = 256, SU_UNROLL = 8, JO_UNROLL = 16, JO_WAYS = 4;
 
 // blockIdx.x < chunks: one chunk of the sorted order; blockIdx.y: blockDim.x V columns. A token
 // whose tokens all lie in the chunk is finished here; a token that goes on into the next chunk or
@@ -381,12 +381,17 @@ void k_embed_sum(EmbedGrad a)
   }
 }
 
-// A token that begins in chunk blockIdx.x and goes on: its partial rows, added in order.
+// A token that begins in chunk blockIdx.x and goes on: its partial rows, added in order by the rows of
+// threads (threadIdx.y), each a share of them, whose sums are then added in order: a token that is
+// a tenth of the batch has hundreds. Four rows of threads where one workgroup holds all columns (65536 x
+// 64: 56 us in all, one row 63), one where they are spread over several anyway and most of the
+// extra waves would only start and end (65536 x 3968: 386 us, four rows 412).
 template <int V>
-__global__ __launch_bounds__(SU_THREADS)
+__global__ __launch_bounds__(SU_THREADS * JO_WAYS)
 void k_embed_join(EmbedGrad a)
 {
   typedef typename Vec<G_F32, V>::f vf;
+  __shared__ vf sums[JO_WAYS - 1][SU_THREADS];
   const int32_t total = gbl(a.seg)[a.vocab];
   const int64_t j = blockIdx.x, p0 = j * a.chunk, p1 = p0 + a.chunk;
   if (p1 >= total) return;
@@ -394,19 +399,28 @@ void k_embed_join(EmbedGrad a)
   const int32_t s0 = gbl(a.seg)[v], s1 = gbl(a.seg)[(int64_t)v + 1];
   if (s0 < p0 || s1 <= p1) return;
   const int64_t col = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * V;
-  if (col >= a.dim) return;
-  vf acc = Vec<G_F32, V>::load(a.partial, (2 * j + 1) * a.ld_partial + col);
+  const bool in = col < a.dim;
   const int64_t je = (s1 - 1) / a.chunk;
-  for (int64_t k0 = j + 1; k0 <= je; k0 += JO_UNROLL) {       // a batch of loads at a time, the last one too
-    vf x[JO_UNROLL];
+  const int ways = blockDim.y;
+  const int64_t share = max((int64_t)JO_UNROLL, (je - j + ways - 1) / ways);
+  const int64_t first = j + 1 + threadIdx.y * share, last = min(first + share - 1, je);
+  vf acc = 0.0f;
+  if (in && threadIdx.y == 0) acc = Vec<G_F32, V>::load(a.partial, (2 * j + 1) * a.ld_partial + col);
+  if (in)
+    for (int64_t k0 = first; k0 <= last; k0 += JO_UNROLL) {    // a batch of loads at a time, the last one too
+      vf x[JO_UNROLL];
 #pragma unroll
-    for (int u = 0; u < JO_UNROLL; ++u) {
-      x[u] = 0.0f;
-      if (k0 + u <= je) x[u] = Vec<G_F32, V>::load(a.partial, 2 * (k0 + u) * a.ld_partial + col);
+      for (int u = 0; u < JO_UNROLL; ++u) {
+        x[u] = 0.0f;
+        if (k0 + u <= last) x[u] = Vec<G_F32, V>::load(a.partial, 2 * (k0 + u) * a.ld_partial + col);
+      }
+#pragma unroll
+      for (int u = 0; u < JO_UNROLL; ++u) acc += x[u];
     }
-#pragma unroll
-    for (int u = 0; u < JO_UNROLL; ++u) acc += x[u];
-  }
+  if (threadIdx.y > 0) sums[threadIdx.y - 1][threadIdx.x] = acc;
+  __syncthreads();
+  if (!in || threadIdx.y > 0) return;
+  for (int w = 1; w < ways && j + 1 + w * share <= je; ++w) acc += sums[w - 1][threadIdx.x];
   const int64_t o = (int64_t)v * a.ld_dtable + col;
   vf r = a.scale * acc;
   if (a.accumulate) r = Vec<G_F32, V>::load(a.dtable, o) + r;
@@ -454,7 +468,7 @@ template <int T, int V> hipError_t grad_sum(const EmbedGrad& a, hipStream_t s) {
   if (const hipError_t e = hipGetLastError(); e != hipSuccess || a.chunks < 2) return e;
   constexpr int VJ = V == 1 ? 1 : 4;
   const Cols j = cols_of(a.dim, VJ);
-  k_embed_join<VJ><<<dim3((unsigned)(a.chunks - 1), j.blocks), dim3(j.threads), 0, s>>>(a);
+  k_embed_join<VJ><<<dim3((unsigned)(a.chunks - 1), j.blocks), dim3(j.threads, j.blocks == 1 ? JO_WAYS : 1), 0, s>>>(a);
   return hipGetLastError();
 }
 template <int T> hipError_t grad_vec(const EmbedGrad& a, hipStream_t s) {
