@@ -433,7 +433,8 @@ psgd_status psgd_muon_update(psgd_ctx* ctx, psgd_plan* plan, const int32_t* skip
  * 1 <= vocab < 2^31 in the lookup and <= 2^20 in the gradient, 1 <= dim <= 2^23. Outputs must not
  * overlap inputs.
  *   workspace: psgd_embed_grad_workspace(n, vocab, dim) bytes of device memory, 16-byte aligned,
- *     contents ignored and overwritten; calls that may overlap need one each.
+ *     contents ignored and overwritten; one for n tokens serves fewer of the same table; calls that
+ *     may overlap need one each.
  * Asynchronous on stream; no plan involved, no allocation.
  */
 typedef enum psgd_itype { PSGD_I32 = 4, PSGD_I64 = 8 } psgd_itype;

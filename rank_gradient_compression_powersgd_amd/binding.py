@@ -546,7 +546,7 @@ def psgd_embed_lookup(ctx: int, table, ids, out, scale: float = 1.0, stream=None
 
 
 def psgd_embed_grad_workspace(n: int, vocab: int, dim: int) -> int:
-    """Bytes of device workspace of psgd_embed_grad for n tokens."""
+    """Bytes of device workspace of psgd_embed_grad for up to n tokens."""
     out = ctypes.c_int64()
     _check(None, "psgd_embed_grad_workspace", load_library().psgd_embed_grad_workspace(n, vocab, dim, ctypes.byref(out)))
     return out.value

@@ -37,6 +37,8 @@ struct EmbedGrad {
 };
 
 int embed_chunk(int64_t n, int64_t dim);
+int64_t embed_max_chunks(int64_t n, int64_t dim);
+int64_t embed_max_shares(int64_t n, int64_t vocab);
 int64_t embed_range(int64_t vocab);
 int64_t embed_tokens(int64_t n, int64_t vocab);
 hipError_t launch_embed_lookup(const EmbedLookup& a, int tt, int ot, int id_bytes, hipStream_t s);

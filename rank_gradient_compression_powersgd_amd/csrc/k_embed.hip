@@ -10,6 +10,8 @@
 // fp32, with no atomics on data: the tokens are sorted stably first, then fixed chunks of the
 // sorted order are summed, so the result is the same bits on every run and a token that fills
 // half the batch is spread over the chip like any other.
+#include <algorithm>
+
 #include "embed.h"
 
 namespace psgd {
@@ -517,7 +519,17 @@ hipError_t launch_embed_grad(const EmbedGrad& a, int dt, int id_bytes, hipStream
 // Sorted tokens per summing workgroup: 32, or one batch of loads where all rows together are few (333
 // x 1000: 13 us instead of 19, 4096 x 1000: 19 instead of 22; 8192 x 1000: 31 instead of 27) and a
 // frequent token does not leave too many partial rows (65536 x 24: 84 us instead of 64).
-int embed_chunk(int64_t n, int64_t dim) { return n <= 8192 && n * dim <= 1 << 22 ? SU_UNROLL : kEmbedChunk; }
+constexpr int64_t kFewTokens = 8192, kFewElements = 1 << 22;
+int embed_chunk(int64_t n, int64_t dim) { return n <= kFewTokens && n * dim <= kFewElements ? SU_UNROLL : kEmbedChunk; }
+// Most chunks of a batch of up to n tokens, and most shares of the three-launch sort: a workspace for n
+// tokens has to serve fewer.
+int64_t embed_max_chunks(int64_t n, int64_t dim) {
+  const int64_t few = std::min({n, kFewTokens, kFewElements / dim});
+  return std::max((n + kEmbedChunk - 1) / kEmbedChunk, (few + SU_UNROLL - 1) / SU_UNROLL);
+}
+int64_t embed_max_shares(int64_t n, int64_t vocab) {
+  return embed_tokens(n, vocab) == 0 ? 0 : std::min<int64_t>(128, (n + 2047) / 2048);
+}
 // Ids per sorting workgroup: enough workgroups for the chip, at most the counters' room.
 int64_t embed_range(int64_t vocab) {
   const int64_t r = (vocab + 255) / 256;

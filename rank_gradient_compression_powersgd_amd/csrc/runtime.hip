@@ -1258,10 +1258,10 @@ EmbedLayout embed_layout(int64_t n, int64_t vocab, int64_t dim) {
   L.sorted = L.list + rup(8 * n, 256);
   L.seg = L.sorted + rup(8 * n, 256);
   L.count = L.seg + rup(4 * (vocab + 1), 256);
-  L.start = L.count + (L.tokens ? rup(4 * ranges * ((n + L.tokens - 1) / L.tokens), 256) : 0);
+  L.start = L.count + rup(4 * ranges * psgd::embed_max_shares(n, vocab), 256);
   L.partial = L.start + (L.tokens ? rup(4 * (ranges + 1), 256) : 0);
   L.ld_partial = rup(dim, 4);
-  L.bytes = L.partial + 8 * L.chunks * L.ld_partial;
+  L.bytes = L.partial + 8 * psgd::embed_max_chunks(n, dim) * L.ld_partial;
   return L;
 }
 }  // namespace

@@ -61,6 +61,14 @@ def test_workspace_grows_past_32_bits():
     assert B.psgd_embed_grad_workspace(2 ** 25, 2 ** 20, 2 ** 14) > 2 ** 36
 
 
+@pytest.mark.parametrize("vocab,dim", [(1, 1), (1031, 1000), (8195, 24), (32768, 3968), (262144, 7), (2 ** 20, 64)])
+def test_a_workspace_serves_shorter_batches(vocab, dim):
+    ns = sorted({max(0, x + d) for x in [0, 8, 32, 1000, 4096, 8192, 24576, 65536, 262144, 300000, 2 ** 22] + [(1 << 22) // dim] if x < 2 ** 24
+                 for d in (-33, -1, 0, 1, 2, 31, 127, 129)})
+    sizes = [B.psgd_embed_grad_workspace(n, vocab, dim) for n in ns]
+    assert sizes == sorted(sizes), [(n, s) for n, s in zip(ns, sizes)]
+
+
 def test_newton_schulz_binding_checks():
     from rank_gradient_compression_powersgd_amd import NewtonSchulzGroup
     f32, f16 = torch.zeros(4, 6), torch.zeros(4, 6, dtype=torch.float16)
