@@ -38,7 +38,7 @@ template <int IT>
 __global__ __launch_bounds__(kThreads)
 void k_ns_norm(const NsMat* __restrict__ mats, const Work* __restrict__ work, NsArgs a)
 {
-  if (a.skip && *a.skip != 0) return;
+  if (*a.skip != 0) return;
   const Work wi = work[blockIdx.x];
   const NsMat& d = mats[wi.mat];
   const int n = d.n, r0 = wi.a, rows = min(d.part_rows, d.m - r0);
@@ -118,7 +118,7 @@ template <int IT>
 __global__ __launch_bounds__(kThreads)
 void k_ns_x0(const NsMat* __restrict__ mats, const Work* __restrict__ work, NsArgs a)
 {
-  if (a.skip && *a.skip != 0) return;
+  if (*a.skip != 0) return;
   const Work wi = work[blockIdx.x];
   const NsMat& d = mats[wi.mat];
   __shared__ double red[kThreads];

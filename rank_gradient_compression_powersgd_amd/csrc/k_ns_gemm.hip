@@ -110,16 +110,13 @@ template <int T> struct Tile {
 // ... in order and runs the epilogue, each wave of the tile as a workgroup of its own.
 template <int ST, int T, bool ACC, int OT, bool REDUCE>
 __global__ __launch_bounds__(REDUCE ? kWave : Tile<T>::THREADS, 2)
-void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, float* __restrict__ partial, int step,
-               NsArgs na)
+void k_ns_gemm(const NsItem* __restrict__ items, float* __restrict__ partial, int step, NsArgs na)
 {
-  if (na.skip && *na.skip != 0) return;
   using TL = Tile<T>;
   constexpr int PER = REDUCE ? TL::WAVES : 1;  // workgroups per item: the sums' waves are on their own
   const int item = xcd_remap(blockIdx.x, gridDim.x);
-  const Work wi = work[item / PER];
-  if (wi.mat < 0) return;
-  const NsMat& d = mats[wi.mat];
+  const Work wi = items[item / PER].w;
+  const NsMat& d = items[item / PER].d;
   constexpr bool OUTER = ST == NS_UPDATE;      // P is read K-outer
   const int cur = step & 1;
   const int i0 = wi.a & ~63, j0 = wi.b & ~63, split = wi.a & 63, splits = wi.b & 63;
@@ -139,6 +136,10 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
   }
   const int K = ST == NS_GRAM ? d.l : d.s;
   const int64_t panel = (int64_t)d.sp * KB;    // elements from one panel of 32 columns to the next
+  const int skip = *na.skip;
+  // all of these loads are under way together before the first is looked at
+  asm volatile("" ::"s"(ph), "s"(pl), "s"(qh), "s"(ql), "s"(K), "s"(panel), "s"(skip), "s"(wi.mat));
+  if (skip != 0 || wi.mat < 0) return;
   // whole pairs of 32 k (the padding up to a tile holds zeros); accurate: two stages per 32 k
   int nst = ns_stages(K, ACC);
   int k0 = 0;                                  // first k of this part
@@ -608,7 +609,7 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
             f32x4 v = *reinterpret_cast<const f32x4*>(&regf[r * cols + 4 * (u ^ (r & (units - 1)))]);
             const int64_t o = (int64_t)row * d.ld_out + col;
             if (vec) {
-              if (na.muon) v = th[y] - na.lr * (d.factor * v + na.weight_decay * th[y]);
+              if (na.muon) v = th[y] - na.lr * (d.factor[na.adjust] * v + na.weight_decay * th[y]);
               out_store4<OT>(d.out, o, v);
             } else {
 #pragma unroll
@@ -617,7 +618,7 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
                 float w = v[t];
                 if (na.muon) {
                   const float one = out_load<OT>(d.out, o + t);
-                  w = one - na.lr * (d.factor * w + na.weight_decay * one);
+                  w = one - na.lr * (d.factor[na.adjust] * w + na.weight_decay * one);
                 }
                 out_store<OT>(d.out, o + t, w);
               }
@@ -630,36 +631,36 @@ void k_ns_gemm(const NsMat* __restrict__ mats, const Work* __restrict__ work, fl
 }
 
 template <int ST, int T, bool ACC, int OT, bool REDUCE = false>
-void go(const NsList& l, const NsMat* mats, int step, const NsArgs& a, hipStream_t s) {
+void go(const NsList& l, int step, const NsArgs& a, hipStream_t s) {
   k_ns_gemm<ST, T, ACC, OT, REDUCE><<<dim3(REDUCE ? l.n_reduce * Tile<T>::WAVES : l.n_work), dim3(REDUCE ? kWave : Tile<T>::THREADS), 0, s>>>(
-      mats, REDUCE ? l.reduce : l.work, l.partial, step, a);
+      REDUCE ? l.reduce : l.work, l.partial, step, a);
 }
 template <int ST, int T, bool ACC>
-void go_split(const NsList& l, const NsMat* mats, int step, const NsArgs& a, hipStream_t s) {
-  go<ST, T, ACC, 0>(l, mats, step, a, s);
-  if (l.n_reduce > 0) go<ST, T, ACC, 0, true>(l, mats, step, a, s);
+void go_split(const NsList& l, int step, const NsArgs& a, hipStream_t s) {
+  go<ST, T, ACC, 0>(l, step, a, s);
+  if (l.n_reduce > 0) go<ST, T, ACC, 0, true>(l, step, a, s);
 }
 template <int T, bool ACC>
-hipError_t pick(NsStage st, int ot, bool last, const NsList& l, const NsMat* mats, int step, const NsArgs& a, hipStream_t s) {
-  if (st == NS_GRAM) go_split<NS_GRAM, T, ACC>(l, mats, step, a, s);
-  else if (st == NS_POLY) go_split<NS_POLY, T, ACC>(l, mats, step, a, s);
-  else if (!last) go<NS_UPDATE, T, ACC, 0>(l, mats, step, a, s);
-  else if (ot == G_F32) go<NS_UPDATE, T, ACC, G_F32>(l, mats, step, a, s);
-  else if (ot == G_F16) go<NS_UPDATE, T, ACC, G_F16>(l, mats, step, a, s);
-  else if (ot == G_BF16) go<NS_UPDATE, T, ACC, G_BF16>(l, mats, step, a, s);
+hipError_t pick(NsStage st, int ot, bool last, const NsList& l, int step, const NsArgs& a, hipStream_t s) {
+  if (st == NS_GRAM) go_split<NS_GRAM, T, ACC>(l, step, a, s);
+  else if (st == NS_POLY) go_split<NS_POLY, T, ACC>(l, step, a, s);
+  else if (!last) go<NS_UPDATE, T, ACC, 0>(l, step, a, s);
+  else if (ot == G_F32) go<NS_UPDATE, T, ACC, G_F32>(l, step, a, s);
+  else if (ot == G_F16) go<NS_UPDATE, T, ACC, G_F16>(l, step, a, s);
+  else if (ot == G_BF16) go<NS_UPDATE, T, ACC, G_BF16>(l, step, a, s);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_ns_gemm(NsStage st, bool accurate, int ot, bool last, const NsList& l, const NsMat* mats, int step,
+hipError_t launch_ns_gemm(NsStage st, bool accurate, int ot, bool last, const NsList& l, int step,
                           const NsArgs& a, hipStream_t s) {
   if (l.tile == 256)
-    return accurate ? hipErrorInvalidValue : pick<256, false>(st, ot, last, l, mats, step, a, s);
+    return accurate ? hipErrorInvalidValue : pick<256, false>(st, ot, last, l, step, a, s);
   if (l.tile == 128)
-    return accurate ? pick<128, true>(st, ot, last, l, mats, step, a, s) : pick<128, false>(st, ot, last, l, mats, step, a, s);
-  return accurate ? pick<64, true>(st, ot, last, l, mats, step, a, s) : pick<64, false>(st, ot, last, l, mats, step, a, s);
+    return accurate ? pick<128, true>(st, ot, last, l, step, a, s) : pick<128, false>(st, ot, last, l, step, a, s);
+  return accurate ? pick<64, true>(st, ot, last, l, step, a, s) : pick<64, false>(st, ot, last, l, step, a, s);
 }
 
 }  // namespace psgd

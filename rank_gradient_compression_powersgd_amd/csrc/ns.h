@@ -30,7 +30,7 @@ struct NsMat {
   int32_t s, l, sp, lp;
   int32_t flip;                          // 1: X holds the transposed update (m > n)
   int32_t parts, part_rows;              // partial sums of squares: rows per part
-  float factor;                          // Muon: scale of the orthogonal update
+  float factor[2];                       // Muon: scale of the orthogonal update, by NsArgs::adjust
   uint16_t* xh[2];   uint16_t* xl[2];    // X, ping-pong between steps
   uint16_t* ah;      uint16_t* al;       // A (lo: accurate products only)
   uint16_t* bh;      uint16_t* bl;       // B likewise
@@ -43,10 +43,17 @@ struct NsArgs {
   double eps;
   int steps;
   // Muon (mu unused otherwise)
-  int muon, nesterov;
+  int muon, nesterov, adjust;
   float lr, mu, weight_decay;
-  const int32_t* skip;                   // NULL: never skipped
+  const int32_t* skip;                   // the step's skip word (NULL, up to NsGroup::run: never skipped)
   const float* norm;                     // norm[1] = clipping factor; NULL: 1
+};
+
+// An item of a product list: its tile, and a copy of its matrix, so that a workgroup waits for one
+// load and not for two in a row before it can ask for its operands.
+struct NsItem {
+  Work w;
+  NsMat d;
 };
 
 // Elements of the update as they enter the iteration and of the result as they leave it.
@@ -59,8 +66,8 @@ hipError_t launch_ns_x0(int it, const NsMat* mats, const Work* work, int n_work,
 // part of a tile whose K is split and the number of parts (0: not split).
 struct NsList {
   int tile = 0;
-  const Work* work = nullptr;   int n_work = 0;
-  const Work* reduce = nullptr; int n_reduce = 0;    // the split tiles, with their first slot
+  const NsItem* work = nullptr;   int n_work = 0;
+  const NsItem* reduce = nullptr; int n_reduce = 0;    // the split tiles, with their first slot
   float* partial = nullptr;                          // tile * tile floats per slot
 };
 // Stages of 32 k a product over K takes (accurate: the hi and the lo plane each), always even, and
@@ -71,7 +78,7 @@ __host__ __device__ inline int ns_part(int stages, int splits, bool accurate) {
   return ((stages + splits - 1) / splits + unit - 1) / unit * unit;
 }
 // One product stage of step `step` (0-based); `last` writes the caller's output.
-hipError_t launch_ns_gemm(NsStage st, bool accurate, int ot, bool last, const NsList& l, const NsMat* mats, int step,
+hipError_t launch_ns_gemm(NsStage st, bool accurate, int ot, bool last, const NsList& l, int step,
                           const NsArgs& a, hipStream_t s);
 
 // A group of matrices orthogonalised together: validated by the caller, laid out and allocated
@@ -91,7 +98,8 @@ class NsGroup {
   struct List { int off = 0, cnt = 0; };
   void* buf_ = nullptr;                  // workspace, descriptors (one table per adjust), work lists
   size_t bytes_ = 0;
-  NsMat* d_mats_[2] = {nullptr, nullptr};
+  NsMat* d_mats_ = nullptr;
+  int32_t* d_zero_ = nullptr;            // a skip word for calls that have none
   Work* d_work_ = nullptr;
   List norm_, x0_;
   NsList gram_, poly_, update_;

@@ -235,60 +235,68 @@ hipError_t NsGroup::create(const std::vector<Item>& items, int in_type, int out_
     for (int a = 0; a < mats[i].sp; a += xt)
       for (int b = 0; b < mats[i].lp; b += xt) w.push_back(Work{i, a, b, 0});
   add(x0_, w);
-  List lists[3], reduces[3];
-  for (int k = 0; k < 3; ++k) {
-    add(lists[k], plan[k].work);
-    add(reduces[k], plan[k].reduce);
-  }
-
-  const size_t mat_bytes = (sizeof(NsMat) * n + 255) / 256 * 256;
-  const size_t work_off = ws + 2 * mat_bytes;
-  bytes_ = work_off + sizeof(Work) * all.size();
+  size_t n_items = 0;
+  for (const Planned& p : plan) n_items += p.work.size() + p.reduce.size();
+  const size_t mats_off = take(sizeof(NsMat) * n), work_off = take(sizeof(Work) * all.size()), zero_off = take(sizeof(int32_t)),
+               items_off = take(sizeof(NsItem) * n_items);
+  bytes_ = ws;
   hipError_t e = hipMalloc(&buf_, bytes_);
   if (e != hipSuccess) { buf_ = nullptr; return hipErrorOutOfMemory; }
   char* base = static_cast<char*>(buf_);
+  d_mats_ = reinterpret_cast<NsMat*>(base + mats_off);
   d_work_ = reinterpret_cast<Work*>(base + work_off);
+  d_zero_ = reinterpret_cast<int32_t*>(base + zero_off);
+  for (int i = 0; i < n; ++i) {
+    NsMat& d = mats[i];
+    const Off& o = offs[i];
+    for (int k = 0; k < 2; ++k) {
+      d.xh[k] = reinterpret_cast<uint16_t*>(base + o.xh[k]);
+      d.xl[k] = reinterpret_cast<uint16_t*>(base + o.xl[k]);
+    }
+    d.ah = reinterpret_cast<uint16_t*>(base + o.ah);
+    d.bh = reinterpret_cast<uint16_t*>(base + o.bh);
+    d.al = accurate ? reinterpret_cast<uint16_t*>(base + o.al) : nullptr;
+    d.bl = accurate ? reinterpret_cast<uint16_t*>(base + o.bl) : nullptr;
+    d.partial = reinterpret_cast<double*>(base + o.partial);
+    d.factor[0] = (float)std::sqrt(std::max(1.0, (double)d.m / d.n));
+    d.factor[1] = (float)(0.2 * std::sqrt((double)std::max(d.m, d.n)));
+  }
+  std::vector<NsItem> items_h;
+  items_h.reserve(n_items);
+  NsItem* const d_items = reinterpret_cast<NsItem*>(base + items_off);
+  auto put = [&](const std::vector<Work>& list) {
+    const NsItem* at = d_items + items_h.size();
+    for (const Work& x : list) items_h.push_back(NsItem{x, mats[std::max(x.mat, 0)]});
+    return at;
+  };
   NsList* const out[3] = {&gram_, &poly_, &update_};
   for (int k = 0; k < 3; ++k) {
     out[k]->tile = plan[k].tile;
-    out[k]->work = d_work_ + lists[k].off;
-    out[k]->n_work = lists[k].cnt;
-    out[k]->reduce = d_work_ + reduces[k].off;
-    out[k]->n_reduce = reduces[k].cnt;
+    out[k]->work = put(plan[k].work);
+    out[k]->n_work = (int)plan[k].work.size();
+    out[k]->reduce = put(plan[k].reduce);
+    out[k]->n_reduce = (int)plan[k].reduce.size();
     out[k]->partial = reinterpret_cast<float*>(base + slots_off);
   }
-  for (int adj = 0; adj < 2; ++adj) {
-    d_mats_[adj] = reinterpret_cast<NsMat*>(base + ws + adj * mat_bytes);
-    for (int i = 0; i < n; ++i) {
-      NsMat& d = mats[i];
-      const Off& o = offs[i];
-      for (int k = 0; k < 2; ++k) {
-        d.xh[k] = reinterpret_cast<uint16_t*>(base + o.xh[k]);
-        d.xl[k] = reinterpret_cast<uint16_t*>(base + o.xl[k]);
-      }
-      d.ah = reinterpret_cast<uint16_t*>(base + o.ah);
-      d.bh = reinterpret_cast<uint16_t*>(base + o.bh);
-      d.al = accurate ? reinterpret_cast<uint16_t*>(base + o.al) : nullptr;
-      d.bl = accurate ? reinterpret_cast<uint16_t*>(base + o.bl) : nullptr;
-      d.partial = reinterpret_cast<double*>(base + o.partial);
-      d.factor = adj == 0 ? (float)std::sqrt(std::max(1.0, (double)d.m / d.n))
-                          : (float)(0.2 * std::sqrt((double)std::max(d.m, d.n)));
-    }
-    if ((e = hipMemcpy(d_mats_[adj], mats.data(), sizeof(NsMat) * n, hipMemcpyHostToDevice)) != hipSuccess) return e;
-  }
+  const int32_t zero = 0;
+  if ((e = hipMemcpy(d_mats_, mats.data(), sizeof(NsMat) * n, hipMemcpyHostToDevice)) != hipSuccess) return e;
   if ((e = hipMemcpy(d_work_, all.data(), sizeof(Work) * all.size(), hipMemcpyHostToDevice)) != hipSuccess) return e;
+  if ((e = hipMemcpy(d_zero_, &zero, sizeof zero, hipMemcpyHostToDevice)) != hipSuccess) return e;
+  if ((e = hipMemcpy(d_items, items_h.data(), sizeof(NsItem) * n_items, hipMemcpyHostToDevice)) != hipSuccess) return e;
   return hipDeviceSynchronize();
 }
 
-hipError_t NsGroup::run(const NsArgs& a, int adjust, hipStream_t s) {
-  const NsMat* dm = d_mats_[adjust];
+hipError_t NsGroup::run(const NsArgs& args, int adjust, hipStream_t s) {
+  NsArgs a = args;
+  a.adjust = adjust;
+  if (!a.skip) a.skip = d_zero_;
   auto W = [&](const List& l) { return d_work_ + l.off; };
-  hipError_t e = launch_ns_norm(it_, dm, W(norm_), norm_.cnt, a, s);
-  if (e == hipSuccess) e = launch_ns_x0(it_, dm, W(x0_), x0_.cnt, a, s);
+  hipError_t e = launch_ns_norm(it_, d_mats_, W(norm_), norm_.cnt, a, s);
+  if (e == hipSuccess) e = launch_ns_x0(it_, d_mats_, W(x0_), x0_.cnt, a, s);
   for (int k = 0; k < a.steps && e == hipSuccess; ++k) {
-    e = launch_ns_gemm(NS_GRAM, accurate_, ot_, false, gram_, dm, k, a, s);
-    if (e == hipSuccess) e = launch_ns_gemm(NS_POLY, accurate_, ot_, false, poly_, dm, k, a, s);
-    if (e == hipSuccess) e = launch_ns_gemm(NS_UPDATE, accurate_, ot_, k + 1 == a.steps, update_, dm, k, a, s);
+    e = launch_ns_gemm(NS_GRAM, accurate_, ot_, false, gram_, k, a, s);
+    if (e == hipSuccess) e = launch_ns_gemm(NS_POLY, accurate_, ot_, false, poly_, k, a, s);
+    if (e == hipSuccess) e = launch_ns_gemm(NS_UPDATE, accurate_, ot_, k + 1 == a.steps, update_, k, a, s);
   }
   return e;
 }
