@@ -7,6 +7,7 @@ import of this module's functions raises: there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Iterable, List, Optional, Sequence
 
@@ -456,21 +457,29 @@ def make_muon_matrix(param, momentum) -> psgd_muon_matrix:
 def _row_stride(t, call: str) -> int:
     """Leading dimension of a 2-D tensor whose rows are contiguous and do not overlap."""
     m, n = t.shape
-    if n > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if n > 1 and one != 1:
         raise PsgdError(call, PSGD_EINVAL, "tensors need unit stride along rows")
     if m <= 1:
         return max(n, 1)                     # one row: its stride is never used
-    if t.stride(0) < n:
+    if ld < n:
         raise PsgdError(call, PSGD_EINVAL, "the rows of a tensor must not overlap")
-    return t.stride(0)
+    return ld
+
+
+@functools.lru_cache(maxsize=None)
+def _codes():
+    """torch dtype -> code, of values and of ids."""
+    import torch
+    return ({torch.float16: PSGD_F16, torch.bfloat16: PSGD_BF16, torch.float32: PSGD_F32},
+            {torch.int32: PSGD_I32, torch.int64: PSGD_I64})
 
 
 def _dtype(t, call: str) -> int:
-    import torch
-    codes = {torch.float16: PSGD_F16, torch.bfloat16: PSGD_BF16, torch.float32: PSGD_F32}
-    if t.dtype not in codes:
+    code = _codes()[0].get(t.dtype)
+    if code is None:
         raise PsgdError(call, PSGD_EDTYPE, f"tensors must be float16, bfloat16 or float32, got {t.dtype}")
-    return codes[t.dtype]
+    return code
 
 
 def psgd_ns_plan_create(ctx: int, mats: Sequence[psgd_ns_matrix], in_dtype: int, out_dtype: int,
@@ -505,21 +514,23 @@ def psgd_muon_update(ctx: int, plan: int, skip_dev, norm_dev, hp: psgd_muon_hpar
 
 
 def _ids(ids, call: str):
-    import torch
-    codes = {torch.int32: PSGD_I32, torch.int64: PSGD_I64}
-    if ids.dtype not in codes:
+    code = _codes()[1].get(ids.dtype)
+    if code is None:
         raise PsgdError(call, PSGD_EDTYPE, f"ids must be int32 or int64, got {ids.dtype}")
     if not ids.is_contiguous():
         raise PsgdError(call, PSGD_EINVAL, "ids must be contiguous")
-    return codes[ids.dtype]
+    return code
 
 
 def _embed_rows(t, n: int, dim: int, name: str, call: str) -> int:
     """Row stride of a tensor that holds one row of dim values per token (2-D, or contiguous with
     the tokens spread over the leading dimensions)."""
-    if t.dim() < 2 or t.shape[-1] != dim or t.numel() != n * dim:
+    shape = t.shape
+    if shape == (n, dim):
+        return _row_stride(t, call)
+    if len(shape) < 2 or shape[-1] != dim or t.numel() != n * dim:
         raise PsgdError(call, PSGD_EINVAL, f"{name} must hold one row of {dim} values per token")
-    if t.dim() > 2:
+    if len(shape) > 2:
         if not t.is_contiguous():
             raise PsgdError(call, PSGD_EINVAL, f"{name} with more than two dimensions must be contiguous")
         return dim
@@ -527,7 +538,8 @@ def _embed_rows(t, n: int, dim: int, name: str, call: str) -> int:
 
 
 def _same_device(call: str, *tensors):
-    if len({t.device for t in tensors}) != 1 or not tensors[0].is_cuda:
+    device = tensors[0].device
+    if device.type != "cuda" or any(t.device != device for t in tensors):
         raise PsgdError(call, PSGD_EINVAL, "tensors must live on one GPU")
 
 
@@ -542,7 +554,7 @@ def psgd_embed_lookup(ctx: int, table, ids, out, scale: float = 1.0, stream=None
     _same_device(call, table, ids, out)
     _check(ctx, call, load_library().psgd_embed_lookup(
         ctx, _ptr(table), _row_stride(table, call), vocab, dim, _dtype(table, call), _ptr(ids), _ids(ids, call),
-        ids.numel(), float(scale), _ptr(out), ld_out, _dtype(out, call), _stream(stream, table.device)))
+        ids.numel(), float(scale), _ptr(out), ld_out, _dtype(out, call), _stream(stream, table.device.index)))
 
 
 def psgd_embed_grad_workspace(n: int, vocab: int, dim: int) -> int:
@@ -583,7 +595,7 @@ def psgd_embed_grad(ctx: int, dx, ids, dtable, scale: float = 1.0, accumulate: b
         raise PsgdError(call, PSGD_EINVAL, "workspace must be contiguous")
     _check(ctx, call, load_library().psgd_embed_grad(
         ctx, _ptr(dx), ld_dx, dt, _ptr(ids), it, n, vocab, dim, float(scale), _ptr(dtable), ld_dt, int(accumulate),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream, dtable.device)))
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream, dtable.device.index)))
 
 
 def psgd_last_error(ctx: int) -> str:
