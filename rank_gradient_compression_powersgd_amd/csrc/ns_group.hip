@@ -240,8 +240,8 @@ hipError_t NsGroup::create(const std::vector<Item>& items, int in_type, int out_
   const size_t mats_off = take(sizeof(NsMat) * n), work_off = take(sizeof(Work) * all.size()), zero_off = take(sizeof(int32_t)),
                items_off = take(sizeof(NsItem) * n_items);
   bytes_ = ws;
-  hipError_t e = hipMalloc(&buf_, bytes_);
-  if (e != hipSuccess) { buf_ = nullptr; return hipErrorOutOfMemory; }
+  hipError_t e = device_alloc(&buf_, bytes_);
+  if (e != hipSuccess) return hipErrorOutOfMemory;
   char* base = static_cast<char*>(buf_);
   d_mats_ = reinterpret_cast<NsMat*>(base + mats_off);
   d_work_ = reinterpret_cast<Work*>(base + work_off);

@@ -23,6 +23,17 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 enum GradType : int { G_F16 = 1, G_BF16 = 2, G_F32 = 3 };
 
+// hipMalloc that leaves nothing behind when it fails: HIP keeps the last error of the thread, and
+// the next launch, which asks for it, would report the refused allocation as its own.
+inline hipError_t device_alloc(void** p, size_t bytes) {
+  const hipError_t e = hipMalloc(p, bytes);
+  if (e != hipSuccess) {
+    *p = nullptr;
+    (void)hipGetLastError();
+  }
+  return e;
+}
+
 // Pointers read out of the descriptor table are generic; accesses through them would compile
 // to FLAT instructions (which wait on both the vector-memory and the LDS counters). Every
 // kernel casts them to the global address space first so the compiler emits global_load /

@@ -113,6 +113,7 @@ psgd_status fail(psgd_ctx* ctx, psgd_status st, const char* fmt, ...) {
 }
 
 psgd_status hip_fail(psgd_ctx* ctx, hipError_t e, const char* what) {
+  (void)hipGetLastError();               // reported here: the next call's launches find none
   return fail(ctx, PSGD_EHIP, "%s: %s", what, hipGetErrorString(e));
 }
 
@@ -602,7 +603,7 @@ psgd_status psgd_plan_create(psgd_ctx* ctx, const psgd_matrix* mats, int n_mats,
 
   // ---- device allocations -----------------------------------------------------------------
   void* wsp = nullptr;
-  hipError_t e = hipMalloc(&wsp, ws ? ws : 256);
+  hipError_t e = psgd::device_alloc(&wsp, ws ? ws : 256);
   if (e != hipSuccess) return fail(ctx, PSGD_ENOMEM, "workspace of %zu bytes: %s", ws, hipGetErrorString(e));
   plan_bind(p.get(), static_cast<char*>(wsp), L);
   auto cleanup = [&]() {
@@ -616,9 +617,9 @@ psgd_status psgd_plan_create(psgd_ctx* ctx, const psgd_matrix* mats, int n_mats,
   if ((e = hipMemset(p->workspace, 0, ws ? ws : 256)) != hipSuccess) { cleanup(); return hip_fail(ctx, e, "workspace clear"); }
   const int32_t one = 1;
   if ((e = hipMemcpy(p->d_one, &one, sizeof one, hipMemcpyHostToDevice)) != hipSuccess) { cleanup(); return hip_fail(ctx, e, "constant upload"); }
-  if ((e = hipMalloc(&p->d_mats, sizeof(DevMat) * n_mats)) != hipSuccess) { cleanup(); return fail(ctx, PSGD_ENOMEM, "descriptor table"); }
+  if ((e = psgd::device_alloc(reinterpret_cast<void**>(&p->d_mats), sizeof(DevMat) * n_mats)) != hipSuccess) { cleanup(); return fail(ctx, PSGD_ENOMEM, "descriptor table"); }
   if ((e = hipMemcpy(p->d_mats, p->mats.data(), sizeof(DevMat) * n_mats, hipMemcpyHostToDevice)) != hipSuccess) { cleanup(); return hip_fail(ctx, e, "descriptor upload"); }
-  if ((e = hipMalloc(&p->d_work, sizeof(Work) * all.size())) != hipSuccess) { cleanup(); return fail(ctx, PSGD_ENOMEM, "work lists"); }
+  if ((e = psgd::device_alloc(reinterpret_cast<void**>(&p->d_work), sizeof(Work) * all.size())) != hipSuccess) { cleanup(); return fail(ctx, PSGD_ENOMEM, "work lists"); }
   if ((e = hipMemcpy(p->d_work, all.data(), sizeof(Work) * all.size(), hipMemcpyHostToDevice)) != hipSuccess) { cleanup(); return hip_fail(ctx, e, "work list upload"); }
   if ((e = hipDeviceSynchronize()) != hipSuccess) { cleanup(); return hip_fail(ctx, e, "plan upload"); }
   *plan_out = p.release();
@@ -934,7 +935,7 @@ psgd_status psgd_adam_attach(psgd_ctx* ctx, psgd_plan* plan, const psgd_adam_mat
   void* buf = nullptr;
   hipError_t e = hipDeviceSynchronize();        // no step of this plan may still be running
   if (e != hipSuccess) return hip_fail(ctx, e, "synchronise before attaching");
-  if ((e = hipMalloc(&buf, bytes)) != hipSuccess) return fail(ctx, PSGD_ENOMEM, "optimizer buffer of %zu bytes", bytes);
+  if ((e = psgd::device_alloc(&buf, bytes)) != hipSuccess) return fail(ctx, PSGD_ENOMEM, "optimizer buffer of %zu bytes", bytes);
   if ((e = hipMemcpy(buf, items.data(), items.size() * sizeof(psgd::NormItem), hipMemcpyHostToDevice)) != hipSuccess ||
       (e = hipMemcpy(plan->d_mats, mats.data(), sizeof(DevMat) * plan->n_mats, hipMemcpyHostToDevice)) != hipSuccess ||
       (e = hipDeviceSynchronize()) != hipSuccess) {
@@ -1188,7 +1189,7 @@ psgd_status psgd_muon_attach(psgd_ctx* ctx, psgd_plan* plan, const psgd_muon_mat
     const size_t items_bytes = (size_t)rup((int64_t)((norm.size() + kMaxPassItems) * sizeof(psgd::NormItem)), 256);
     const size_t bytes = items_bytes + (norm.size() + kMaxPassItems) * sizeof(double);
     void* buf = nullptr;
-    if (hipMalloc(&buf, bytes) != hipSuccess) return fail(ctx, PSGD_ENOMEM, "optimizer buffer of %zu bytes", bytes);
+    if (psgd::device_alloc(&buf, bytes) != hipSuccess) return fail(ctx, PSGD_ENOMEM, "optimizer buffer of %zu bytes", bytes);
     const hipError_t e = hipMemcpy(buf, norm.data(), norm.size() * sizeof(psgd::NormItem), hipMemcpyHostToDevice);
     if (e != hipSuccess) {
       (void)hipFree(buf);
