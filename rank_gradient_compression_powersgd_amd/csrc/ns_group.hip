@@ -95,6 +95,16 @@ struct Planned {
   double time = 0.0;
 };
 
+// Tiles of one product stage.
+int64_t tile_count(const std::vector<NsMat>& mats, NsStage st, int tile) {
+  int64_t n = 0;
+  for (const NsMat& d : mats) {
+    const int64_t ns = (d.s + tile - 1) / tile, nl = (d.l + tile - 1) / tile;
+    n += st == NS_UPDATE ? ns * nl : ns * (ns + 1) / 2;
+  }
+  return n;
+}
+
 // The tiles of one product stage, `tile` wide, in an order in which neighbours share operands:
 // blocks of up to 8 x 8 tiles of the lower triangle (A and B), or the row tiles over one column panel
 // of X (the update).
@@ -125,9 +135,9 @@ Planned plan_list(const std::vector<NsMat>& mats, NsStage st, bool accurate) {
   const int kinds = accurate ? 2 : 3;
   for (int kind = 0; kind < kinds; ++kind) {
     const TileCost& tc = accurate ? kAccurate[kind] : kFast[kind];
+    if (kind + 1 < kinds && tile_count(mats, st, tc.tile) > 64 * kCus) continue;   // far past what narrow tiles are for
     const std::vector<Work> w = tiles_of(mats, st, tc.tile);
     const int n = (int)w.size();
-    if (kind + 1 < kinds && n > 64 * kCus) continue;        // far past what narrow tiles are for
     const double fixed = st == NS_UPDATE ? tc.fixed_update : tc.fixed;
     const double tile_bytes = 4.0 * tc.tile * tc.tile;
     auto stages = [&](const Work& x) { return ns_stages(st == NS_GRAM ? mats[x.mat].l : mats[x.mat].s, accurate); };
@@ -183,6 +193,16 @@ hipError_t NsGroup::create(const std::vector<Item>& items, int in_type, int out_
   ot_ = out_type;
   accurate_ = accurate;
   const int n = (int)items.size();
+  // A group whose X, A and B exceed the card, padded to the narrowest tiles, is refused before its tiles
+  // are listed: 2^22 x 2^22 has 2^32 of them. What passes has 10^7 at most.
+  size_t card_free = 0, card = 0;
+  hipError_t e = hipMemGetInfo(&card_free, &card);
+  if (e != hipSuccess) return e;
+  for (const Item& t : items) {
+    const size_t s = (size_t)rup(std::min(t.m, t.n), 64), l = (size_t)rup(std::max(t.m, t.n), 64);
+    bytes_ += 8 * s * l + (accurate ? 8 : 4) * s * s;
+    if (bytes_ > card) return hipErrorOutOfMemory;
+  }
   std::vector<NsMat> mats(n);
   struct Off { size_t xh[2], xl[2], ah, al, bh, bl, partial; };
   std::vector<Off> offs(n);
@@ -240,7 +260,7 @@ hipError_t NsGroup::create(const std::vector<Item>& items, int in_type, int out_
   const size_t mats_off = take(sizeof(NsMat) * n), work_off = take(sizeof(Work) * all.size()), zero_off = take(sizeof(int32_t)),
                items_off = take(sizeof(NsItem) * n_items);
   bytes_ = ws;
-  hipError_t e = device_alloc(&buf_, bytes_);
+  e = device_alloc(&buf_, bytes_);
   if (e != hipSuccess) return hipErrorOutOfMemory;
   char* base = static_cast<char*>(buf_);
   d_mats_ = reinterpret_cast<NsMat*>(base + mats_off);

@@ -2,6 +2,8 @@
 from __future__ import annotations
 
 import math
+import resource
+import time
 
 import pytest
 
@@ -68,3 +70,20 @@ def test_a_refused_allocation_leaves_no_error_behind(refused):
     torch.cuda.empty_cache()
     a.close()
     b.close()
+
+
+@pytest.mark.parametrize("side,count", [(2 ** 22, 1), (2 ** 20, 3000)])
+def test_groups_past_the_memory_are_refused_before_they_are_planned(side, count):
+    """The largest shapes a descriptor may hold want terabytes: refused from their sizes, without host
+    lists of their tiles (2^32 of them)."""
+    import torch
+    from rank_gradient_compression_powersgd_amd import binding as B
+    x = torch.zeros(4, device="cuda")
+    ctx = B.psgd_create(0, 1)
+    before, t0 = resource.getrusage(resource.RUSAGE_SELF).ru_maxrss, time.monotonic()
+    with pytest.raises(B.PsgdError) as ei:
+        B.psgd_ns_plan_create(ctx, [B.psgd_ns_matrix(x.data_ptr(), side, x.data_ptr(), side, side, side)] * count, B.PSGD_F32, B.PSGD_F32)
+    grown = resource.getrusage(resource.RUSAGE_SELF).ru_maxrss - before
+    assert ei.value.status == B.PSGD_ENOMEM
+    assert grown < 1 << 18 and time.monotonic() - t0 < 5.0, (grown, time.monotonic() - t0)        # KiB
+    B.psgd_destroy(ctx)
