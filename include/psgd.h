@@ -307,7 +307,7 @@ psgd_status psgd_adam_attach(psgd_ctx* ctx, psgd_plan* plan, const psgd_adam_mat
 /* The scalars of a step, after psgd_check_finite and before the updates. Not skipped:
  * *step_dev += 1, norm_dev[0] = N, norm_dev[1] = c. Skipped: nothing is written.
  * N covers the decompressed gradient of every plan matrix and the pass-through gradients
- * (pass[i].grad, numel; at most 8192 * 65536 elements in all). For a plan matrix ||D||_F is
+ * (pass[i].grad, numel; at most 8192 tensors with elements). For a plan matrix ||D||_F is
  * taken as ||q_next||_F, equal to it because P has orthonormal columns, so N is known before
  * D is formed. Sums run in fp64 in a fixed order (bit-reproducible).
  *  step_dev  device int32: the optimizer's step count t (caller-owned, checkpointed with the

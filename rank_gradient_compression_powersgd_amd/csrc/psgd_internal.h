@@ -173,7 +173,8 @@ struct DevMat {
 };
 
 // One item of the global-norm reduction: a contiguous fp32 range of a gradient (q_next of a
-// compressed matrix, or a pass-through gradient), at most kNormItem elements.
+// compressed matrix, or a pass-through gradient), at most kNormItem elements (more where the
+// pass-through gradients would otherwise need more items than the buffer holds).
 struct NormItem {
   const float* ptr;
   int64_t n;

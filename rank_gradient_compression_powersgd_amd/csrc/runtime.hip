@@ -985,13 +985,25 @@ psgd_status psgd_adam_prepare(psgd_ctx* ctx, psgd_plan* plan, const psgd_adam_te
   if (!plan->adam_pt && !plan->muon) return fail(ctx, PSGD_EINVAL, "no optimizer attached to the plan (psgd_adam_attach)");
   if (!skip_dev || !step_dev || !norm_dev) return fail(ctx, PSGD_EINVAL, "skip_dev, step_dev and norm_dev are required");
   if (psgd_status st = check_pass_tensors(ctx, pass, n_pass, false); st != PSGD_OK) return st;
+  // the shortest items, kNormItem times a power of two, of which the buffer holds all (from 2^29
+  // elements on, an embedding's gradient, they are longer)
+  int64_t len = psgd::kNormItem, tensors = 0, longest = 0;
+  for (int i = 0; i < n_pass; ++i) {
+    tensors += pass[i].numel > 0;
+    longest = std::max(longest, pass[i].numel);
+  }
+  if (tensors > kMaxPassItems)
+    return fail(ctx, PSGD_EINVAL, "%lld pass-through tensors, at most %d", (long long)tensors, kMaxPassItems);
+  auto n_of = [&](int64_t l) {
+    int64_t n = 0;
+    for (int i = 0; i < n_pass && n <= kMaxPassItems; ++i) n += pass[i].numel / l + (pass[i].numel % l != 0);
+    return n;
+  };
+  while (len < longest && n_of(len) > kMaxPassItems) len *= 2;
   std::vector<psgd::NormItem> items;
   for (int i = 0; i < n_pass; ++i)
-    for (int64_t o = 0; o < pass[i].numel; o += psgd::kNormItem)
-      items.push_back(psgd::NormItem{pass[i].grad + o, std::min<int64_t>(psgd::kNormItem, pass[i].numel - o)});
-  if ((int)items.size() > kMaxPassItems)
-    return fail(ctx, PSGD_EINVAL, "pass-through gradients hold more than %lld elements",
-                (long long)kMaxPassItems * psgd::kNormItem);
+    for (int64_t o = 0; o < pass[i].numel; o += len)
+      items.push_back(psgd::NormItem{pass[i].grad + o, std::min<int64_t>(len, pass[i].numel - o)});
   const int n_items = plan->n_plan_items + (int)items.size();
   HIPCHK(ctx, traced(ctx, S_ADAM_NORM, stream, [&] {
     hipError_t e = items.empty() ? hipSuccess

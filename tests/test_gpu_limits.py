@@ -1,11 +1,16 @@
-"""Calls at the limits of memory and of sizes: what is refused leaves nothing behind."""
+"""Calls at the limits of memory and of sizes: what is refused leaves nothing behind, and what is
+allowed goes through the whole step."""
 from __future__ import annotations
 
 import math
 import resource
 import time
 
+import numpy as np
 import pytest
+
+import oracle
+from tests.gpu_helpers import log
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +92,53 @@ def test_groups_past_the_memory_are_refused_before_they_are_planned(side, count)
     assert ei.value.status == B.PSGD_ENOMEM
     assert grown < 1 << 18 and time.monotonic() - t0 < 5.0, (grown, time.monotonic() - t0)        # KiB
     B.psgd_destroy(ctx)
+
+
+def test_step_with_an_embedding_past_2_29_elements():
+    """The gradient of a table of 2^29 elements and more goes through the whole Muon step: norm, clipping
+    and Adam on the rows that have a gradient; the others stay as they are (no decay, zero moments)."""
+    import torch
+    from rank_gradient_compression_powersgd_amd import binding as B
+    vocab, dim, n = 2 ** 18 + 5, 2056, 300
+    assert vocab * dim > 2 ** 29
+    (g, params, mom), (other, _, _) = _muon_pair()
+    other.close()
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    table = torch.randn(vocab, dim, device="cuda", generator=gen)
+    m1, m2, dtable = torch.zeros_like(table), torch.zeros_like(table), torch.empty_like(table)
+    ids = torch.randint(0, vocab, (n,), device="cuda", generator=gen)
+    ids[0], ids[1] = vocab - 1, 0
+    dx = torch.randn(n, dim, device="cuda", generator=gen)
+    B.psgd_embed_grad(g.ctx, dx, ids, dtable)
+    rows = torch.unique(ids)
+    old = table[rows].double().cpu().numpy()
+    sums = [float(table[i:i + 65536].double().sum()) for i in range(0, vocab, 65536)]
+    hp, hpa = B.muon_hparams(0.01), B.psgd_adam_hparams(1e-2, 0.9, 0.999, 1e-8, 0.0)
+    log(f"step_muon with a table of {vocab} x {dim}")
+    g.step_muon(hp, [(table, m1, m2, dtable)], hpa, max_norm=5.0)
+    torch.cuda.synchronize()
+    grad = dtable[rows].double().cpu().numpy()
+    norm = math.sqrt(float((grad ** 2).sum()) + sum(float((q.double() ** 2).sum()) for q in g.q_next))
+    assert abs(float(g.adam_norm[0]) - norm) <= 1e-6 * norm
+    clip = float(g.adam_norm[1])
+    assert abs(clip - 5.0 / norm) <= 1e-6
+    state = oracle.AdamState(old, np.zeros_like(old), np.zeros_like(old), "f32", "f32", "f32")
+    (state,), _, _, _ = oracle.adam_group_step([state], [grad * clip], 0, False, hpa, hpa, n_mats=0, max_norm=0.0)
+    got = table[rows].double().cpu().numpy()
+    assert np.linalg.norm(got - state.theta) <= 1e-6 * np.linalg.norm(state.theta)
+    table[rows] = torch.from_numpy(old).float().cuda()
+    assert sums == [float(table[i:i + 65536].double().sum()) for i in range(0, vocab, 65536)]
+    g.close()
+
+
+def test_too_many_pass_through_tensors():
+    """More tensors than the norm has items are refused, whatever their size."""
+    import torch
+    from rank_gradient_compression_powersgd_amd import binding as B
+    (g, _, _), (other, _, _) = _muon_pair()
+    other.close()
+    x = torch.ones(4, device="cuda")
+    with pytest.raises(B.PsgdError) as ei:
+        B.psgd_adam_prepare(g.ctx, g.plan, [B.make_adam_tensor(x, x, x, x)] * 8193, 0.0, g.skip, g.adam_step, g.adam_norm)
+    assert ei.value.status == B.PSGD_EINVAL
+    g.close()
