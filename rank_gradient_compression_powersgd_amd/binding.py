@@ -193,13 +193,18 @@ def psgd_version() -> int:
     return int(load_library().psgd_version())
 
 
+_ctx_device = {}                             # device of every context made here
+
+
 def psgd_create(device: int, rank: int) -> int:
     h = ctypes.c_void_p()
     _check(None, "psgd_create", load_library().psgd_create(ctypes.byref(h), device, rank))
+    _ctx_device[h.value] = device
     return h.value
 
 
 def psgd_destroy(ctx: int) -> None:
+    _ctx_device.pop(ctx, None)
     load_library().psgd_destroy(ctx)
 
 
@@ -496,9 +501,10 @@ def psgd_ns_plan_destroy(plan: int) -> None:
 
 
 def psgd_newton_schulz(ctx: int, plan: int, hp: Optional[psgd_ns_hparams] = None, stream=None) -> None:
-    """Orthogonalise every matrix of the plan."""
+    """Orthogonalise every matrix of the plan, on the current stream of the context's device by default."""
     _check(ctx, "psgd_newton_schulz",
-           load_library().psgd_newton_schulz(ctx, plan, ctypes.byref(hp or ns_hparams()), _stream(stream)))
+           load_library().psgd_newton_schulz(ctx, plan, ctypes.byref(hp or ns_hparams()),
+                                             _stream(stream, _ctx_device.get(ctx))))
 
 
 def psgd_muon_attach(ctx: int, plan: int, opt: Sequence[psgd_muon_matrix], param_dtype: int,
@@ -508,9 +514,11 @@ def psgd_muon_attach(ctx: int, plan: int, opt: Sequence[psgd_muon_matrix], param
 
 
 def psgd_muon_update(ctx: int, plan: int, skip_dev, norm_dev, hp: psgd_muon_hparams, stream=None) -> None:
-    """One Muon step of every matrix of the plan on its decompressed gradient (norm_dev may be None)."""
+    """One Muon step of every matrix of the plan on its decompressed gradient (norm_dev may be None), on
+    the current stream of the context's device by default."""
     _check(ctx, "psgd_muon_update",
-           load_library().psgd_muon_update(ctx, plan, _ptr(skip_dev), _ptr(norm_dev), ctypes.byref(hp), _stream(stream)))
+           load_library().psgd_muon_update(ctx, plan, _ptr(skip_dev), _ptr(norm_dev), ctypes.byref(hp),
+                                           _stream(stream, _ctx_device.get(ctx))))
 
 
 def _ids(ids, call: str):

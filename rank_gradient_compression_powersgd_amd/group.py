@@ -148,6 +148,7 @@ class PowerSGDGroup:
             raise B.PsgdError("psgd_muon_update", B.PSGD_EINVAL, "no Muon state attached (attach_muon)")
         if passthrough and hp_pass is None:
             raise ValueError("pass-through tensors need their Adam hyperparameters (hp_pass)")
+        stream = B._stream(stream, self.flags.device)          # one stream, of the group's device, for all of them
         self.compress(stream)
         s = self.check_finite([t[3] for t in passthrough], host, stream)
         ts = [B.make_adam_tensor(*t) for t in passthrough]
