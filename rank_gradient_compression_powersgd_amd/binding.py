@@ -545,10 +545,13 @@ def _embed_rows(t, n: int, dim: int, name: str, call: str) -> int:
     return _row_stride(t, call)
 
 
-def _same_device(call: str, *tensors):
+def _same_device(call: str, *tensors, ctx: int = 0):
+    """All on one GPU, and on the context's: its device is the one that the kernels are launched on."""
     device = tensors[0].device
     if device.type != "cuda" or any(t.device != device for t in tensors):
         raise PsgdError(call, PSGD_EINVAL, "tensors must live on one GPU")
+    if _ctx_device.get(ctx, device.index) != device.index:
+        raise PsgdError(call, PSGD_EINVAL, f"tensors live on {device}, the context on device {_ctx_device[ctx]}")
 
 
 def psgd_embed_lookup(ctx: int, table, ids, out, scale: float = 1.0, stream=None) -> None:
@@ -559,7 +562,7 @@ def psgd_embed_lookup(ctx: int, table, ids, out, scale: float = 1.0, stream=None
         raise PsgdError(call, PSGD_EINVAL, "table must be a vocab x dim tensor")
     vocab, dim = table.shape
     ld_out = _embed_rows(out, ids.numel(), dim, "out", call)
-    _same_device(call, table, ids, out)
+    _same_device(call, table, ids, out, ctx=ctx)
     _check(ctx, call, load_library().psgd_embed_lookup(
         ctx, _ptr(table), _row_stride(table, call), vocab, dim, _dtype(table, call), _ptr(ids), _ids(ids, call),
         ids.numel(), float(scale), _ptr(out), ld_out, _dtype(out, call), _stream(stream, table.device.index)))
@@ -587,7 +590,7 @@ def psgd_embed_grad(ctx: int, dx, ids, dtable, scale: float = 1.0, accumulate: b
     n = ids.numel()
     ld_dx, ld_dt = _embed_rows(dx, n, dim, "dx", call), _row_stride(dtable, call)
     dt, it = _dtype(dx, call), _ids(ids, call)
-    _same_device(call, dx, ids, dtable, *([] if workspace is None else [workspace]))
+    _same_device(call, dx, ids, dtable, *([] if workspace is None else [workspace]), ctx=ctx)
     if workspace is None:
         need = psgd_embed_grad_workspace(n, vocab, dim)
         if stream is None:

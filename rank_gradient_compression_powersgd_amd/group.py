@@ -125,7 +125,7 @@ class PowerSGDGroup:
         for p, e in zip(params, self.err):
             if tuple(p.shape) != tuple(e.shape):
                 raise B.PsgdError(call, B.PSGD_EINVAL, "param and matrix shapes differ")
-        B._same_device(call, self.flags, *params, *momentum)
+        B._same_device(call, self.flags, *params, *momentum, ctx=self.ctx)
         if accurate is None:
             accurate = params[0].dtype == torch.float32
         opt = [B.make_muon_matrix(p, m) for p, m in zip(params, momentum)]

@@ -98,3 +98,23 @@ def test_one_stream_through_the_whole_muon_step(lib):
     assert [n for n, _ in lib.calls if n in names] == names
     for n in names:
         assert lib.args(n)[0][-1] == 101, n
+
+
+def test_tensors_on_another_device_than_the_context_are_refused(lib):
+    """A launch on the context's device would read the other device's memory."""
+    ctx = B.psgd_create(0, 1)
+    table, ids, rows = _On(torch.zeros(5, 8), 1), _On(torch.zeros(3, dtype=torch.int64), 1), _On(torch.zeros(3, 8), 1)
+    for call in (lambda c: B.psgd_embed_lookup(c, table, ids, rows),
+                 lambda c: B.psgd_embed_grad(c, rows, ids, table, workspace=_On(torch.zeros(1 << 16, dtype=torch.uint8), 1))):
+        with pytest.raises(B.PsgdError) as ei:
+            call(ctx)
+        assert ei.value.status == B.PSGD_EINVAL and "context" in str(ei.value)
+    g = _group(0)
+    with pytest.raises(B.PsgdError) as ei:
+        g.attach_muon([_On(torch.zeros(4, 8), 1)], [_On(torch.zeros(4, 8), 1)])
+    assert ei.value.status == B.PSGD_EINVAL and "context" in str(ei.value)
+    assert not [n for n, _ in lib.calls if n in ("psgd_embed_lookup", "psgd_embed_grad", "psgd_muon_attach")]
+    there = B.psgd_create(1, 1)
+    B.psgd_embed_lookup(there, table, ids, rows)
+    B.psgd_embed_grad(there, rows, ids, table, workspace=_On(torch.zeros(1 << 16, dtype=torch.uint8), 1))
+    assert lib.args("psgd_embed_lookup")[0][-1] == 101 and lib.args("psgd_embed_grad")[0][-1] == 101
