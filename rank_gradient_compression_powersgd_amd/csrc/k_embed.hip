@@ -20,7 +20,7 @@ namespace {
 // ---- element access ------------------------------------------------------------------------
 template <int T, int V> struct Vec {
   typedef float f __attribute__((ext_vector_type(V)));
-  // V consecutive elements at p[i], widened; V > 1: 16-byte (8-byte for 4 half-width) aligned
+  // V consecutive elements at p[i], widened; V > 1: 16-byte aligned. 16-bit types take 8 or 1.
   static __device__ __forceinline__ f load(const void* p, int64_t i) {
     if constexpr (T == G_F32) {
       const GLOBAL float* q = gbl(static_cast<const float*>(p)) + i;
@@ -32,8 +32,10 @@ template <int T, int V> struct Vec {
       if constexpr (V == 1) {
         if constexpr (T == G_F16) return f{(float)__builtin_bit_cast(_Float16, *q)};
         else return f{__builtin_bit_cast(float, (uint32_t)*q << 16)};
-      } else if constexpr (V == 4) return GradIO<T>::load4(gcast<char>(q));
-      else return GradIO<T>::load8(gcast<char>(q));
+      } else {
+        static_assert(V == 8);
+        return GradIO<T>::load8(gcast<char>(q));
+      }
     }
   }
   static __device__ __forceinline__ void store(void* p, int64_t i, f v) {
