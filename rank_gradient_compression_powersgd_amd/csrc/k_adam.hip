@@ -11,7 +11,8 @@
 //
 // Global norm. For a compressed matrix the gradient the optimizer consumes is D = P Q'^T with
 // orthonormal columns in P, so ||D||_F = ||Q'||_F: the norm is taken over q_next (n x r)
-// instead of D (m x n), before D exists. Items of at most kNormItem floats are summed in fp64
+// instead of D (m x n), before D exists. Items of at most kNormItem floats (longer ones where the
+// pass-through gradients have 2^29 elements or more) are summed in fp64
 // in a fixed order (deterministic), then one workgroup adds the item sums in order.
 #include "psgd_internal.h"
 

@@ -28,10 +28,11 @@ template <int IT> __device__ __forceinline__ f32x4 load4(const void* p, int64_t 
   if constexpr (IT == G_F32) return *gcast<f32x4>(gbl(static_cast<const float*>(p)) + i);
   else return GradIO<IT>::load4(gcast<char>(gbl(static_cast<const uint16_t*>(p)) + i));
 }
+// Muon's matrices always qualify: a compression plan's n is a multiple of 8, the pitch of its
+// gradients one of 4, and gradients and momentum are 16-byte aligned.
 template <int IT> __device__ __forceinline__ bool vec4_ok(const NsMat& d) {
   constexpr uintptr_t mask = IT == G_F32 ? 15 : 7;
-  return ((d.n | (int)(d.ld_in & 3)) & 3) == 0 && (reinterpret_cast<uintptr_t>(d.in) & mask) == 0 &&
-         (reinterpret_cast<uintptr_t>(d.mom) & 15) == 0;
+  return ((d.n | (int)(d.ld_in & 3)) & 3) == 0 && (reinterpret_cast<uintptr_t>(d.in) & mask) == 0;
 }
 
 template <int IT>
@@ -73,25 +74,17 @@ void k_ns_norm(const NsMat* __restrict__ mats, const Work* __restrict__ work, Ns
   } else {
     const uint32_t total = (uint32_t)rows * (uint32_t)n;
     for (uint32_t e0 = threadIdx.x; e0 < total; e0 += 2 * BATCH * kThreads) {
-      float u[2 * BATCH], mo[2 * BATCH];
-      int64_t at[2 * BATCH];
+      float u[2 * BATCH];
 #pragma unroll
       for (int k = 0; k < 2 * BATCH; ++k) {
         const uint32_t e = min(e0 + k * kThreads, total - 1), r = e / (uint32_t)n, col = e - r * (uint32_t)n;
         u[k] = load1<IT>(d.in, (int64_t)(r0 + (int)r) * d.ld_in + col);
-        at[k] = (int64_t)(r0 + (int)r) * n + col;
-        if (a.muon) mo[k] = gbl(d.mom)[at[k]];
       }
+      __builtin_amdgcn_sched_barrier(0);       // or the loads sink to their uses (6.6 us become 10.3)
 #pragma unroll
       for (int k = 0; k < 2 * BATCH; ++k) {
         if (e0 + k * kThreads >= total) break;
-        float x = u[k];
-        if (a.muon) {
-          const float g = clip * x, m1 = a.mu * mo[k] + g;
-          gbl(d.mom)[at[k]] = m1;
-          x = a.nesterov ? g + a.mu * m1 : m1;
-        }
-        acc += (double)x * (double)x;
+        acc += (double)u[k] * (double)u[k];
       }
     }
   }
@@ -144,14 +137,7 @@ void k_ns_x0(const NsMat* __restrict__ mats, const Work* __restrict__ work, NsAr
       } else {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-          if (col + t < d.n) {
-            float x = load1<IT>(d.in, (int64_t)row * d.ld_in + col + t);
-            if (a.muon) {
-              const float mo = gbl(d.mom)[(int64_t)row * d.n + col + t];
-              x = a.nesterov ? clip * x + a.mu * mo : mo;
-            }
-            u[k][t] = x;
-          }
+          if (col + t < d.n) u[k][t] = load1<IT>(d.in, (int64_t)row * d.ld_in + col + t);
       }
     }
   }
