@@ -342,8 +342,13 @@ psgd_status psgd_adam_update(psgd_ctx* ctx, const psgd_adam_tensor* pass, int n_
  *
  * Products. PSGD_NS_FAST multiplies factors rounded to fp16 (2^-12 each) with fp32 sums and
  * carries X itself in 22 bits: the result is within about 2e-3 of its Frobenius norm (4e-3 for a
- * few rows of equal singular values), the rounding of a bf16 output. PSGD_NS_ACCURATE multiplies fp16 halves hi + lo (three products),
- * as close to the exact result as fp32 products, at a third to a half of the speed.
+ * few rows of equal singular values), before the output's own rounding. PSGD_NS_ACCURATE multiplies
+ * fp16 halves hi + lo (three products) at a third to a half of the speed: with the coefficients below
+ * the result's Frobenius error is about 1e-6, a quarter of that of fp32 products on large matrices,
+ * twice it on tiny ones. That is of the whole norm: what halves hold has a floor, 2^-39 in X and A
+ * and 2^-35 in B, so a row that is 1e-4 of the others is as good as with fp32 products, but one
+ * that is 1e-5 (1e-6) of them 8e-5 (8e-4) of itself off, where those leave 7e-6, and a result that
+ * comes from small elements of B alone (a = 0) up to 5e-4.
  *
  * Coefficients: the singular values entering each step must stay below 1.97, |b x^2 + c x^4| and
  * |a + b x^2 + c x^4| at most 60 (checked on the host by following the polynomial from [0, 1]);
@@ -371,7 +376,9 @@ typedef struct psgd_ns_plan psgd_ns_plan;
 
 /* Describe a group orthogonalised in grouped launches. Allocates the plan's workspace (8 bytes per
  * element of the matrices padded to whole tiles, 4 per element of s x s, 8 when accurate, and the
- * partial sums of products that are split) and uploads the tables (synchronously). The pointers are captured. One plan runs one call at a time. */
+ * partial sums of products that are split) and uploads the tables (synchronously). The pointers are
+ * captured. One plan runs one call at a time. PSGD_ENOMEM when the workspace does not fit. Planning
+ * takes longer than a call on small matrices: keep the plan, do not make one per step. */
 psgd_status psgd_ns_plan_create(psgd_ctx* ctx, const psgd_ns_matrix* mats, int n_mats, psgd_dtype in_dtype,
                                 psgd_dtype out_dtype, psgd_ns_precision precision, psgd_ns_plan** plan);
 
@@ -388,7 +395,13 @@ psgd_status psgd_newton_schulz(psgd_ctx* ctx, psgd_ns_plan* plan, const psgd_ns_
  *     theta <- theta - lr (f O + wd theta)
  *     f = sqrt(max(1, m / n)) (adjust 0) or 0.2 sqrt(max(m, n)) (adjust 1: the update's root mean
  *     square is then near Adam's, so learning rates carry over)
- * with c the clipping factor norm_dev[1] of psgd_adam_prepare. Call order per step:
+ * with c the clipping factor norm_dev[1] of psgd_adam_prepare.
+ *  - adjust 0 is the method's factor sqrt(max(1, outputs / inputs)) for weights stored outputs x
+ *    inputs. For weights stored inputs x outputs, as the resblock matrices of this step are, it is
+ *    not (an m x n weight of n outputs would want sqrt(max(1, n / m))); adjust 1 is the same for both.
+ *  - Each plan matrix is orthogonalised on its own. Where it is one GPU's shard of a weight, O is
+ *    the factor of that block, not the block of the whole weight's factor; f takes the block's m, n.
+ * Call order per step:
  *     psgd_compress -> psgd_check_finite -> psgd_adam_prepare -> psgd_decompress_update
  *     -> psgd_muon_update -> psgd_adam_update (the pass-through tensors)
  */
@@ -423,15 +436,18 @@ psgd_status psgd_muon_update(psgd_ctx* ctx, psgd_plan* plan, const int32_t* skip
  * which is a pass-through gradient of psgd_check_finite, psgd_adam_prepare and psgd_adam_update.
  *   psgd_embed_lookup: out[t] = round(scale * table[ids[t]]), t = 0..n-1, rounded once to
  *     out_dtype; a row of zeros for an id outside [0, vocab) (padding).
- *   psgd_embed_grad: dtable[v] = scale * sum of dx[t] over the t with ids[t] = v, in fp32 in the
- *     order of the batch (the same bits on every run); rows of absent tokens become 0. With
- *     accumulate != 0 the sums are added to dtable instead and rows of absent tokens are not
- *     touched. Ids outside [0, vocab) are ignored. Non-finite dx values end up in dtable.
+ *   psgd_embed_grad: dtable[v] = scale * sum of dx[t] over the t with ids[t] = v; rows of absent
+ *     tokens become 0. With accumulate != 0 the sums are added to dtable instead and rows of absent
+ *     tokens are not touched. Ids outside [0, vocab) are ignored. Non-finite dx values end up in
+ *     dtable. The k rows of a token are added in fp32, in a grouping that the ids of the whole call
+ *     determine: the same inputs give the same bits, but other ids elsewhere may group a token's rows
+ *     otherwise. The error is at most (k + 2) 2^-24 of scale * sum |dx| (+ |dtable|).
  * table, dx and out: fp16, bf16 or fp32, row-major, any leading dimension >= dim, aligned to their
  * element type. ids: n int32 (PSGD_I32) or int64 (PSGD_I64) on the device. dtable: fp32.
  * 0 <= n <= 2^25 (0: lookup does nothing, gradient clears dtable unless accumulating),
  * 1 <= vocab < 2^31 in the lookup and <= 2^20 in the gradient, 1 <= dim <= 2^23. Outputs must not
- * overlap inputs.
+ * overlap inputs. All buffers live on the ctx's device. Past 2^18 rows the gradient's sort takes
+ * longer: 65537 tokens x 64 in 44 us up to there, in 82 us just past it, in 0.2 ms with 2^20 rows.
  *   workspace: psgd_embed_grad_workspace(n, vocab, dim) bytes of device memory, 16-byte aligned,
  *     contents ignored and overwritten; one for n tokens serves fewer of the same table; calls that
  *     may overlap need one each.
@@ -494,7 +510,8 @@ psgd_status psgd_plan_counters(psgd_plan* plan, const int64_t** counters);
  * row scales (rank > 128 only, and psgd_refresh_q), 11 second orthonormalisation pass (all
  * four of its launches; they return at once for matrices whose first pass was well
  * conditioned), 12 global gradient norm of psgd_adam_prepare, 13 decompression with the Adam
- * update, 14 pass-through Adam. Slots a call does not launch keep their events unrecorded.
+ * update, 14 pass-through Adam. Slots a call does not launch keep their events unrecorded; the
+ * Newton-Schulz, Muon and embedding launches belong to no slot.
  * n must be at least 30.
  * events == NULL (n ignored) removes the hook. The events stay owned by the caller.
  */

@@ -6,10 +6,11 @@
 // The embeddings are the uncompressed 32-bit tensors of the step (Korean summary of the paper,
 // section "Mixed-Precision Training"): the gradient formed here is a pass-through gradient.
 //
-// Both are bound by HBM. The gradient adds the rows of a token in the order of the batch, in
-// fp32, with no atomics on data: the tokens are sorted stably first, then fixed chunks of the
-// sorted order are summed, so the result is the same bits on every run and a token that fills
-// half the batch is spread over the chip like any other.
+// Both are bound by HBM. The gradient adds the rows of a token in fp32 with no atomics on data: the
+// tokens are sorted stably first, then fixed chunks of the sorted order are summed, each in the
+// order of the batch, and the chunks' sums of a token added. The same inputs give the same bits on
+// every run (where chunks cut a token's rows depends on the tokens sorted before it), and a token
+// that fills half the batch is spread over the chip like any other.
 #include <algorithm>
 
 #include "embed.h"
@@ -538,7 +539,8 @@ int64_t embed_range(int64_t vocab) {
   return r < 16 ? 16 : r > kEmbedRange ? kEmbedRange : r;
 }
 // Tokens per workgroup of the three-launch sort (at most 128 workgroups, since each adds up the
-// counts of all), or 0: one launch. That one takes any vocabulary.
+// counts of all), or 0: one launch. That one takes any vocabulary, and reads every id once per range:
+// 2^20 ids, 2048 ranges, take 0.2 ms with 65537 tokens, 2.3 with 2^20, 76 with 2^25.
 int64_t embed_tokens(int64_t n, int64_t vocab) {
   const int64_t ranges = (vocab + embed_range(vocab) - 1) / embed_range(vocab);
   if (n <= kEmbedShort || ranges > kEmbedRanges) return 0;

@@ -11,7 +11,8 @@ namespace psgd {
 // The iteration works on the smaller side: X is s x l with s = min(m, n), l = max(m, n), the
 // update transposed when m > n. Everything between the first and the last kernel lives in the
 // workspace as fp16 values times a fixed power of two, zero-padded to whole tiles:
-//   X  (sp x lp)  as hi + lo, X * 2^14 = hi + lo to 2^-22: singular values stay below 4
+//   X  (sp x lp)  as hi + lo, X * 2^14 = hi + lo to 2^-22 of itself, or to lo's floor of 2^-25 for
+//                 |X| below 2^-17: singular values stay below 4
 //   A  (sp x sp)  X X^T, times 2^14 (entries bounded by the squared singular values)
 //   B  (sp x sp)  b A + c A A, times 2^10
 // All of them are stored as panels of 32 columns, one after another, 64 bytes per row within a panel:
@@ -56,7 +57,7 @@ struct NsItem {
   NsMat d;
 };
 
-// Elements of the update as they enter the iteration and of the result as they leave it.
+// The products of one step: A = X X^T, B = b A + c A A, X <- a X + B X.
 enum NsStage : int { NS_GRAM = 0, NS_POLY = 1, NS_UPDATE = 2 };
 
 hipError_t launch_ns_norm(int it, const NsMat* mats, const Work* work, int n_work, const NsArgs& a, hipStream_t s);
@@ -87,16 +88,16 @@ class NsGroup {
  public:
   struct Item { const void* in; int64_t ld_in; float* mom; void* out; int64_t ld_out; int64_t m, n; };
   ~NsGroup();
-  // types are GradType; adds no host work to later calls. Returns hipErrorOutOfMemory when the
-  // workspace does not fit, hipErrorInvalidValue when a matrix is too large for 32-bit tiles.
+  // types are GradType; adds no host work to later calls. Sides are at most 2^22 (the caller has
+  // checked). Returns hipErrorOutOfMemory when the workspace does not fit.
   hipError_t create(const std::vector<Item>& items, int in_type, int out_type, bool accurate);
-  // factor(m, n) of every matrix for Muon calls (adjust: 0 sqrt(max(1, m/n)), 1 0.2 sqrt(max(m, n)))
+  // adjust selects NsMat::factor for Muon calls: 0 sqrt(max(1, m/n)), 1 0.2 sqrt(max(m, n))
   hipError_t run(const NsArgs& a, int adjust, hipStream_t s);
   size_t workspace_bytes() const { return bytes_; }
 
  private:
   struct List { int off = 0, cnt = 0; };
-  void* buf_ = nullptr;                  // workspace, descriptors (one table per adjust), work lists
+  void* buf_ = nullptr;                  // workspace, descriptors, work lists
   size_t bytes_ = 0;
   NsMat* d_mats_ = nullptr;
   int32_t* d_zero_ = nullptr;            // a skip word for calls that have none

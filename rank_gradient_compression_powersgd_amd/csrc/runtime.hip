@@ -1247,7 +1247,8 @@ psgd_status psgd_muon_update(psgd_ctx* ctx, psgd_plan* plan, const int32_t* skip
 
 namespace {
 // A launch is at most 2^32 threads long: 64 per token in the lookup. The gradient's vocabulary is
-// bounded for its time, since past 2^18 ids its sort reads every id once per 512 of them.
+// bounded for its time, since past 2^18 ids its sort reads every id once per 512 of them
+// (embed_tokens has the times).
 constexpr int64_t kMaxTokens = 1 << 25, kMaxGradVocab = 1 << 20;
 
 psgd_status check_embed(psgd_ctx* ctx, const void* ids, psgd_itype it, int64_t n, int64_t vocab, int64_t max_vocab, int64_t dim, float scale) {

@@ -114,8 +114,9 @@ class PowerSGDGroup:
     def attach_muon(self, params: Sequence, momentum: Sequence, accurate: Optional[bool] = None):
         """Attach per-matrix Muon state (caller-owned device tensors, updated in place): params
         m x n (fp16, bf16 or fp32), momentum m x n fp32. The group needs its out buffers
-        (write_out). accurate: products as exact as fp32 ones; default: for fp32 parameters,
-        whose rounding the fast products' 2e-3 of the update would exceed."""
+        (write_out). accurate: products with the norm-wise error of fp32 ones; default: for fp32
+        parameters, whose rounding the fast products' 2e-3 of the update would exceed. Each
+        matrix is orthogonalised on its own: a shard of a weight gets its block's factor."""
         torch, call = self.torch, "psgd_muon_attach"
         params, momentum = list(params), list(momentum)
         if len(params) != len(self.err) or len(momentum) != len(self.err):
@@ -185,8 +186,9 @@ class NewtonSchulzGroup:
 
     updates, outs: lists of 2-D device tensors (unit row stride), each list of one dtype (fp16,
                    bf16 or fp32); out may be its update itself. The buffers are captured.
-    accurate: products as exact as fp32 ones (default: unless the outputs are bf16, whose rounding
-              is as large as the fast products' error)
+    accurate: products with the norm-wise error of fp32 ones (about 1e-6). Default: unless the
+              outputs are bf16, whose rounding, 1.7e-3 of the norm, exceeds the fast products'
+              error of about 1e-3 (both together: 2e-3)
     """
 
     def __init__(self, updates: Sequence, outs: Sequence, accurate: Optional[bool] = None):
