@@ -344,8 +344,8 @@ psgd_status psgd_adam_update(psgd_ctx* ctx, const psgd_adam_tensor* pass, int n_
  * carries X itself in 22 bits: the result is within about 2e-3 of its Frobenius norm (4e-3 for a
  * few rows of equal singular values), before the output's own rounding. PSGD_NS_ACCURATE multiplies
  * fp16 halves hi + lo (three products) at a third to a half of the speed: with the coefficients below
- * the result's Frobenius error is about 1e-6, a quarter of that of fp32 products on large matrices,
- * twice it on tiny ones. That is of the whole norm: what halves hold has a floor, 2^-39 in X and A
+ * the result's Frobenius error is 1e-6 on random updates, up to 5e-6 where a few directions dominate:
+ * a quarter to the whole of that of fp32 products, twice it on tiny matrices. That is of the whole norm: what halves hold has a floor, 2^-39 in X and A
  * and 2^-35 in B, so a row that is 1e-4 of the others is as good as with fp32 products, but one
  * that is 1e-5 (1e-6) of them 8e-5 (8e-4) of itself off, where those leave 7e-6, and a result that
  * comes from small elements of B alone (a = 0) up to 5e-4.

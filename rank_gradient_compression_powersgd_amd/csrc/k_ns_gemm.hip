@@ -11,7 +11,7 @@
 // reaches directions the update already has, while a rounded X itself would put noise into the
 // directions it lacks, which every step then multiplies by a = 3.4 (an update of rank 112 came
 // out 3% off, against 0.15%). The accurate products use both halves of every factor
-// (hi hi + hi lo + lo hi): the result's error, about 1e-6 of its norm, is that of fp32 products.
+// (hi hi + hi lo + lo hi): the result's error, 1e-6 to 5e-6 of its norm, is that of fp32 products.
 //
 // Measured. Four resblock shards (s 496..1984, l 3968), fast: A 181 us, B 106, update 350; the
 // unsharded resblock (s 3968, l up to 15872): A 596, B 243, update 1256, 1.2 PFLOP/s.

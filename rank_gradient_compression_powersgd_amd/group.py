@@ -186,7 +186,7 @@ class NewtonSchulzGroup:
 
     updates, outs: lists of 2-D device tensors (unit row stride), each list of one dtype (fp16,
                    bf16 or fp32); out may be its update itself. The buffers are captured.
-    accurate: products with the norm-wise error of fp32 ones (about 1e-6). Default: unless the
+    accurate: products with the norm-wise error of fp32 ones (1e-6 to 5e-6). Default: unless the
               outputs are bf16, whose rounding, 1.7e-3 of the norm, exceeds the fast products'
               error of about 1e-3 (both together: 2e-3)
     """
