@@ -187,9 +187,7 @@ def _quantize4(x, r, stochastic):
     a = v.abs() * torch.exp2((127 - exps).double()).float()[:, :, None]
     step = torch.where(a < 2, 0.5, torch.where(a < 4, 1.0, 2.0))
     if stochastic:
-        small = (a < 1).to(torch.float32)
-        u = (r.view(v.shape) >> 10).double() * 2.0 ** -22
-        q = (torch.floor((a + small).double() / step + u) * step - small).float()
+        q = (torch.floor(a.double() / step + (r.view(v.shape) >> 10).double() * 2.0 ** -22) * step).float()
     else:
         q = torch.round(a / step) * step
     q = torch.where(v < 0, -q, q).clamp(-6, 6)
@@ -226,11 +224,16 @@ def _pad(x):
     return torch.nn.functional.pad(x, (0, _panels(x.shape[1]) * PANEL - x.shape[1]))
 
 
+def _pair_bits(m, n, seed):
+    """32 random bits of each element of an m x n matrix: a hash for two neighbours, the second's turned by 16."""
+    h = _bits(_key(seed, 0, 0), torch.arange(m * ((n + 1) // 2), device="cuda")).view(m, -1)
+    return torch.stack([h, ((h << 16) & MASK) | (h >> 16)], 2).view(m, -1)[:, :n]
+
+
 def _random4(x, seed, flip):
-    """32 random bits of each element of a matrix, of its transpose where `flip`, padded."""
-    m, n = x.shape
-    i = torch.arange(m * n, device=x.device).view(m, n)
-    return _pad(_bits(_key(seed, 0, 0), i.t() if flip else i))
+    """The random bits of a matrix, of its transpose where `flip`, padded."""
+    r = _pair_bits(*x.shape, seed)
+    return _pad(r.t() if flip else r)
 
 
 def _round4(x, stochastic, seed, flip=False):
@@ -499,7 +502,7 @@ def _exact_adamw(case, seed):
 
 def _exact4(x, stochastic, seed, flip=False):
     v = x.double()
-    r = _bits(_key(seed, 0, 0), torch.arange(v.numel(), device="cuda").view(v.shape)) if stochastic else None
+    r = _pair_bits(*v.shape, seed) if stochastic else None
     v = v.t() if flip else v
     k = v.shape[1]
     pad = -k % BLOCK
