@@ -171,7 +171,8 @@ def _store16(v, r2, kind, stochastic):
 
 # ---- the 4-bit matrices ---------------------------------------------------------------------
 # Rows of k elements, padded with zeros to panels of 128 columns; a panel holds 64 bytes of codes a
-# row (the even element in the low nibble), and after all panels come 4 exponent bytes a row and panel.
+# row (the even element in the low nibble). After all panels come the exponents: per panel and 64 rows
+# 256 bytes, ordered by block of the panel, row % 16, row / 16.
 VALUES = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 
 
@@ -206,14 +207,15 @@ def _pack4(q, exps):
     level = torch.bucketize(q.abs().view(rows, -1), torch.tensor(VALUES, device=q.device))
     code = (level + 8 * torch.signbit(q).view(rows, -1)).view(rows, -1, PANEL // 2, 2)
     codes = (code[..., 0] + 16 * code[..., 1]).view(rows, -1, PANEL // 2).transpose(0, 1)
-    return torch.cat([codes.reshape(-1), exps.view(rows, -1, PANEL // BLOCK).transpose(0, 1).reshape(-1)]).to(torch.uint8)
+    exps = torch.nn.functional.pad(exps, (0, 0, 0, -rows % 64), value=1).view(-1, 4, 16, codes.shape[0], 4).permute(3, 0, 4, 2, 1)
+    return torch.cat([codes.reshape(-1), exps.reshape(-1)]).to(torch.uint8)
 
 
 def _unpack4(data, rows, k):
     """fp32 values [rows, k] of a quantised matrix."""
     p = _panels(k)
     codes = data[:p * rows * 64].view(p, rows, 64).transpose(0, 1).to(torch.int64)
-    exps = data[p * rows * 64:].view(p, rows, 4).transpose(0, 1).reshape(rows, -1).to(torch.int64)
+    exps = data[p * rows * 64:].view(p, -1, 4, 16, 4).permute(1, 4, 3, 0, 2).reshape(-1, 4 * p)[:rows].to(torch.int64)
     grid = torch.tensor(VALUES + tuple(-v for v in VALUES), device=data.device)
     q = grid[torch.stack([codes & 15, codes >> 4], 3).view(rows, -1, BLOCK)]
     s = torch.where(exps == 255, math.nan, torch.exp2((exps - 127).double())).float()
@@ -341,7 +343,7 @@ def prepare(case, seed):
         st["a"], st["b"] = psgd.MxTensor(case["m"], case["k"], data=st["a"]), psgd.MxTensor(case["n"], case["k"], data=st["b"])
         st["workspace"] = torch.empty(psgd.psgd_mx_product_workspace(case["m"], case["n"], case["k"]), dtype=torch.uint8, device="cuda")
     else:
-        st["layer"] = psgd.MxLinear(st["w"], max_tokens=case["t"], seed=seed)
+        st["layer"] = psgd.MxLinear(st["w"], seed=seed)
     return st
 
 
@@ -546,7 +548,7 @@ def exact(case, seed):
 
 # ---- what a pass cannot do without ----------------------------------------------------------
 def _bytes4(rows, k):
-    return _panels(k) * rows * 68
+    return _panels(k) * (rows * 64 + -(-rows // 64) * 256)
 
 
 def work(case):
