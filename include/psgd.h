@@ -465,6 +465,120 @@ psgd_status psgd_embed_grad(psgd_ctx* ctx, const void* dx, int64_t ld_dx, psgd_d
                             hipStream_t stream);
 
 /*
+ * How a value is stored in fewer bits than it was computed in. PSGD_NEAREST: to nearest even.
+ * PSGD_STOCHASTIC: to one of its two neighbours, up with the probability of the fraction cut off, so
+ * that the expectation is the value. The random bits are a hash of the caller's seed, the step count
+ * on the device, the tensor's number and the element's index: the same call gives the same bits.
+ */
+typedef enum psgd_rounding { PSGD_NEAREST = 0, PSGD_STOCHASTIC = 1 } psgd_rounding;
+
+/*
+ * AdamW over a list of tensors at once, of any parameter and gradient type: the update above for
+ * pass-through tensors (a model's own, or a plan's decompressed gradients), with moments in fp32 or
+ * in 8 bits.
+ *   PSGD_STATE_F32   m1, m2: fp32, numel rounded up to 64
+ *   PSGD_STATE_BYTE  m1, m2: one code per element, numel rounded up to 64; e1, e2: one exponent byte per
+ *     64 elements, of their largest magnitude (one more from 1.875 times its power of two on). m1: sign,
+ *     4 exponent and 3 fraction bits; m2: 5 exponent and 3 fraction bits, the largest field standing for
+ *     the byte's exponent, both with subnormals: 3 fraction bits down to 2^-14 (m1) and 2^-30 (m2) of the
+ *     largest. A positive m2 never becomes 0. Byte 255: all 64 are NaN (a moment from 1.875 2^127 on).
+ * All zero is the state before the first step, in both forms. Elements past numel are written as 0.
+ * Moments rounded to nearest stand still once a step changes them by less than half a code; with
+ * PSGD_STOCHASTIC their expectation moves as in fp32.
+ */
+typedef enum psgd_state { PSGD_STATE_F32 = 0, PSGD_STATE_BYTE = 1 } psgd_state;
+
+/* One tensor: numel >= 0 elements, contiguous. param and grad aligned to their element type, m1 and m2
+ * to 16 bytes; e1 and e2 are not read with PSGD_STATE_F32. Caller-owned device memory; no two tensors'
+ * buffers may overlap, nor a tensor's own. */
+typedef struct psgd_adamw_tensor {
+  void* param;  const void* grad;
+  void* m1;     void* m2;
+  uint8_t* e1;  uint8_t* e2;
+  int64_t numel;
+} psgd_adamw_tensor;
+
+typedef struct psgd_adamw_plan psgd_adamw_plan;
+
+/* Describe a list that is stepped together. Allocates and uploads its table (64 bytes per 4096 elements,
+ * synchronously). The pointers are captured. One plan runs one call at a time. */
+psgd_status psgd_adamw_plan_create(psgd_ctx* ctx, const psgd_adamw_tensor* tensors, int n, psgd_dtype param_dtype,
+                                   psgd_dtype grad_dtype, psgd_state state, psgd_adamw_plan** plan);
+
+/* Free a plan (synchronises the device). NULL is accepted. */
+psgd_status psgd_adamw_plan_destroy(psgd_adamw_plan* plan);
+
+/* The scalars of a step from the list's gradients. *skip_dev = 1 when any gradient is non-finite or
+ * skip_in is not NULL and *skip_in != 0 (the skip word of psgd_check_finite, where the gradients are
+ * decompressed ones; it may be skip_dev itself), else 0. Not skipped: *step_dev += 1, norm_dev[0] = the
+ * gradients' norm N, norm_dev[1] = min(1, max_norm / N) (1 when max_norm <= 0). Skipped: only skip_dev is
+ * written. Sums run in fp64 in a fixed order. */
+psgd_status psgd_adamw_prepare(psgd_ctx* ctx, psgd_adamw_plan* plan, float max_norm, const int32_t* skip_in,
+                               int32_t* skip_dev, int32_t* step_dev, float* norm_dev, hipStream_t stream);
+
+/* One step on the list with the scalars of psgd_adamw_prepare (or psgd_adam_prepare, where the clipping
+ * factor covers more than this list). norm_dev may be NULL (no clipping). A step whose skip word is set
+ * changes nothing. rounding applies to 8-bit moments and 16-bit parameters; seed is not read with
+ * PSGD_NEAREST. Moments are computed in fp32, each operation rounded; the quotient is within 2^-21. */
+psgd_status psgd_adamw_update(psgd_ctx* ctx, psgd_adamw_plan* plan, const int32_t* skip_dev, const int32_t* step_dev,
+                              const float* norm_dev, const psgd_adam_hparams* hp, psgd_rounding rounding, uint64_t seed,
+                              hipStream_t stream);
+
+/* The values of 8-bit moments, for checkpoints and monitoring: out1, out2 [n] in out_dtype PSGD_F32 or
+ * PSGD_BF16 (which hold them exactly, down to their subnormals). m1 and m2 16-byte aligned, out aligned
+ * to its type; n >= 0 elements from the start of a group of 64 on. */
+psgd_status psgd_adamw_moments(psgd_ctx* ctx, const uint8_t* m1, const uint8_t* e1, const uint8_t* m2, const uint8_t* e2,
+                               int64_t n, void* out1, void* out2, psgd_dtype out_dtype, hipStream_t stream);
+
+/*
+ * Microscaled 4-bit matrices: the operands of a layer's three products in low precision, of which the
+ * weight's gradient goes straight into the error buffer of an in-place psgd_matrix (M = s_b G + E).
+ * An element is sign, 2 exponent and 1 fraction bits: 0, 0.5, 1, 1.5, 2, 3, 4, 6. 32 consecutive elements
+ * of a row share a scale 2^(s - 127), one byte s; s = 255 makes all of them NaN.
+ *   A matrix is rows x k, k the dimension its products sum over. Its data is one buffer of
+ *   psgd_mx_bytes(rows, k) bytes, 16-byte aligned; with P = ceil(k / 128) panels and G = ceil(rows / 64):
+ *     codes   byte (p rows + r) 64 + i, p < P, r < rows, i < 64: elements 128 p + 2 i (low nibble), + 1
+ *     scales  behind them, byte ((p G + r / 64) 64 + 16 g + r % 16) 4 + r / 16 % 4: elements
+ *             128 p + 32 g .. + 31 of row r, g < 4
+ *   Elements at or beyond k are 0 with s = 1. 0 <= rows, k <= 2^25.
+ *
+ * psgd_mx_quantize: x (m x n, row-major, fp16, bf16 or fp32, any leading dimension >= n) to `row` (m x n,
+ *   blocks along the rows) and to `col` (x transposed, n x m, blocks along the columns); either may be
+ *   NULL. x is read once. With e the exponent of a block's largest magnitude a:
+ *     PSGD_NEAREST     s = 127 + e - 2, or e - 1 from a = 1.75 2^e on; to nearest even, magnitudes up to 7
+ *                      to the 6: every element is off by at most half a step
+ *     PSGD_STOCHASTIC  e - 1 past a = 1.5 2^e: nothing exceeds 6, the expectation is the value (to 2^-23 of
+ *                      a step)
+ *   s >= 1. A block that holds an infinity or NaN gets s = 255 and codes 0.
+ *   seed, step_dev (NULL: 0) are not read with PSGD_NEAREST. Two neighbours of a row share a hash; the
+ *   two directions share their bits.
+ * psgd_mx_dequantize: the values, rounded to any type (bf16 and fp32 hold them, but for 2^128, to which
+ *   magnitudes near fp32's largest round), out row-major, ld_out >= k.
+ * psgd_mx_product: C (m x n, fp16, bf16 or fp32, any leading dimension >= n) = s A B^T, a m x k, b n x k,
+ *   summed in fp32 and rounded once; with accumulate != 0 (PSGD_F32 only) C += s A B^T. scale: one fp32 on
+ *   the device, NULL: 1. Sums run in a fixed order, which the sizes determine.
+ *   workspace: psgd_mx_product_workspace(m, n, k) bytes of device memory (0 for most sizes, workspace may
+ *   then be NULL), 16-byte aligned, contents ignored and overwritten; calls that may overlap need one each.
+ * Pointers to elements need their type's alignment. Outputs must not overlap inputs. All buffers live on
+ * the ctx's device. Asynchronous on stream, no allocation.
+ */
+typedef struct psgd_mx_tensor {
+  void* data;
+  int64_t rows, k;
+} psgd_mx_tensor;
+
+psgd_status psgd_mx_bytes(int64_t rows, int64_t k, int64_t* bytes);
+psgd_status psgd_mx_quantize(psgd_ctx* ctx, const void* x, int64_t ld_x, int64_t m, int64_t n, psgd_dtype x_dtype,
+                             const psgd_mx_tensor* row, const psgd_mx_tensor* col, psgd_rounding rounding, uint64_t seed,
+                             const int32_t* step_dev, hipStream_t stream);
+psgd_status psgd_mx_dequantize(psgd_ctx* ctx, const psgd_mx_tensor* a, void* out, int64_t ld_out, psgd_dtype out_dtype,
+                               hipStream_t stream);
+psgd_status psgd_mx_product_workspace(int64_t m, int64_t n, int64_t k, int64_t* bytes);
+psgd_status psgd_mx_product(psgd_ctx* ctx, const psgd_mx_tensor* a, const psgd_mx_tensor* b, const float* scale, void* c,
+                            int64_t ld_c, psgd_dtype c_dtype, int accumulate, void* workspace, int64_t workspace_bytes,
+                            hipStream_t stream);
+
+/*
  * One whole step (psgd_compress, psgd_check_finite without the host copy, then
  * psgd_decompress_update) on a group given by its descriptors, with no plan and no device
  * allocation: for callers that cannot allocate (code under HIP graph capture, tight serving

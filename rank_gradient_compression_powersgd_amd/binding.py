@@ -18,6 +18,8 @@ PSGD_OK, PSGD_EINVAL, PSGD_EDTYPE, PSGD_ENOMEM, PSGD_EHIP, PSGD_EUNSUPPORTED = r
 PSGD_F16, PSGD_BF16, PSGD_F32 = 1, 2, 3
 PSGD_NS_FAST, PSGD_NS_ACCURATE = 0, 1
 PSGD_I32, PSGD_I64 = 4, 8
+PSGD_NEAREST, PSGD_STOCHASTIC = 0, 1
+PSGD_STATE_F32, PSGD_STATE_BYTE = 0, 1
 STATUS_NAMES = {0: "PSGD_OK", 1: "PSGD_EINVAL", 2: "PSGD_EDTYPE", 3: "PSGD_ENOMEM",
                 4: "PSGD_EHIP", 5: "PSGD_EUNSUPPORTED"}
 
@@ -79,6 +81,15 @@ class psgd_muon_hparams(ctypes.Structure):
 
 class psgd_muon_matrix(ctypes.Structure):
     _fields_ = [("param", ctypes.c_void_p), ("ld_param", ctypes.c_int64), ("momentum", ctypes.c_void_p)]
+
+
+class psgd_adamw_tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m1", ctypes.c_void_p), ("m2", ctypes.c_void_p),
+                ("e1", ctypes.c_void_p), ("e2", ctypes.c_void_p), ("numel", ctypes.c_int64)]
+
+
+class psgd_mx_tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("k", ctypes.c_int64)]
 
 
 class PsgdError(RuntimeError):
@@ -149,7 +160,20 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.psgd_embed_grad_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
     lib.psgd_embed_grad.argtypes = [vp, vp, i64, ctypes.c_int, vp, ctypes.c_int, i64, i64, i64, ctypes.c_float,
                                     vp, i64, ctypes.c_int, vp, i64, vp]
-    for name in ("psgd_ns_plan_create", "psgd_ns_plan_destroy", "psgd_newton_schulz", "psgd_muon_attach",
+    u64, cint, mxp = ctypes.c_uint64, ctypes.c_int, ctypes.POINTER(psgd_mx_tensor)
+    lib.psgd_adamw_plan_create.argtypes = [vp, ctypes.POINTER(psgd_adamw_tensor), cint, cint, cint, cint, ctypes.POINTER(vp)]
+    lib.psgd_adamw_plan_destroy.argtypes = [vp]
+    lib.psgd_adamw_prepare.argtypes = [vp, vp, ctypes.c_float, vp, vp, vp, vp, vp]
+    lib.psgd_adamw_update.argtypes = [vp, vp, vp, vp, vp, ctypes.POINTER(psgd_adam_hparams), cint, u64, vp]
+    lib.psgd_adamw_moments.argtypes = [vp, vp, vp, vp, vp, i64, vp, vp, cint, vp]
+    lib.psgd_mx_bytes.argtypes = [i64, i64, ctypes.POINTER(i64)]
+    lib.psgd_mx_quantize.argtypes = [vp, vp, i64, i64, i64, cint, mxp, mxp, cint, u64, vp, vp]
+    lib.psgd_mx_dequantize.argtypes = [vp, mxp, vp, i64, cint, vp]
+    lib.psgd_mx_product_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
+    lib.psgd_mx_product.argtypes = [vp, mxp, mxp, vp, vp, i64, cint, cint, vp, i64, vp]
+    for name in ("psgd_adamw_plan_create", "psgd_adamw_plan_destroy", "psgd_adamw_prepare", "psgd_adamw_update",
+                 "psgd_adamw_moments", "psgd_mx_bytes", "psgd_mx_quantize", "psgd_mx_dequantize", "psgd_mx_product_workspace",
+                 "psgd_mx_product", "psgd_ns_plan_create", "psgd_ns_plan_destroy", "psgd_newton_schulz", "psgd_muon_attach",
                  "psgd_muon_update", "psgd_embed_lookup", "psgd_embed_grad_workspace", "psgd_embed_grad",
                  "psgd_create", "psgd_destroy", "psgd_plan_create", "psgd_plan_destroy",
                  "psgd_compress", "psgd_check_finite", "psgd_decompress_update",
@@ -575,6 +599,18 @@ def psgd_embed_grad_workspace(n: int, vocab: int, dim: int) -> int:
     return out.value
 
 
+def _workspace(need: int, device, stream):
+    """Device memory for one call, allocated on the stream that uses it, so that it is not handed out earlier."""
+    import torch
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    s = stream
+    if isinstance(stream, int):
+        s = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(s):
+        return torch.empty(need, dtype=torch.uint8, device=device)
+
+
 def psgd_embed_grad(ctx: int, dx, ids, dtable, scale: float = 1.0, accumulate: bool = False, workspace=None,
                     stream=None) -> None:
     """dtable[v] = (accumulate: dtable[v] +) scale * sum of dx[t] over the tokens with ids[t] = v.
@@ -592,21 +628,152 @@ def psgd_embed_grad(ctx: int, dx, ids, dtable, scale: float = 1.0, accumulate: b
     dt, it = _dtype(dx, call), _ids(ids, call)
     _same_device(call, dx, ids, dtable, *([] if workspace is None else [workspace]), ctx=ctx)
     if workspace is None:
-        need = psgd_embed_grad_workspace(n, vocab, dim)
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dtable.device)
-        else:
-            # allocated on the stream that uses it, so that its memory is not handed out earlier
-            s = stream
-            if isinstance(stream, int):
-                s = torch.cuda.ExternalStream(stream, dtable.device) if stream else torch.cuda.default_stream(dtable.device)
-            with torch.cuda.stream(s):
-                workspace = torch.empty(need, dtype=torch.uint8, device=dtable.device)
+        workspace = _workspace(psgd_embed_grad_workspace(n, vocab, dim), dtable.device, stream)
     elif not workspace.is_contiguous():
         raise PsgdError(call, PSGD_EINVAL, "workspace must be contiguous")
     _check(ctx, call, load_library().psgd_embed_grad(
         ctx, _ptr(dx), ld_dx, dt, _ptr(ids), it, n, vocab, dim, float(scale), _ptr(dtable), ld_dt, int(accumulate),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream, dtable.device.index)))
+
+
+def _rounding(stochastic: bool) -> int:
+    return PSGD_STOCHASTIC if stochastic else PSGD_NEAREST
+
+
+def make_adamw_tensor(param, grad, m1, m2, e1=None, e2=None) -> psgd_adamw_tensor:
+    """psgd_adamw_tensor over contiguous torch tensors: param and grad of one size; m1 and m2 fp32, or uint8
+    codes with the exponents e1 and e2, of that size rounded up to groups of 64."""
+    import torch
+    call = "psgd_adamw_plan_create"
+    n = param.numel()
+    room = (n + 63) // 64 * 64
+    if grad.numel() != n:
+        raise PsgdError(call, PSGD_EINVAL, "param and grad must have one size")
+    for name, t, want, dtype in (("param", param, n, None), ("grad", grad, n, None),
+                                 ("m1", m1, room, torch.float32 if e1 is None else torch.uint8),
+                                 ("m2", m2, room, torch.float32 if e1 is None else torch.uint8),
+                                 ("e1", e1, room // 64, torch.uint8), ("e2", e2, room // 64, torch.uint8)):
+        if t is None and e1 is None and e2 is None:
+            continue
+        if t is None or not t.is_contiguous() or t.numel() < want:
+            raise PsgdError(call, PSGD_EINVAL, f"{name} must be contiguous with at least {want} elements")
+        if dtype is not None and t.dtype != dtype:
+            raise PsgdError(call, PSGD_EDTYPE, f"{name} must be {dtype}, got {t.dtype}")
+    return psgd_adamw_tensor(_ptr(param), _ptr(grad), _ptr(m1), _ptr(m2), _ptr(e1), _ptr(e2), n)
+
+
+def psgd_adamw_plan_create(ctx: int, tensors: Sequence[psgd_adamw_tensor], param_dtype: int, grad_dtype: int, state: int) -> int:
+    arr = (psgd_adamw_tensor * max(1, len(tensors)))(*tensors)
+    h = ctypes.c_void_p()
+    _check(ctx, "psgd_adamw_plan_create", load_library().psgd_adamw_plan_create(
+        ctx, arr, len(tensors), param_dtype, grad_dtype, state, ctypes.byref(h)))
+    return h.value
+
+
+def psgd_adamw_plan_destroy(plan: int) -> None:
+    load_library().psgd_adamw_plan_destroy(plan)
+
+
+def psgd_adamw_prepare(ctx: int, plan: int, max_norm: float, skip_in, skip_dev, step_dev, norm_dev, stream=None) -> None:
+    """Skip word, step count, norm and clipping factor of a step from the list's gradients (skip_in: a skip word
+    decided before, or None), on the current stream of the context's device by default."""
+    _check(ctx, "psgd_adamw_prepare", load_library().psgd_adamw_prepare(
+        ctx, plan, float(max_norm), _ptr(skip_in), _ptr(skip_dev), _ptr(step_dev), _ptr(norm_dev),
+        _stream(stream, _ctx_device.get(ctx))))
+
+
+def psgd_adamw_update(ctx: int, plan: int, skip_dev, step_dev, norm_dev, hp, stochastic: bool = False, seed: int = 0,
+                      stream=None) -> None:
+    """One AdamW step of the plan's list (norm_dev may be None: no clipping)."""
+    h = _hparams(hp)
+    _check(ctx, "psgd_adamw_update", load_library().psgd_adamw_update(
+        ctx, plan, _ptr(skip_dev), _ptr(step_dev), _ptr(norm_dev), ctypes.byref(h), _rounding(stochastic),
+        seed & 0xFFFFFFFFFFFFFFFF, _stream(stream, _ctx_device.get(ctx))))
+
+
+def psgd_adamw_moments(ctx: int, m1, e1, m2, e2, out1, out2, stream=None) -> None:
+    """The values of 8-bit moments (contiguous uint8 codes and exponents) in fp32 or bf16 tensors."""
+    import torch
+    call = "psgd_adamw_moments"
+    n = out1.numel()
+    room = (n + 63) // 64 * 64
+    if any(not t.is_contiguous() for t in (m1, e1, m2, e2, out1, out2)) or out2.numel() != n or out2.dtype != out1.dtype:
+        raise PsgdError(call, PSGD_EINVAL, "all must be contiguous, the outputs of one size and type")
+    if any(t.dtype != torch.uint8 for t in (m1, e1, m2, e2)):
+        raise PsgdError(call, PSGD_EDTYPE, "codes and exponents must be uint8")
+    if min(m1.numel(), m2.numel()) < room or min(e1.numel(), e2.numel()) < room // 64:
+        raise PsgdError(call, PSGD_EINVAL, f"{n} values need {room} codes and {room // 64} exponents")
+    _same_device(call, m1, e1, m2, e2, out1, out2, ctx=ctx)
+    _check(ctx, call, load_library().psgd_adamw_moments(
+        ctx, _ptr(m1), _ptr(e1), _ptr(m2), _ptr(e2), n, _ptr(out1), _ptr(out2), _dtype(out1, call),
+        _stream(stream, m1.device.index)))
+
+
+def psgd_mx_bytes(rows: int, k: int) -> int:
+    """Bytes of a rows x k matrix in microscaled 4-bit elements."""
+    out = ctypes.c_int64()
+    _check(None, "psgd_mx_bytes", load_library().psgd_mx_bytes(rows, k, ctypes.byref(out)))
+    return out.value
+
+
+def _mx(t):
+    return None if t is None else ctypes.byref(psgd_mx_tensor(_ptr(t.data), t.rows, t.k))
+
+
+def psgd_mx_quantize(ctx: int, x, row=None, col=None, stochastic: bool = False, seed: int = 0, step=None, stream=None) -> None:
+    """x (2-D, unit row stride, fp16, bf16 or fp32) to the MxTensor row (x's shape) and, transposed, to col.
+    step: one-element int32 device tensor mixed into the random bits, or None."""
+    import torch
+    call = "psgd_mx_quantize"
+    if x.dim() != 2:
+        raise PsgdError(call, PSGD_EINVAL, "x must be a 2-D tensor")
+    if step is not None and step.dtype != torch.int32:
+        raise PsgdError(call, PSGD_EDTYPE, "step must be int32")
+    m, n = x.shape
+    _same_device(call, x, *[t.data for t in (row, col) if t is not None], *([] if step is None else [step]), ctx=ctx)
+    _check(ctx, call, load_library().psgd_mx_quantize(
+        ctx, _ptr(x), _row_stride(x, call), m, n, _dtype(x, call), _mx(row), _mx(col), _rounding(stochastic),
+        seed & 0xFFFFFFFFFFFFFFFF, _ptr(step), _stream(stream, x.device.index)))
+
+
+def psgd_mx_dequantize(ctx: int, a, out, stream=None) -> None:
+    """out (rows x k, unit row stride) = the values of the MxTensor a."""
+    call = "psgd_mx_dequantize"
+    if tuple(out.shape) != (a.rows, a.k):
+        raise PsgdError(call, PSGD_EINVAL, f"out must be {a.rows} x {a.k}")
+    _same_device(call, out, a.data, ctx=ctx)
+    _check(ctx, call, load_library().psgd_mx_dequantize(ctx, _mx(a), _ptr(out), _row_stride(out, call), _dtype(out, call),
+                                                        _stream(stream, out.device.index)))
+
+
+def psgd_mx_product_workspace(m: int, n: int, k: int) -> int:
+    """Bytes of device workspace of psgd_mx_product (0 for most sizes)."""
+    out = ctypes.c_int64()
+    _check(None, "psgd_mx_product_workspace", load_library().psgd_mx_product_workspace(m, n, k, ctypes.byref(out)))
+    return out.value
+
+
+def psgd_mx_product(ctx: int, a, b, out, scale=None, accumulate: bool = False, workspace=None, stream=None) -> None:
+    """out (a.rows x b.rows) = scale * A B^T of two MxTensors of one k, or added to an fp32 out. scale: one-element
+    fp32 device tensor or None; workspace: a contiguous device tensor of at least psgd_mx_product_workspace(...)
+    bytes, allocated for the call on its stream when None."""
+    import torch
+    call = "psgd_mx_product"
+    if tuple(out.shape) != (a.rows, b.rows):
+        raise PsgdError(call, PSGD_EINVAL, f"out must be {a.rows} x {b.rows}")
+    if scale is not None and (scale.dtype != torch.float32 or scale.numel() < 1):
+        raise PsgdError(call, PSGD_EDTYPE, "scale must be one float32")
+    _same_device(call, out, a.data, b.data, *[t for t in (scale, workspace) if t is not None], ctx=ctx)
+    ld, dt = _row_stride(out, call), _dtype(out, call)
+    if workspace is None:
+        need = psgd_mx_product_workspace(a.rows, b.rows, a.k)
+        if need:
+            workspace = _workspace(need, out.device, stream)
+    elif not workspace.is_contiguous():
+        raise PsgdError(call, PSGD_EINVAL, "workspace must be contiguous")
+    _check(ctx, call, load_library().psgd_mx_product(
+        ctx, _mx(a), _mx(b), _ptr(scale), _ptr(out), ld, dt, int(accumulate), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream, out.device.index)))
 
 
 def psgd_last_error(ctx: int) -> str:

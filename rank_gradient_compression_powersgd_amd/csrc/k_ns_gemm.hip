@@ -20,6 +20,7 @@
 // their first loads.
 #include <type_traits>
 
+#include "lds_load.h"
 #include "ns.h"
 
 namespace psgd {
@@ -29,7 +30,6 @@ constexpr int KB = 32;                         // k per stage
 constexpr int RING = 4;                        // stages in LDS
 
 typedef short i16x4 __attribute__((ext_vector_type(4)));
-#define LDS __attribute__((address_space(3)))
 __device__ __forceinline__ i16x4 lds_read_tr16(const uint16_t* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(p));
 }
@@ -42,21 +42,6 @@ __device__ __forceinline__ int swz_outer(int k, int q) { return q ^ (((k >> 3) &
 // K-contiguous rows are 64 bytes (4 units): 8 consecutive rows put one logical unit on the 8
 // distinct 16-byte groups of one LDS pass.
 __device__ __forceinline__ int swz_inner(int row, int q) { return q ^ ((row >> 1) & 3); }
-
-// 16 bytes per lane from base + off (bytes) straight to LDS: lane x writes at l + 16 x. As asm, since
-// with the builtin the compiler waits for every such load before each transposing LDS read; the
-// waits are written out below (wait_loads). The load has no register output.
-__device__ __forceinline__ void load_lds16(const GLOBAL uint16_t* base, uint32_t off, uint32_t l) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(l), "v"(off), "s"(base) : "m0", "memory");
-}
-
-// All but the wave's n newest loads have landed, and its LDS reads have been answered. The builtin
-// rather than asm: the compiler then knows that the fragments are there. The empty asm keeps LDS
-// reads from moving across.
-template <int N> __device__ __forceinline__ void wait_loads() {
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
-  asm volatile("" ::: "memory");
-}
 
 __device__ __forceinline__ float h2f(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
 __device__ __forceinline__ f32x4 h2f4(u32x2 v) { return __builtin_convertvector(__builtin_bit_cast(f16x4, v), f32x4); }

@@ -12,8 +12,7 @@
 #include <string>
 #include <vector>
 
-#include "../../include/psgd.h"
-#include "psgd_internal.h"
+#include "ctx.h"
 #include "embed.h"
 #include "ns.h"
 
@@ -28,17 +27,6 @@ int decomp_tile_n();
 
 using psgd::DevMat;
 using psgd::Work;
-
-struct psgd_plan;
-
-struct psgd_ctx {
-  int device = 0;
-  int rank = 0;
-  std::string err;
-  std::vector<hipEvent_t> events;   // tracing hook: 2 per slot, empty when off
-  char* scratch = nullptr;          // device address of this device's static scratch array
-  std::unique_ptr<psgd_plan> noalloc_plan;   // host side of psgd_step_noalloc's transient plan
-};
 
 // ------------------------------------------------------------------------------------------
 // Static device scratch for psgd_step_noalloc: the workspace, descriptor table and work lists
@@ -99,24 +87,6 @@ struct psgd_ns_plan {
 
 namespace {
 
-psgd_status fail(psgd_ctx* ctx, psgd_status st, const char* fmt, ...) __attribute__((format(printf, 3, 4)));
-psgd_status fail(psgd_ctx* ctx, psgd_status st, const char* fmt, ...) {
-  if (ctx) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    ctx->err = buf;
-  }
-  return st;
-}
-
-psgd_status hip_fail(psgd_ctx* ctx, hipError_t e, const char* what) {
-  (void)hipGetLastError();               // reported here: the next call's launches find none
-  return fail(ctx, PSGD_EHIP, "%s: %s", what, hipGetErrorString(e));
-}
-
 enum Slot { S_ZERO_FLAGS, S_K1, S_GRAM, S_FACTOR, S_APPLY, S_K2, S_ZERO_SKIP, S_CHECK,
             S_K3, S_REDUCE, S_SPLIT3, S_REORTH, S_ADAM_NORM, S_K3_ADAM, S_ADAM_PASS, S_SLOTS };
 constexpr int kMaxPassItems = 8192;      // norm items of pass-through gradients per call
@@ -132,15 +102,6 @@ hipError_t traced(psgd_ctx* ctx, int slot, hipStream_t s, F&& launch) {
   if (e != hipSuccess || ctx->events.empty()) return e;
   return hipEventRecord(ctx->events[2 * slot + 1], s);
 }
-
-#define HIPCHK(ctx, expr, what)                         \
-  do {                                                  \
-    hipError_t e_ = (expr);                             \
-    if (e_ != hipSuccess) return hip_fail(ctx, e_, what); \
-  } while (0)
-
-inline int64_t rup(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace
 
@@ -967,15 +928,6 @@ psgd_status check_pass_tensors(psgd_ctx* ctx, const psgd_adam_tensor* pass, int 
 psgd::AdamArgs adam_args(const psgd_adam_hparams* hp, const int32_t* step, const float* norm) {
   return psgd::AdamArgs{hp->lr, hp->beta1, hp->beta2, hp->eps, hp->weight_decay, step, norm + 1};
 }
-psgd_status check_hparams(psgd_ctx* ctx, const psgd_adam_hparams* hp) {
-  if (!hp) return fail(ctx, PSGD_EINVAL, "hyperparameters are required");
-  if (!(hp->beta1 >= 0.0f && hp->beta1 < 1.0f) || !(hp->beta2 >= 0.0f && hp->beta2 < 1.0f))
-    return fail(ctx, PSGD_EINVAL, "betas must lie in [0, 1)");
-  if (!(hp->eps >= 0.0f) || !(hp->lr >= 0.0f) || !(hp->weight_decay >= 0.0f) ||
-      !std::isfinite(hp->eps) || !std::isfinite(hp->lr) || !std::isfinite(hp->weight_decay))
-    return fail(ctx, PSGD_EINVAL, "lr, eps and weight_decay must be finite and >= 0");
-  return PSGD_OK;
-}
 }  // namespace
 
 psgd_status psgd_adam_prepare(psgd_ctx* ctx, psgd_plan* plan, const psgd_adam_tensor* pass, int n_pass,
@@ -1055,29 +1007,6 @@ psgd_status psgd_adam_update(psgd_ctx* ctx, const psgd_adam_tensor* pass, int n_
 namespace {
 
 constexpr int64_t kMaxNsDim = 1 << 22;   // rows of a tile are addressed by 32-bit byte offsets
-
-// Makes a context's device current for one call and gives the caller's back.
-struct DeviceGuard {
-  int prev = -1;
-  hipError_t err;
-  explicit DeviceGuard(int device) {
-    err = hipGetDevice(&prev);
-    if (err == hipSuccess && prev != device) err = hipSetDevice(device);
-    else prev = -1;
-  }
-  ~DeviceGuard() { if (prev >= 0) (void)hipSetDevice(prev); }
-};
-
-int grad_type(psgd_dtype dt) {
-  switch (dt) {
-    case PSGD_F16: return psgd::G_F16;
-    case PSGD_BF16: return psgd::G_BF16;
-    case PSGD_F32: return psgd::G_F32;
-  }
-  return 0;
-}
-int type_size(int gt) { return gt == psgd::G_F32 ? 4 : 2; }
-bool aligned_to(const void* p, int size) { return reinterpret_cast<uintptr_t>(p) % size == 0; }
 
 psgd_status check_ns(psgd_ctx* ctx, const psgd_ns_hparams& h) {
   if (!std::isfinite(h.a) || !std::isfinite(h.b) || !std::isfinite(h.c))

@@ -1,0 +1,199 @@
+"""AdamW over a list of tensors with moments in 8 or 32 bits, microscaled 4-bit matrices, and a linear layer
+on them whose weight gradient goes into a PowerSGD error buffer. All compute happens in libpsgd.so.
+"""
+from __future__ import annotations
+
+from typing import Optional, Sequence
+
+from . import binding as B
+
+GROUP = 64                                   # elements under one exponent byte of the 8-bit moments
+
+
+class AdamWGroup:
+    """Tensors stepped together by AdamW.
+
+    params, grads: lists of contiguous device tensors, one grad per param and of its size, each list of
+                   one dtype (fp16, bf16 or fp32). The buffers are captured; the caller fills grads.
+    bits: 8 (codes under an exponent per 64 elements) or 32, of both moments
+    stochastic: stochastic rounding of 8-bit moments and 16-bit params, by bits hashed from `seed`, the
+                step and the element. Default: with 8 bits, which rounding to nearest leaves standing still
+    moments: state to continue from, as `state()` gives it (kept and updated in place); default zeros
+
+    m1, m2 (and e1, e2): flat state, every tensor's part starting at a group of 64 (`offsets`)
+    step_count, skip, norm: device words of the last step (t; 1 where it was skipped; norm, clipping factor)
+    """
+
+    def __init__(self, params: Sequence, grads: Sequence, bits: int = 8, stochastic: Optional[bool] = None, seed: int = 0,
+                 moments: Optional[Sequence] = None):
+        import torch
+        call = "psgd_adamw_plan_create"
+        self.ctx = self.plan = None
+        self.params, self.grads = list(params), list(grads)
+        if not self.params or len(self.params) != len(self.grads):
+            raise B.PsgdError(call, B.PSGD_EINVAL, "need one grad per param, and at least one")
+        if bits not in (8, 32):
+            raise B.PsgdError(call, B.PSGD_EINVAL, f"moments have 8 or 32 bits, not {bits}")
+        for ts in (self.params, self.grads):
+            if any(t.dtype != ts[0].dtype for t in ts):
+                raise B.PsgdError(call, B.PSGD_EDTYPE, "params and grads must each have one dtype")
+        pt, gt = B._dtype(self.params[0], call), B._dtype(self.grads[0], call)
+        self.bits, self.seed = bits, seed
+        self.stochastic = bits == 8 if stochastic is None else bool(stochastic)
+        dev = self.device = self.params[0].device
+        self.offsets, room = [], 0
+        for p in self.params:
+            self.offsets.append(room)
+            room += (p.numel() + GROUP - 1) // GROUP * GROUP
+        if moments is None:
+            kind = torch.uint8 if bits == 8 else torch.float32
+            moments = [torch.zeros(room, dtype=kind, device=dev) for _ in range(2)]
+            if bits == 8:
+                moments += [torch.zeros(room // GROUP, dtype=torch.uint8, device=dev) for _ in range(2)]
+        moments = list(moments)
+        if len(moments) != (4 if bits == 8 else 2):
+            raise B.PsgdError(call, B.PSGD_EINVAL, "moments are (m1, m2, e1, e2) with 8 bits, (m1, m2) with 32")
+        for t, want in zip(moments, (room, room, room // GROUP, room // GROUP)):
+            if t.dim() != 1 or t.numel() != want:
+                raise B.PsgdError(call, B.PSGD_EINVAL, f"moments must be flat: {room} values, {room // GROUP} exponents")
+        self.m1, self.m2 = moments[:2]
+        self.e1, self.e2 = moments[2:] if bits == 8 else (None, None)
+        B._same_device(call, *self.params, *self.grads, *moments)
+        part = lambda t, o, n: t[o:o + (n + GROUP - 1) // GROUP * GROUP]  # noqa: E731
+        ts = [B.make_adamw_tensor(p, g, part(self.m1, o, p.numel()), part(self.m2, o, p.numel()),
+                                  *([self.e1[o // GROUP:], self.e2[o // GROUP:]] if bits == 8 else []))
+              for p, g, o in zip(self.params, self.grads, self.offsets)]
+        self.step_count = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.skip = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.norm = torch.zeros(2, dtype=torch.float32, device=dev)
+        self.ctx = B.psgd_create(dev.index or 0, 1)
+        self.plan = B.psgd_adamw_plan_create(self.ctx, ts, pt, gt, B.PSGD_STATE_BYTE if bits == 8 else B.PSGD_STATE_F32)
+
+    def step(self, hp, max_norm: float = 0.0, skip=None, stream=None):
+        """One step: skip word, norm and clipping factor from the gradients, then the update. skip: a skip word
+        decided before (PowerSGDGroup.skip, where the gradients are its decompressed ones), or None."""
+        if skip is not None:
+            B._same_device("psgd_adamw_prepare", self.skip, skip, ctx=self.ctx)
+        stream = B._stream(stream, self.device)
+        B.psgd_adamw_prepare(self.ctx, self.plan, max_norm, skip, self.skip, self.step_count, self.norm, stream)
+        B.psgd_adamw_update(self.ctx, self.plan, self.skip, self.step_count, self.norm, hp, self.stochastic, self.seed, stream)
+
+    def state(self):
+        """The moments, for the constructor's `moments`; step_count belongs to a checkpoint as well."""
+        return (self.m1, self.m2, self.e1, self.e2) if self.bits == 8 else (self.m1, self.m2)
+
+    def moments(self, dtype=None, stream=None):
+        """The moments' values, flat: new bf16 (or fp32) tensors of 8-bit moments, the fp32 ones themselves."""
+        import torch
+        if self.bits == 32:
+            return self.m1, self.m2
+        out = [torch.empty(self.m1.numel(), dtype=dtype or torch.bfloat16, device=self.device) for _ in range(2)]
+        if out[0].numel():
+            B.psgd_adamw_moments(self.ctx, self.m1, self.e1, self.m2, self.e2, *out, B._stream(stream, self.device))
+        return out[0], out[1]
+
+    def close(self):
+        if getattr(self, "plan", None):
+            B.psgd_adamw_plan_destroy(self.plan)
+            self.plan = None
+        if getattr(self, "ctx", None):
+            B.psgd_destroy(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class MxTensor:
+    """A rows x k matrix in microscaled 4-bit elements, k the dimension its products sum over: `data`, one
+    buffer of psgd_mx_bytes(rows, k) bytes, filled by psgd_mx_quantize."""
+
+    def __init__(self, rows: int, k: int, device=None, data=None):
+        import torch
+        self.rows, self.k = int(rows), int(k)
+        need = B.psgd_mx_bytes(self.rows, self.k)
+        if data is None:
+            data = torch.empty(need, dtype=torch.uint8, device=device or "cuda")
+        elif data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() < need:
+            raise B.PsgdError("psgd_mx_bytes", B.PSGD_EINVAL, f"data must be {need} contiguous bytes")
+        self.data = data
+
+
+class MxLinear:
+    """A linear layer y = x W whose three products run on 4-bit operands.
+
+    weight: in x out device tensor (fp16, bf16 or fp32). Its 4-bit forms are made here and by refresh(),
+            which follows every step on the weight
+    seed: of the stochastic rounding of the output's gradient; another one for every layer
+
+    Runs on the current stream of the weight's device.
+    """
+
+    def __init__(self, weight, seed: int = 0):
+        self.ctx = None
+        if weight.dim() != 2 or min(weight.shape) < 1:
+            raise B.PsgdError("psgd_mx_quantize", B.PSGD_EINVAL, "weight must be an in x out tensor")
+        B._dtype(weight, "psgd_mx_quantize")
+        B._same_device("psgd_mx_quantize", weight)
+        self.weight, self.seed, self.device = weight, seed, weight.device
+        self.n_in, self.n_out = weight.shape
+        self.w_row = MxTensor(self.n_in, self.n_out, self.device)
+        self.w_col = MxTensor(self.n_out, self.n_in, self.device)
+        self.x_col = None
+        self.ctx = B.psgd_create(self.device.index or 0, 1)
+        self.refresh()
+
+    def refresh(self):
+        """4-bit forms of the weight as it is now."""
+        B.psgd_mx_quantize(self.ctx, self.weight, self.w_row, self.w_col)
+
+    def _tokens(self, t, width, name):
+        if t.shape[-1:] != (width,) or t.dim() < 2:
+            raise B.PsgdError("psgd_mx_quantize", B.PSGD_EINVAL, f"{name} must hold one row of {width} values per token")
+        return t if t.dim() == 2 else t.reshape(-1, width)
+
+    def forward(self, x, train: bool = True):
+        """y = x W, in x's dtype; x [..., in] to nearest. With train, x's 4-bit transpose is kept for backward()."""
+        import torch
+        x2 = self._tokens(x, self.n_in, "x")
+        t = x2.shape[0]
+        row = MxTensor(t, self.n_in, self.device)
+        col = MxTensor(self.n_in, t, self.device) if train else None
+        y = torch.empty(*x.shape[:-1], self.n_out, dtype=x.dtype, device=self.device)
+        B.psgd_mx_quantize(self.ctx, x2, row, col)
+        B.psgd_mx_product(self.ctx, row, self.w_col, y.view(t, self.n_out))
+        if train:
+            self.x_col = col
+        return y
+
+    def backward(self, dy, err=None, scale=None, step=None):
+        """dx = dy W^T, in dy's dtype, and err += scale x^T dy (err: in x out fp32, the error buffer of an
+        in-place matrix of a PowerSGDGroup; scale: its one-element fp32 multiplier, or None). dy is rounded
+        stochastically by seed and step (one-element int32 device tensor, which the caller advances, or None)."""
+        import torch
+        dy2 = self._tokens(dy, self.n_out, "dy")
+        t = dy2.shape[0]
+        if err is not None and (self.x_col is None or self.x_col.k != t):
+            raise B.PsgdError("psgd_mx_product", B.PSGD_EINVAL, "backward() needs the forward() of the same tokens before it")
+        row = MxTensor(t, self.n_out, self.device)
+        col = MxTensor(self.n_out, t, self.device) if err is not None else None
+        dx = torch.empty(*dy.shape[:-1], self.n_in, dtype=dy.dtype, device=self.device)
+        B.psgd_mx_quantize(self.ctx, dy2, row, col, stochastic=True, seed=self.seed, step=step)
+        B.psgd_mx_product(self.ctx, row, self.w_row, dx.view(t, self.n_in))
+        if err is not None:
+            B.psgd_mx_product(self.ctx, self.x_col, col, err, scale=scale, accumulate=True)
+        return dx
+
+    def close(self):
+        if getattr(self, "ctx", None):
+            B.psgd_destroy(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
