@@ -3,6 +3,7 @@
 //
 // P is B (the columns i of C), Q is A (its rows j): a lane then holds C[j][i .. i + 3], consecutive in a
 // row of C.
+#include <algorithm>
 #include <type_traits>
 #include <utility>
 
@@ -29,13 +30,73 @@ template <int SP, int SQ> __device__ __forceinline__ f32x4 mfma_mx(u32x4 p, u32x
                                                           __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1), c, 4, 4, SP, (int)sp, SQ, (int)sq);
 }
 
+// The same with sum I of a tile of N x N in the accumulation registers 4 I .. 4 I + 3; NEW: what the sum
+// held is not read. As asm, since the compiler keeps sums of this many registers in ordinary ones, with
+// a move for every use, and on registers by name: every statement marks all of the tile's as written, so
+// the compiler keeps nothing of its own there and never moves a sum. Consecutive uses of one sum are a
+// whole row of MFMAs apart; settle() stands between the last of them and the first read of a sum.
+#define MX_A10(p) "a" #p "0", "a" #p "1", "a" #p "2", "a" #p "3", "a" #p "4", "a" #p "5", "a" #p "6", "a" #p "7", "a" #p "8", "a" #p "9"
+#define MX_A16 "a0", "a1", "a2", "a3", "a4", "a5", "a6", "a7", "a8", "a9", "a10", "a11", "a12", "a13", "a14", "a15"
+#define MX_A64 MX_A16, "a16", "a17", "a18", "a19", MX_A10(2), MX_A10(3), MX_A10(4), MX_A10(5), "a60", "a61", "a62", "a63"
+#define MX_A256                                                                                                              \
+  MX_A64, "a64", "a65", "a66", "a67", "a68", "a69", MX_A10(7), MX_A10(8), MX_A10(9), MX_A10(10), MX_A10(11), MX_A10(12),     \
+      MX_A10(13), MX_A10(14), MX_A10(15), MX_A10(16), MX_A10(17), MX_A10(18), MX_A10(19), MX_A10(20), MX_A10(21), MX_A10(22), \
+      MX_A10(23), MX_A10(24), "a250", "a251", "a252", "a253", "a254", "a255"
+#define MX_LINE(LO, HI, Q, C, S0, S1, SP, SQ, B0, B1)                                                             \
+  "v_mfma_scale_f32_16x16x128_f8f6f4 a[%" LO ":%" HI "], %0, %" Q ", " C ", %" SP ", %" SQ " op_sel:[%" S0        \
+  "," B0 ",0] op_sel_hi:[%" S1 "," B1 ",0] cbsz:4 blgp:4\n\t"
+#define MX_I(y) "n"(4 * (I + y)), "n"(4 * (I + y) + 3)
+#define MX_KEEP(LO, HI) "a[%" LO ":%" HI "]"
+#define MX_ZERO(LO, HI) "0"
+#define MX_ROW8(C)                                                                                                 \
+  asm volatile(MX_LINE("12", "13", "1", C("12", "13"), "28", "29", "9", "10", "0", "0")                            \
+               MX_LINE("14", "15", "2", C("14", "15"), "28", "29", "9", "10", "1", "0")                            \
+               MX_LINE("16", "17", "3", C("16", "17"), "28", "29", "9", "10", "0", "1")                            \
+               MX_LINE("18", "19", "4", C("18", "19"), "28", "29", "9", "10", "1", "1")                            \
+               MX_LINE("20", "21", "5", C("20", "21"), "28", "29", "9", "11", "0", "0")                            \
+               MX_LINE("22", "23", "6", C("22", "23"), "28", "29", "9", "11", "1", "0")                            \
+               MX_LINE("24", "25", "7", C("24", "25"), "28", "29", "9", "11", "0", "1")                            \
+               MX_LINE("26", "27", "8", C("26", "27"), "28", "29", "9", "11", "1", "1")                            \
+               ::"v"(p), "v"(q[0]), "v"(q[1]), "v"(q[2]), "v"(q[3]), "v"(q[4]), "v"(q[5]), "v"(q[6]), "v"(q[7]),   \
+               "v"(sp), "v"(sq[0]), "v"(sq[1]), MX_I(0), MX_I(1), MX_I(2), MX_I(3), MX_I(4), MX_I(5), MX_I(6),     \
+               MX_I(7), "n"(SP & 1), "n"(SP >> 1) : MX_A256)
+#define MX_ROW4(C)                                                                                                 \
+  asm volatile(MX_LINE("7", "8", "1", C("7", "8"), "15", "16", "5", "6", "0", "0")                                 \
+               MX_LINE("9", "10", "2", C("9", "10"), "15", "16", "5", "6", "1", "0")                               \
+               MX_LINE("11", "12", "3", C("11", "12"), "15", "16", "5", "6", "0", "1")                             \
+               MX_LINE("13", "14", "4", C("13", "14"), "15", "16", "5", "6", "1", "1")                             \
+               ::"v"(p), "v"(q[0]), "v"(q[1]), "v"(q[2]), "v"(q[3]), "v"(sp), "v"(sq[0]), MX_I(0), MX_I(1),        \
+               MX_I(2), MX_I(3), "n"(SP & 1), "n"(SP >> 1) : MX_A64)
+#define MX_ROW2(C)                                                                                                 \
+  asm volatile(MX_LINE("5", "6", "1", C("5", "6"), "9", "10", "3", "4", "0", "0")                                  \
+               MX_LINE("7", "8", "2", C("7", "8"), "9", "10", "3", "4", "1", "0")                                  \
+               ::"v"(p), "v"(q[0]), "v"(q[1]), "v"(sp), "v"(sq[0]), MX_I(0), MX_I(1), "n"(SP & 1), "n"(SP >> 1) : MX_A16)
+// row I / N of the tile: sums I .. I + N - 1; byte SP of sp is p's exponent, byte y % 4 of sq[y / 4] that of q[y]
+template <int N, int I, int SP, bool NEW> __device__ __forceinline__ void mfma_row(u32x4 p, const u32x4 (&q)[N], uint32_t sp, const uint32_t* sq) {
+  if constexpr (N == 8 && NEW) MX_ROW8(MX_ZERO);
+  else if constexpr (N == 8) MX_ROW8(MX_KEEP);
+  else if constexpr (N == 4 && NEW) MX_ROW4(MX_ZERO);
+  else if constexpr (N == 4) MX_ROW4(MX_KEEP);
+  else if constexpr (NEW) MX_ROW2(MX_ZERO);
+  else MX_ROW2(MX_KEEP);
+}
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+template <int I> __device__ __forceinline__ f32x4 sum_of() {
+  float v0, v1, v2, v3;
+  asm volatile("v_accvgpr_read_b32 %0, a[%4]\n\tv_accvgpr_read_b32 %1, a[%5]\n\tv_accvgpr_read_b32 %2, a[%6]\n\tv_accvgpr_read_b32 %3, a[%7]"
+               : "=v"(v0), "=v"(v1), "=v"(v2), "=v"(v3) : "n"(4 * I), "n"(4 * I + 1), "n"(4 * I + 2), "n"(4 * I + 3));
+  return f32x4{v0, v1, v2, v3};
+}
+
 typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
 typedef _Float16 f16x4_u __attribute__((ext_vector_type(4), aligned(2)));
 typedef __bf16 bf16x4_u __attribute__((ext_vector_type(4), aligned(2)));
+typedef _Float16 f16x8_u __attribute__((ext_vector_type(8), aligned(2)));
+typedef __bf16 bf16x8_u __attribute__((ext_vector_type(8), aligned(2)));
 template <int T> struct Elem;
 template <> struct Elem<G_F32> { typedef float one; typedef f32x4_u four; };
-template <> struct Elem<G_F16> { typedef _Float16 one; typedef f16x4_u four; };
-template <> struct Elem<G_BF16> { typedef __bf16 one; typedef bf16x4_u four; };
+template <> struct Elem<G_F16> { typedef _Float16 one; typedef f16x4_u four; typedef f16x8_u eight; };
+template <> struct Elem<G_BF16> { typedef __bf16 one; typedef bf16x4_u four; typedef bf16x8_u eight; };
 
 // v = C[j][i .. i + 3] of the product, scaled and written or added
 template <int OT> __device__ __forceinline__ void finish(const MxProduct& a, int64_t j, int64_t i, f32x4 v, float scale) {
@@ -115,10 +176,8 @@ void k_mx_few(MxProduct a) {
 
 // ---- tiles ------------------------------------------------------------------------------------------------
 template <int T> struct Tile {
-  static constexpr int WAVES = T == 256 ? 8 : 4;
-  static constexpr int WI = WAVES / 2;                       // waves along i; 2 along j
-  static constexpr int SI = T / WI, SJ = T / 2;              // a wave's sides
-  static constexpr int NI = SI / 16, NJ = SJ / 16;           // in MFMA tiles
+  static constexpr int WAVES = 4;                            // 2 along i, 2 along j
+  static constexpr int S = T / 2, N = S / 16;                // a wave's side, in rows and in MFMA tiles
   static constexpr int CODES = T * kMxRowBytes;              // bytes of an operand's stage
   static constexpr int SCALES = T / kMxGroup * kMxGroupBytes;
   static constexpr int STAGE = 2 * (CODES + SCALES);
@@ -127,155 +186,290 @@ template <int T> struct Tile {
   static constexpr int SLOADS = (WORDS + WAVES - 1) / WAVES; // per wave (some of them twice where a wave has none of its own)
 };
 
-__device__ __forceinline__ int swz(int row, int q) { return q ^ ((row >> 1) & 3); }
-
 __device__ __forceinline__ void load_lds4(const GLOBAL uint8_t* base, uint32_t off, uint32_t l) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(l), "v"(off), "s"(base) : "m0", "memory");
 }
 
+// Which row of P's 64 is row c of MFMA tile x. A lane's results are rows 4 g .. 4 g + 3 of each tile; with
+// PAIRS tiles 2 x and 2 x + 1 give it 8 columns of C in a row, 16 bytes of a 16-bit output, and the four g
+// of a row 64.
+template <bool PAIRS> __device__ __forceinline__ int p_row(int x, int c) {
+  return PAIRS ? 32 * (x >> 1) + 8 * (c >> 2) + 4 * (x & 1) + (c & 3) : 16 * x + c;
+}
+// Place of a row's 16-byte unit q: 8 lanes of one LDS pass, rows of 64 bytes, on 8 distinct places.
+template <bool PAIRS> __device__ __forceinline__ int p_place(int row, int q) {
+  return q ^ (PAIRS ? (row >> 1 & 1) | (row >> 2 & 2) : row >> 1 & 3);
+}
+__device__ __forceinline__ int q_place(int row, int q) { return q ^ (row >> 1 & 3); }
+
+// Workgroups stay: each takes items (a tile, or a part of one's panels) off its XCD's range until there
+// are none. Stages of one panel go straight from L2 to a ring of four LDS buffers (the global addresses
+// carry the places), three stages ahead of their use and on into the next item's. While a stage is
+// multiplied out of registers, the fragments of the next one are read from LDS into the other set and
+// the one after three more is sent for, a few between the rows of MFMAs. One barrier a stage: it says
+// that the next stage has landed for every wave and that every wave has read this one out of the
+// buffer that is then loaded into. An item's results leave while the next one's stages arrive.
 template <int T, int OT, bool SPLIT>
-__global__ __launch_bounds__(Tile<T>::WAVES * kWave, 2)
-void k_mx_gemm(MxProduct a) {
+__global__ __launch_bounds__(Tile<T>::WAVES * kWave, T == 256 ? 1 : 2)
+void k_mx_gemm(MxProduct a, int items) {
   using TL = Tile<T>;
-  constexpr int NI = TL::NI, NJ = TL::NJ;
+  constexpr int N = TL::N;
+  constexpr bool PAIRS = OT != G_F32;
   const int lane = threadIdx.x & (kWave - 1), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane & 15, g = lane >> 4;
-  const int ti = (int)((a.n + T - 1) / T), tj = (int)((a.m + T - 1) / T);
+  const int ti = (int)((a.n + T - 1) / T), tj = (int)((a.m + T - 1) / T), tiles = ti * tj;
+  const int per_xcd = (items + kXcds - 1) / kXcds, slots = gridDim.x / kXcds;     // the grid is a multiple of 8
+  const int range = (int)(blockIdx.x & (kXcds - 1)) * per_xcd, end = min(per_xcd, items - range);
+  const int wi0 = (wv >> 1) * TL::S, wj0 = (wv & 1) * TL::S;
+
+  struct Item { int64_t i0, j0; int split, first, stages; };
   // neighbours in the list share operands: strips of 4 tiles of rows
-  const int item = xcd_remap(blockIdx.x, gridDim.x);
-  const int tiles = ti * tj;
-  const int split = item / tiles;
-  if (split >= a.splits) return;
-  const int tile = item - split * tiles;
-  const int strip = tile / (4 * ti), in = tile - strip * 4 * ti;
-  const int high = tj - 4 * strip < 4 ? tj - 4 * strip : 4;
-  const int64_t i0 = (int64_t)(in / high) * T, j0 = (int64_t)(4 * strip + in % high) * T;
-  const int first = split * a.per;
-  const int nst = (int)(a.p.panels - first < a.per ? a.p.panels - first : a.per);
-  const int wi0 = (wv >> 1) * TL::SI, wj0 = (wv & 1) * TL::SJ;
+  auto locate = [&](int slot) {
+    const int item = range + slot, split = item / tiles, tile = item - split * tiles;
+    const int strip = tile / (4 * ti), in = tile - strip * 4 * ti, high = min(tj - 4 * strip, 4);
+    const int first = split * a.per;
+    return Item{(int64_t)(in / high) * T, (int64_t)(4 * strip + in % high) * T, split, first, min((int)a.p.panels - first, a.per)};
+  };
+  int slot = (int)(blockIdx.x / kXcds);
+  if (slot >= end) return;
 
   __shared__ __attribute__((aligned(16))) uint8_t lds[RING][TL::STAGE];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS uint8_t*)&lds[0][0];
-  // this wave's loads of a stage: load x of all 2 CODES / 1024, P's first
+  // ---- sending for stages: half of the waves load P, the others Q; rows past a matrix read its last -----
+  const bool wq = wv >= TL::WAVES / 2;
+  const MxView& mv = wq ? a.q : a.p;
+  const int64_t step = mv.rows * kMxRowBytes, sstep = mv.groups * kMxGroupBytes;
+  const GLOBAL uint8_t* codes;
+  const GLOBAL uint8_t* scales;
   uint32_t off[TL::LOADS], soff[TL::SLOADS];
-#pragma unroll
-  for (int x = 0; x < TL::LOADS; ++x) {
-    const int id = wv * TL::LOADS + x;
-    const bool q = id >= TL::CODES / 1024;
-    const int r = (q ? id - TL::CODES / 1024 : id) * 16 + (lane >> 2);
-    const int64_t left = (q ? a.m - j0 : a.n - i0) - 1;       // rows past the matrix read its last one
-    off[x] = (uint32_t)((q ? j0 : i0) + (r < left ? r : left)) * kMxRowBytes + 16 * swz(r, lane & 3);
-  }
-#pragma unroll
-  for (int x = 0; x < TL::SLOADS; ++x) {
-    const int id = (wv * TL::SLOADS + x) % TL::WORDS;
-    const bool q = id >= TL::WORDS / 2;
-    const int64_t grp = (q ? j0 : i0) / kMxGroup + (q ? id - TL::WORDS / 2 : id), last = (q ? a.q.groups : a.p.groups) - 1;
-    soff[x] = (uint32_t)(grp < last ? grp : last) * kMxGroupBytes + 4 * lane;
-  }
-  const int64_t pstep = a.n * kMxRowBytes, qstep = a.m * kMxRowBytes, psstep = a.p.groups * kMxGroupBytes, qsstep = a.q.groups * kMxGroupBytes;
-  auto load_stage = [&](int j) {
-    const int64_t panel = first + j;
-    const uint32_t l = lds0 + (uint32_t)(j % RING) * TL::STAGE;
-    const GLOBAL uint8_t* pc = gbl(a.p.codes) + panel * pstep;
-    const GLOBAL uint8_t* qc = gbl(a.q.codes) + panel * qstep;
-    const GLOBAL uint8_t* ps = gbl(a.p.scales) + panel * psstep;
-    const GLOBAL uint8_t* qs = gbl(a.q.scales) + panel * qsstep;
+  const uint32_t lcodes = lds0 + (wq ? TL::CODES : 0) + (wv & 1) * TL::LOADS * 1024;
+  const uint32_t lscales = lds0 + 2 * TL::CODES + (wq ? TL::SCALES : 0);
+  int send_slot = slot, send_left, ahead = 0;
+  uint32_t send_to = 0;                                      // its buffer
+  auto aim = [&] {                                           // at the first stage of the item in send_slot
+    const Item it = locate(send_slot);
+    const int64_t t0 = wq ? it.j0 : it.i0;
+    codes = gbl(mv.codes) + it.first * step;
+    scales = gbl(mv.scales) + it.first * sstep;
+    send_left = it.stages;
+    const int left = (int)min(mv.rows - t0 - 1, (int64_t)T);
 #pragma unroll
     for (int x = 0; x < TL::LOADS; ++x) {
-      const int id = wv * TL::LOADS + x;
-      load_lds16(gcast<uint16_t>(id >= TL::CODES / 1024 ? qc : pc), off[x], l + id * 1024);
+      const int r = ((wv & 1) * TL::LOADS + x) * 16 + (lane >> 2);
+      off[x] = (uint32_t)((int)t0 + min(r, left)) * kMxRowBytes + 16 * (wq ? q_place(r, lane & 3) : p_place<PAIRS>(r, lane & 3));
     }
 #pragma unroll
     for (int x = 0; x < TL::SLOADS; ++x) {
-      const int id = (wv * TL::SLOADS + x) % TL::WORDS;
-      load_lds4(id >= TL::WORDS / 2 ? qs : ps, soff[x], l + 2 * TL::CODES + id * 256);
+      const int grp = (int)(t0 / kMxGroup) + ((wv & 1) * TL::SLOADS + x) % (TL::WORDS / 2);
+      soff[x] = (uint32_t)min(grp, (int)mv.groups - 1) * kMxGroupBytes + 4 * lane;
     }
   };
   constexpr int PER = TL::LOADS + TL::SLOADS;
-  // stage j + 1 has landed when at most the `behind` later ones are under way
-  auto wait_stages = [&](int behind) {
-    if (behind >= 2) wait_loads<2 * PER>();
-    else if (behind == 1) wait_loads<PER>();
-    else wait_loads<0>();
-    __builtin_amdgcn_s_barrier();
+  // loads x = 0 .. PER - 1 of the next stage, in this order; STAY: it is not its item's last
+  auto send = [&](int x, auto stay) {
+    if (x < TL::LOADS) {
+      load_lds16(gcast<uint16_t>(codes), off[x], send_to + lcodes + x * 1024);
+    } else {
+      const int id = ((wv & 1) * TL::SLOADS + x - TL::LOADS) % (TL::WORDS / 2);
+      load_lds4(scales, soff[x - TL::LOADS], send_to + lscales + id * 256);
+    }
+    if (x < PER - 1) return;
+    ++ahead;
+    send_to = send_to == (RING - 1) * TL::STAGE ? 0 : send_to + TL::STAGE;
+    codes += step;
+    scales += sstep;
+    --send_left;
+    if (!decltype(stay)::value && send_left == 0) {
+      send_slot += slots;
+      if (send_slot < end) aim();
+    }
+  };
+  auto more = [&] { return send_slot < end; };
+
+  // ---- fragments ---------------------------------------------------------------------------------------
+  // words of exponents of 64 rows: with PAIRS a lane's rows have two places in them and a byte of its own
+  constexpr int KP = (N + 3) / 4 * (PAIRS ? 2 : 1), KQ = (N + 3) / 4;
+  struct Frag { u32x4 p[N], q[N]; uint32_t sp[KP], sq[KQ]; };
+  const int pshift = (PAIRS ? 8 * (c >> 3) : 0) + wi0 % kMxGroup / 2;   // 16 rows a byte
+  const int prow = wi0 + p_row<PAIRS>(0, c), qrow = wj0 + c;
+  const uint32_t plane = lds0 + prow * kMxRowBytes + 16 * p_place<PAIRS>(prow, g);
+  const uint32_t qlane = lds0 + TL::CODES + qrow * kMxRowBytes + 16 * q_place(qrow, g);
+  const uint32_t splane = lds0 + 2 * TL::CODES + wi0 / kMxGroup * kMxGroupBytes + 4 * (PAIRS ? 16 * g + 8 * (c >> 2 & 1) + (c & 3) : lane);
+  const uint32_t sqlane = lds0 + 2 * TL::CODES + TL::SCALES + wj0 / kMxGroup * kMxGroupBytes + 4 * lane;
+  uint32_t read_from = 0;                                    // buffer of the stage to be read next
+  auto ld4 = [](uint32_t at) { return *(const LDS u32x4*)(uintptr_t)at; };
+  auto ld1 = [](uint32_t at) { return *(const LDS uint32_t*)(uintptr_t)at; };
+  auto read_p = [&](Frag& f, int x) { f.p[x] = ld4(read_from + plane + (64 * (x / 4) + p_row<PAIRS>(x & 3, 0)) * kMxRowBytes); };
+  auto read_q = [&](Frag& f, int x) { f.q[x] = ld4(read_from + qlane + 16 * x * kMxRowBytes); };
+  auto read_scales = [&](Frag& f) {
+#pragma unroll
+    for (int x = 0; x < KP; ++x) f.sp[x] = ld1(read_from + splane + (PAIRS ? x / 2 : x) * kMxGroupBytes + (PAIRS ? 16 * (x & 1) : 0));
+#pragma unroll
+    for (int x = 0; x < KQ; ++x) f.sq[x] = ld1(read_from + sqlane + x * kMxGroupBytes);
+  };
+  auto read_done = [&] { read_from = read_from == (RING - 1) * TL::STAGE ? 0 : read_from + TL::STAGE; };
+
+  // ---- a stage -------------------------------------------------------------------------------------------
+  // Stores of a whole tile's results, all younger than the stages that are then under way. Three stages
+  // later every stage waited for is younger than they are.
+  constexpr int STORES = N * N / 2;
+  constexpr bool LATE = PAIRS && 2 * PER + STORES <= 63;
+  int late = 0;
+  // Before a stage (`now`) is multiplied: its fragments are there, the next stage has landed, and every
+  // wave is this far. ahead: stages sent for and not multiplied, this one among them.
+  // STEADY: four stages ahead, nothing late.
+  auto turn = [&](Frag& now, auto steady) {
+    if (decltype(steady)::value) {
+      wait_loads<2 * PER>();
+    } else {
+      if (ahead >= 4) {
+        if (LATE && late > 0) wait_loads<LATE ? 2 * PER + STORES : 0>();
+        else wait_loads<2 * PER>();
+      } else if (ahead == 3) {
+        wait_loads<PER>();
+      } else {
+        wait_loads<0>();
+      }
+      if (late > 0) --late;
+    }
+    if (PAIRS || TL::S < kMxGroup) {
+#pragma unroll
+      for (int x = 0; x < KP; ++x) now.sp[x] >>= pshift;
+    }
+    if (TL::S < kMxGroup) {
+#pragma unroll
+      for (int x = 0; x < KQ; ++x) now.sq[x] >>= wj0 % kMxGroup / 2;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 3\n\ts_barrier" ::: "memory");      // the shifts are written before an MFMA reads them
     __builtin_amdgcn_sched_barrier(0);
   };
-
-  constexpr int KI = (NI + 3) / 4, KJ = (NJ + 3) / 4;        // exponent words of a side
-  struct Frag { u32x4 p[NI], q[NJ]; uint32_t sp[KI], sq[KJ]; };
-  auto read = [&](Frag& f, int j) {
-    const uint8_t* s = lds[j % RING];
+  // reads over the first half of the rows, loads over the second (behind the last stage the reads fetch
+  // what nobody uses)
+  auto mul = [&](Frag& now, Frag& next, auto fresh, auto steady) {
+    constexpr int HALF = N / 2;
+    const bool sends = decltype(steady)::value || more();
+    each<N>([&](auto xx) {
+      constexpr int X = decltype(xx)::value;
+      if constexpr (X < HALF) {
+        if constexpr (X == 0) read_scales(next);
 #pragma unroll
-    for (int x = 0; x < NI; ++x) {
-      const int r = wi0 + 16 * x + c;
-      f.p[x] = *reinterpret_cast<const u32x4*>(s + r * kMxRowBytes + 16 * swz(r, g));
-    }
+        for (int x = X * N / HALF; x < (X + 1) * N / HALF; ++x) {
+          read_p(next, x);
+          read_q(next, x);
+        }
+      } else if (sends) {
 #pragma unroll
-    for (int x = 0; x < NJ; ++x) {
-      const int r = wj0 + 16 * x + c;
-      f.q[x] = *reinterpret_cast<const u32x4*>(s + TL::CODES + r * kMxRowBytes + 16 * swz(r, g));
-    }
-    const uint8_t* e = s + 2 * TL::CODES + 4 * lane;
-#pragma unroll
-    for (int x = 0; x < KI; ++x) f.sp[x] = *reinterpret_cast<const uint32_t*>(e + (wi0 / kMxGroup + x) * kMxGroupBytes);
-#pragma unroll
-    for (int x = 0; x < KJ; ++x) f.sq[x] = *reinterpret_cast<const uint32_t*>(e + TL::SCALES + (wj0 / kMxGroup + x) * kMxGroupBytes);
-    if constexpr (TL::SI < kMxGroup) f.sp[0] >>= wi0 % kMxGroup / 2;    // 16 rows a byte
-    if constexpr (TL::SJ < kMxGroup) f.sq[0] >>= wj0 % kMxGroup / 2;
-  };
-  f32x4 acc[NI][NJ];
-#pragma unroll
-  for (int x = 0; x < NI; ++x)
-#pragma unroll
-    for (int y = 0; y < NJ; ++y) acc[x][y] = f32x4{0, 0, 0, 0};
-  auto mul = [&](const Frag& f) {
-    each<NI>([&](auto x) {
-      each<NJ>([&](auto y) {
-        constexpr int X = decltype(x)::value, Y = decltype(y)::value;
-        acc[X][Y] = mfma_mx<X & 3, Y & 3>(f.p[X], f.q[Y], acc[X][Y], f.sp[X / 4], f.sq[Y / 4]);
-      });
+        for (int x = (X - HALF) * PER / (N - HALF); x < (X - HALF + 1) * PER / (N - HALF); ++x) send(x, steady);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      constexpr int BP = PAIRS ? 2 * (X >> 1 & 1) : X & 3, WP = PAIRS ? 2 * (X / 4) + (X & 1) : X / 4;
+      mfma_row<N, X * N, BP, decltype(fresh)::value>(now.p[X], now.q, now.sp[WP], now.sq);
+      __builtin_amdgcn_sched_barrier(0);
     });
+    read_done();
+    --ahead;
   };
 
-  for (int j = 0; j < RING && j < nst; ++j) load_stage(j);
-  if (nst >= 4) wait_loads<3 * PER>();
+  // ---- results -------------------------------------------------------------------------------------------
+  const float scale = !SPLIT && a.scale ? *a.scale : 1.0f;
+  auto results = [&](const Item& it) {
+    settle();
+    const int64_t i0 = it.i0 + wi0, j0 = it.j0 + wj0;
+    if constexpr (SPLIT) {
+      GLOBAL float* o = gbl(a.partial) + ((int64_t)it.split * a.m + j0 + c) * a.n + i0 + 4 * g;
+      const int rows = (int)min(a.m - j0 - c, (int64_t)T), cols = (int)min(a.n - i0 - 4 * g, (int64_t)T);   // from this lane's first on
+      each<N>([&](auto yy) {
+        constexpr int Y = decltype(yy)::value;
+        each<N>([&](auto xx) {
+          constexpr int X = decltype(xx)::value;
+          const f32x4 v = sum_of<X * N + Y>();
+          if (16 * Y < rows && 16 * X < cols) {
+            if (16 * X + 4 <= cols) *gcast<f32x4_u>(o + 16 * X) = v;
+            else
+#pragma unroll
+              for (int t = 0; t < 3; ++t)
+                if (16 * X + t < cols) o[16 * X + t] = v[t];
+          }
+        });
+        o += 16 * a.n;
+      });
+    } else if constexpr (PAIRS) {
+      typedef typename Elem<OT>::one one;
+      typedef typename Elem<OT>::eight eight;
+      GLOBAL one* o = gbl(static_cast<one*>(a.c)) + (j0 + c) * a.ldc + i0 + 8 * g;
+      const int rows = (int)min(a.m - j0 - c, (int64_t)T), cols = (int)min(a.n - i0 - 8 * g, (int64_t)T);
+      const bool eights = (a.n & 7) == 0;
+      if (it.i0 + T <= a.n && it.j0 + T <= a.m && eights) late = 3;
+      each<N>([&](auto yy) {
+        constexpr int Y = decltype(yy)::value;
+        each<N / 2>([&](auto xx) {
+          constexpr int X = 2 * decltype(xx)::value;
+          const f32x4 v = sum_of<X * N + Y>() * scale, w = sum_of<(X + 1) * N + Y>() * scale;
+          const eight u = __builtin_convertvector(f32x8{v[0], v[1], v[2], v[3], w[0], w[1], w[2], w[3]}, eight);
+          if (16 * Y < rows && 16 * X < cols) {
+            if (eights) {
+              *gcast<eight>(o + 16 * X) = u;
+            } else {
+#pragma unroll
+              for (int t = 0; t < 8; ++t)
+                if (16 * X + t < cols) o[16 * X + t] = u[t];
+            }
+          }
+        });
+        o += 16 * a.ldc;
+      });
+    } else {
+      each<N>([&](auto yy) {
+        constexpr int Y = decltype(yy)::value;
+        each<N>([&](auto xx) {
+          constexpr int X = decltype(xx)::value;
+          finish<OT>(a, j0 + 16 * Y + c, i0 + 16 * X + 4 * g, sum_of<X * N + Y>(), scale);
+        });
+      });
+    }
+  };
+
+  aim();
+  for (int j = 0; j < RING; ++j)
+    if (more()) {
+#pragma unroll
+      for (int x = 0; x < PER; ++x) send(x, std::false_type{});
+    }
+  if (ahead == 4) wait_loads<3 * PER>();
   else wait_loads<0>();
   __builtin_amdgcn_s_barrier();
   Frag f0, f1;
-  read(f0, 0);
-  auto step = [&](Frag& now, Frag& next, int j) {
-    wait_stages(nst - 2 - j);
-    if (j + RING < nst) load_stage(j + RING);
-    if (j + 1 < nst) read(next, j + 1);
-    mul(now);
+#pragma unroll
+  for (int x = 0; x < N; ++x) {
+    read_p(f0, x);
+    read_q(f0, x);
+  }
+  read_scales(f0);
+  read_done();
+  Item it = locate(slot);
+  bool fresh = true;
+  // one stage; false behind the last
+  auto stage = [&](Frag& now, Frag& next) {
+    using Yes = std::true_type;
+    using No = std::false_type;
+    if (!fresh && ahead == 4 && late == 0 && send_left > 1 && more()) {
+      turn(now, Yes{});
+      mul(now, next, No{}, Yes{});
+    } else {
+      turn(now, No{});
+      if (fresh) mul(now, next, Yes{}, No{});
+      else mul(now, next, No{}, No{});
+    }
+    fresh = --it.stages == 0;
+    if (!fresh) return true;
+    results(it);
+    slot += slots;
+    if (slot >= end) return false;
+    it = locate(slot);
+    return true;
   };
-  for (int j = 0; j < nst; j += 2) {
-    step(f0, f1, j);
-    if (j + 1 < nst) step(f1, f0, j + 1);
-  }
-
-  if constexpr (SPLIT) {
-    GLOBAL float* o = gbl(a.partial) + (int64_t)split * a.m * a.n;
-#pragma unroll
-    for (int x = 0; x < NI; ++x)
-#pragma unroll
-      for (int y = 0; y < NJ; ++y) {
-        const int64_t i = i0 + wi0 + 16 * x + 4 * g, j = j0 + wj0 + 16 * y + c;
-        if (j >= a.m) continue;
-        if (i + 4 <= a.n) *gcast<f32x4_u>(o + j * a.n + i) = acc[x][y];
-        else
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-            if (i + t < a.n) o[j * a.n + i + t] = acc[x][y][t];
-      }
-  } else {
-    const float scale = a.scale ? *a.scale : 1.0f;
-#pragma unroll
-    for (int x = 0; x < NI; ++x)
-#pragma unroll
-      for (int y = 0; y < NJ; ++y) finish<OT>(a, j0 + wj0 + 16 * y + c, i0 + wi0 + 16 * x + 4 * g, acc[x][y], scale);
-  }
+  while (stage(f0, f1) && stage(f1, f0)) {}
 }
 
 // The parts of a split product, added in order.
@@ -287,11 +481,12 @@ void k_mx_join(MxProduct a) {
   if (i >= a.n) return;
   const GLOBAL float* p = gbl(a.partial) + j * a.n + i;
   const int64_t step = a.m * a.n;
+  const int parts = a.p.panels > 0 ? a.splits : 0;
   f32x4 sum{0, 0, 0, 0};
   if (i + 4 <= a.n) {
-    for (int s = 0; s < a.splits; ++s) sum += *gcast<f32x4_u>(p + s * step);
+    for (int s = 0; s < parts; ++s) sum += *gcast<f32x4_u>(p + s * step);
   } else {
-    for (int s = 0; s < a.splits; ++s)
+    for (int s = 0; s < parts; ++s)
       for (int t = 0; t < 4; ++t)
         if (i + t < a.n) sum[t] += p[s * step + t];
   }
@@ -300,22 +495,25 @@ void k_mx_join(MxProduct a) {
 
 template <int T, int OT>
 hipError_t go_tiles(const MxProduct& a, hipStream_t s) {
-  const int64_t tiles = ((a.n + T - 1) / T) * ((a.m + T - 1) / T) * a.splits;
-  const dim3 grid((unsigned)((tiles + 7) / 8 * 8)), block(Tile<T>::WAVES * kWave);
-  if (a.splits == 1) {
-    k_mx_gemm<T, OT, false><<<grid, block, 0, s>>>(a);
-    return hipGetLastError();
-  }
-  k_mx_gemm<T, G_F32, true><<<grid, block, 0, s>>>(a);
-  if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  const int64_t items = ((a.n + T - 1) / T) * ((a.m + T - 1) / T) * a.splits;
+  constexpr int64_t fit = 256 * (T == 256 ? 1 : T == 128 ? 2 : 4);            // what 256 CUs hold
+  const dim3 grid((unsigned)std::min<int64_t>((items + kXcds - 1) / kXcds * kXcds, fit)), block(Tile<T>::WAVES * kWave);
+  if (a.splits == 1) k_mx_gemm<T, OT, false><<<grid, block, 0, s>>>(a, (int)items);
+  else k_mx_gemm<T, G_F32, true><<<grid, block, 0, s>>>(a, (int)items);
+  return hipGetLastError();
+}
+template <int OT>
+hipError_t go_join(const MxProduct& a, hipStream_t s) {
   k_mx_join<OT><<<dim3((unsigned)((a.n + 1023) / 1024 * a.m)), dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }
 template <int OT>
 hipError_t go(const MxProduct& a, int tile, hipStream_t s) {
-  if (tile == 256) return go_tiles<256, OT>(a, s);
-  if (tile == 128) return go_tiles<128, OT>(a, s);
-  if (tile == 64) return go_tiles<64, OT>(a, s);
+  if (a.p.panels == 0) return go_join<OT>(a, s);                              // no parts: zeros
+  if (tile != 0) {
+    const hipError_t e = tile == 256 ? go_tiles<256, OT>(a, s) : tile == 128 ? go_tiles<128, OT>(a, s) : go_tiles<64, OT>(a, s);
+    return e != hipSuccess || a.splits == 1 ? e : go_join<OT>(a, s);
+  }
   const dim3 grid((unsigned)((a.n + 15) / 16)), block(kFewWaves * kWave);
   if (a.m <= 16) k_mx_few<1, OT><<<grid, block, 0, s>>>(a);
   else if (a.m <= 32) k_mx_few<2, OT><<<grid, block, 0, s>>>(a);

@@ -279,8 +279,8 @@ psgd_status psgd_mx_product(psgd_ctx* ctx, const psgd_mx_tensor* a, const psgd_m
   p.m = m; p.n = n;
   p.c = c; p.ldc = ld_c;
   p.scale = scale; p.accumulate = accumulate != 0;
-  p.splits = plan.splits;
   p.per = (int32_t)((p.p.panels + plan.splits - 1) / plan.splits);
+  p.splits = p.per > 0 ? (int32_t)((p.p.panels + p.per - 1) / p.per) : 1;      // no part is empty
   p.partial = static_cast<float*>(workspace);
   DeviceGuard dev(ctx->device);
   HIPCHK(ctx, dev.err, "hipSetDevice");
