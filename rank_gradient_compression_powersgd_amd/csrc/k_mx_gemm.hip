@@ -48,35 +48,24 @@ template <int SP, int SQ> __device__ __forceinline__ f32x4 mfma_mx(u32x4 p, u32x
 #define MX_I(y) "n"(4 * (I + y)), "n"(4 * (I + y) + 3)
 #define MX_KEEP(LO, HI) "a[%" LO ":%" HI "]"
 #define MX_ZERO(LO, HI) "0"
-#define MX_ROW8(C)                                                                                                 \
-  asm volatile(MX_LINE("12", "13", "1", C("12", "13"), "28", "29", "9", "10", "0", "0")                            \
-               MX_LINE("14", "15", "2", C("14", "15"), "28", "29", "9", "10", "1", "0")                            \
-               MX_LINE("16", "17", "3", C("16", "17"), "28", "29", "9", "10", "0", "1")                            \
-               MX_LINE("18", "19", "4", C("18", "19"), "28", "29", "9", "10", "1", "1")                            \
-               MX_LINE("20", "21", "5", C("20", "21"), "28", "29", "9", "11", "0", "0")                            \
-               MX_LINE("22", "23", "6", C("22", "23"), "28", "29", "9", "11", "1", "0")                            \
-               MX_LINE("24", "25", "7", C("24", "25"), "28", "29", "9", "11", "0", "1")                            \
-               MX_LINE("26", "27", "8", C("26", "27"), "28", "29", "9", "11", "1", "1")                            \
-               ::"v"(p), "v"(q[0]), "v"(q[1]), "v"(q[2]), "v"(q[3]), "v"(q[4]), "v"(q[5]), "v"(q[6]), "v"(q[7]),   \
-               "v"(sp), "v"(sq[0]), "v"(sq[1]), MX_I(0), MX_I(1), MX_I(2), MX_I(3), MX_I(4), MX_I(5), MX_I(6),     \
-               MX_I(7), "n"(SP & 1), "n"(SP >> 1) : MX_A256)
-#define MX_ROW4(C)                                                                                                 \
+#define MX_ROW4(C, CLOBBER)                                                                                        \
   asm volatile(MX_LINE("7", "8", "1", C("7", "8"), "15", "16", "5", "6", "0", "0")                                 \
                MX_LINE("9", "10", "2", C("9", "10"), "15", "16", "5", "6", "1", "0")                               \
                MX_LINE("11", "12", "3", C("11", "12"), "15", "16", "5", "6", "0", "1")                             \
                MX_LINE("13", "14", "4", C("13", "14"), "15", "16", "5", "6", "1", "1")                             \
-               ::"v"(p), "v"(q[0]), "v"(q[1]), "v"(q[2]), "v"(q[3]), "v"(sp), "v"(sq[0]), MX_I(0), MX_I(1),        \
-               MX_I(2), MX_I(3), "n"(SP & 1), "n"(SP >> 1) : MX_A64)
+               ::"v"(p), "v"(q[Y]), "v"(q[Y + 1]), "v"(q[Y + 2]), "v"(q[Y + 3]), "v"(sp), "v"(sq[Y / 4]), MX_I(Y), \
+               MX_I(Y + 1), MX_I(Y + 2), MX_I(Y + 3), "n"(SP & 1), "n"(SP >> 1) : CLOBBER)
 #define MX_ROW2(C)                                                                                                 \
   asm volatile(MX_LINE("5", "6", "1", C("5", "6"), "9", "10", "3", "4", "0", "0")                                  \
                MX_LINE("7", "8", "2", C("7", "8"), "9", "10", "3", "4", "1", "0")                                  \
                ::"v"(p), "v"(q[0]), "v"(q[1]), "v"(sp), "v"(sq[0]), MX_I(0), MX_I(1), "n"(SP & 1), "n"(SP >> 1) : MX_A16)
-// row I / N of the tile: sums I .. I + N - 1; byte SP of sp is p's exponent, byte y % 4 of sq[y / 4] that of q[y]
-template <int N, int I, int SP, bool NEW> __device__ __forceinline__ void mfma_row(u32x4 p, const u32x4 (&q)[N], uint32_t sp, const uint32_t* sq) {
-  if constexpr (N == 8 && NEW) MX_ROW8(MX_ZERO);
-  else if constexpr (N == 8) MX_ROW8(MX_KEEP);
-  else if constexpr (N == 4 && NEW) MX_ROW4(MX_ZERO);
-  else if constexpr (N == 4) MX_ROW4(MX_KEEP);
+// Up to four MFMAs of a row of the tile: sums I + Y, ...; byte SP of sp is p's exponent, byte y % 4 of
+// sq[y / 4] that of q[y].
+template <int N, int I, int Y, int SP, bool NEW> __device__ __forceinline__ void mfma_row(u32x4 p, const u32x4 (&q)[N], uint32_t sp, const uint32_t* sq) {
+  if constexpr (N == 8 && NEW) MX_ROW4(MX_ZERO, MX_A256);
+  else if constexpr (N == 8) MX_ROW4(MX_KEEP, MX_A256);
+  else if constexpr (N == 4 && NEW) MX_ROW4(MX_ZERO, MX_A64);
+  else if constexpr (N == 4) MX_ROW4(MX_KEEP, MX_A64);
   else if constexpr (NEW) MX_ROW2(MX_ZERO);
   else MX_ROW2(MX_KEEP);
 }
@@ -299,13 +288,27 @@ void k_mx_gemm(MxProduct a, int items) {
   uint32_t read_from = 0;                                    // buffer of the stage to be read next
   auto ld4 = [](uint32_t at) { return *(const LDS u32x4*)(uintptr_t)at; };
   auto ld1 = [](uint32_t at) { return *(const LDS uint32_t*)(uintptr_t)at; };
-  auto read_p = [&](Frag& f, int x) { f.p[x] = ld4(read_from + plane + (64 * (x / 4) + p_row<PAIRS>(x & 3, 0)) * kMxRowBytes); };
-  auto read_q = [&](Frag& f, int x) { f.q[x] = ld4(read_from + qlane + 16 * x * kMxRowBytes); };
-  auto read_scales = [&](Frag& f) {
+  // a lane's first addresses, as asm: the compiler would give every read one of its own
+  auto at = [&](uint32_t lane_part) {
+    uint32_t v;
+    asm("v_add_u32 %0, %1, %2" : "=v"(v) : "s"(read_from), "v"(lane_part));
+    return v;
+  };
+  // reads of a stage: 0 the exponents, then p and q in turn
+  constexpr int READS = 2 * N + 1;
+  struct Places { uint32_t p, q, sp, sq; };
+  auto read = [&](Frag& f, const Places& b, int i) {
+    if (i == 0) {
 #pragma unroll
-    for (int x = 0; x < KP; ++x) f.sp[x] = ld1(read_from + splane + (PAIRS ? x / 2 : x) * kMxGroupBytes + (PAIRS ? 16 * (x & 1) : 0));
+      for (int x = 0; x < KP; ++x) f.sp[x] = ld1(b.sp + (PAIRS ? x / 2 : x) * kMxGroupBytes + (PAIRS ? 16 * (x & 1) : 0));
 #pragma unroll
-    for (int x = 0; x < KQ; ++x) f.sq[x] = ld1(read_from + sqlane + x * kMxGroupBytes);
+      for (int x = 0; x < KQ; ++x) f.sq[x] = ld1(b.sq + x * kMxGroupBytes);
+    } else if (i & 1) {
+      const int x = i / 2;
+      f.p[x] = ld4(b.p + (64 * (x / 4) + p_row<PAIRS>(x & 3, 0)) * kMxRowBytes);
+    } else {
+      f.q[i / 2 - 1] = ld4(b.q + 16 * (i / 2 - 1) * kMxRowBytes);
+    }
   };
   auto read_done = [&] { read_from = read_from == (RING - 1) * TL::STAGE ? 0 : read_from + TL::STAGE; };
 
@@ -344,27 +347,26 @@ void k_mx_gemm(MxProduct a, int items) {
     asm volatile("s_nop 3\n\ts_barrier" ::: "memory");      // the shifts are written before an MFMA reads them
     __builtin_amdgcn_sched_barrier(0);
   };
-  // reads over the first half of the rows, loads over the second (behind the last stage the reads fetch
-  // what nobody uses)
+  // Reads over the first three quarters of the MFMAs, loads over the second half, one or two ahead of four
+  // MFMAs: more at once wait for the LDS, and the matrix pipe with them. Behind the last stage the reads
+  // fetch what nobody uses.
   auto mul = [&](Frag& now, Frag& next, auto fresh, auto steady) {
-    constexpr int HALF = N / 2;
+    constexpr int STEPS = N == 8 ? 16 : N, RSTEPS = N == 8 ? 12 : N == 4 ? 3 : 1, LFIRST = STEPS / 2, LSTEPS = STEPS - LFIRST;
     const bool sends = decltype(steady)::value || more();
-    each<N>([&](auto xx) {
-      constexpr int X = decltype(xx)::value;
-      if constexpr (X < HALF) {
-        if constexpr (X == 0) read_scales(next);
+    const Places b{at(plane), at(qlane), at(splane), at(sqlane)};
+    each<STEPS>([&](auto hh) {
+      constexpr int H = decltype(hh)::value, X = N == 8 ? H / 2 : H, Y = N == 8 ? 4 * (H & 1) : 0;
 #pragma unroll
-        for (int x = X * N / HALF; x < (X + 1) * N / HALF; ++x) {
-          read_p(next, x);
-          read_q(next, x);
+      for (int i = H * READS / RSTEPS; i < (H + 1) * READS / RSTEPS && i < READS; ++i) read(next, b, i);
+      if constexpr (H >= LFIRST) {
+        if (sends) {
+#pragma unroll
+          for (int x = (H - LFIRST) * PER / LSTEPS; x < (H - LFIRST + 1) * PER / LSTEPS; ++x) send(x, steady);
         }
-      } else if (sends) {
-#pragma unroll
-        for (int x = (X - HALF) * PER / (N - HALF); x < (X - HALF + 1) * PER / (N - HALF); ++x) send(x, steady);
       }
       __builtin_amdgcn_sched_barrier(0);
       constexpr int BP = PAIRS ? 2 * (X >> 1 & 1) : X & 3, WP = PAIRS ? 2 * (X / 4) + (X & 1) : X / 4;
-      mfma_row<N, X * N, BP, decltype(fresh)::value>(now.p[X], now.q, now.sp[WP], now.sq);
+      mfma_row<N, X * N, Y, BP, decltype(fresh)::value>(now.p[X], now.q, now.sp[WP], now.sq);
       __builtin_amdgcn_sched_barrier(0);
     });
     read_done();
@@ -440,12 +442,11 @@ void k_mx_gemm(MxProduct a, int items) {
   else wait_loads<0>();
   __builtin_amdgcn_s_barrier();
   Frag f0, f1;
+  {
+    const Places b{at(plane), at(qlane), at(splane), at(sqlane)};
 #pragma unroll
-  for (int x = 0; x < N; ++x) {
-    read_p(f0, x);
-    read_q(f0, x);
+    for (int i = 0; i < READS; ++i) read(f0, b, i);
   }
-  read_scales(f0);
   read_done();
   Item it = locate(slot);
   bool fresh = true;
