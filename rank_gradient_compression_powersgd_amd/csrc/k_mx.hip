@@ -8,6 +8,9 @@
 //
 // Both directions in one pass. A lane holds 2 columns x 32 rows: a column's block is the lane's own, a
 // row's block spans 16 lanes, whose maximum is four DPP steps. No LDS; the input is read once.
+#include <type_traits>
+#include <utility>
+
 #include "hash.h"
 #include "mx.h"
 
@@ -17,24 +20,49 @@ namespace {
 constexpr int kThreads = 256;
 
 typedef float f32x2_u __attribute__((ext_vector_type(2), aligned(4)));
-typedef _Float16 f16x2_u __attribute__((ext_vector_type(2), aligned(2)));
-typedef __bf16 bf16x2_u __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32_u __attribute__((aligned(2)));
+typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x8_u __attribute__((ext_vector_type(8), aligned(4)));
 typedef _Float16 f16x8_u __attribute__((ext_vector_type(8), aligned(2)));
 typedef __bf16 bf16x8_u __attribute__((ext_vector_type(8), aligned(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 template <int T> struct Elem;
-template <> struct Elem<G_F32> { typedef float one; typedef f32x2_u two; typedef f32x8_u eight; };
-template <> struct Elem<G_F16> { typedef _Float16 one; typedef f16x2_u two; typedef f16x8_u eight; };
-template <> struct Elem<G_BF16> { typedef __bf16 one; typedef bf16x2_u two; typedef bf16x8_u eight; };
+template <> struct Elem<G_F32> { typedef float one; typedef f32x8_u eight; };
+template <> struct Elem<G_F16> { typedef _Float16 one; typedef f16x8_u eight; };
+template <> struct Elem<G_BF16> { typedef __bf16 one; typedef bf16x8_u eight; };
+
+template <typename F, int... I> __device__ __forceinline__ void each_of(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F> __device__ __forceinline__ void each(F&& f) { each_of(f, std::make_integer_sequence<int, N>{}); }
 
 __device__ __forceinline__ uint32_t mag(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7fffffffu; }
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
-template <int CTRL> __device__ __forceinline__ uint32_t row_max(uint32_t v) {
-  return umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true));
+template <int CTRL> __device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
 }
-__device__ __forceinline__ uint32_t max4(uint32_t v) { return row_max<0x4E>(row_max<0xB1>(v)); }       // of 4 lanes
-__device__ __forceinline__ uint32_t max16(uint32_t v) { return row_max<0x140>(row_max<0x141>(max4(v))); }
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kRor4 = 0x124, kRor8 = 0x128, kBcast = 0x150;   // of 4 lanes, of 16
+__device__ __forceinline__ uint32_t max4(uint32_t v) {                                     // of 4 lanes
+  v = umax(v, dpp<kXor1>(v));
+  return umax(v, dpp<kXor2>(v));
+}
+// m[r]: a lane's value of row r, 16 rows; the largest of row `lane % 16` over the 16 lanes. Each of two
+// exchanges halves the rows that a lane carries.
+__device__ __forceinline__ uint32_t max_of_rows(const uint32_t (&m)[16], int lane) {
+  uint32_t a[8], b[4];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) a[k] = umax(lane & 1 ? m[2 * k + 1] : m[2 * k], dpp<kXor1>(lane & 1 ? m[2 * k] : m[2 * k + 1]));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    b[k] = umax(lane & 2 ? a[2 * k + 1] : a[2 * k], dpp<kXor2>(lane & 2 ? a[2 * k] : a[2 * k + 1]));
+    b[k] = umax(b[k], dpp<kRor4>(b[k]));
+    b[k] = umax(b[k], dpp<kRor8>(b[k]));
+  }
+  const uint32_t lo = lane & 4 ? b[1] : b[0], hi = lane & 4 ? b[3] : b[2];
+  return lane & 8 ? hi : lo;
+}
 
 // Exponent byte of a block from the bits of its largest magnitude.
 template <bool SR> __device__ __forceinline__ uint32_t block_exponent(uint32_t high) {
@@ -44,16 +72,13 @@ template <bool SR> __device__ __forceinline__ uint32_t block_exponent(uint32_t h
 // The factor 2^(s - 127) for the conversions; of a NaN block 2^127, its codes are dropped.
 __device__ __forceinline__ float block_factor(uint32_t s) { return __builtin_bit_cast(float, (s < 254 ? s : 254) << 23); }
 
-// Two elements to byte SEL of `old`, a in the low nibble.
-template <int SEL> __device__ __forceinline__ uint32_t pack2(uint32_t old, float a, float b, float f) {
-  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, a, b, f, SEL);
-}
-// The same by random bits, in byte 0 (the others hold anything: the compiler drops this conversion's
-// old value). Its bits come in at the top of a 32-bit number for the low nibble, one bit lower for the
-// high one, and one instruction shares them: two elements of their own bits take two.
+// Two elements by random bits, in byte 0, a in the low nibble (the other bytes hold anything: the
+// compiler drops this conversion's old value; from fp32, the 16-bit types' conversions keep fewer bits of
+// what they cut off). Its bits come in at the top of a 32-bit number for the low nibble, one bit lower for the
+// high one, and one instruction shares them: two elements of their own bits take two, each for a nibble.
 __device__ __forceinline__ uint32_t pack2_random(float a, float b, float f, uint32_t ra, uint32_t rb) {
-  const uint32_t lo = __builtin_amdgcn_cvt_scalef32_sr_pk_fp4_f32(0u, f32x2{a, 0.0f}, ra, f, 0);
-  const uint32_t hi = __builtin_amdgcn_cvt_scalef32_sr_pk_fp4_f32(0u, f32x2{0.0f, b}, rb >> 1, f, 0);
+  const uint32_t lo = __builtin_amdgcn_cvt_scalef32_sr_pk_fp4_f32(0u, f32x2{a, b}, ra, f, 0);
+  const uint32_t hi = __builtin_amdgcn_cvt_scalef32_sr_pk_fp4_f32(0u, f32x2{a, b}, rb >> 1, f, 0);
   return (lo & 0x0fu) | (hi & ~0x0fu);
 }
 // the bytes 0 of four
@@ -66,6 +91,78 @@ __device__ __forceinline__ int64_t scale_at(const MxView& v, int64_t panel, int6
   return (panel * v.groups + row / kMxGroup) * kMxGroupBytes + 4 * (16 * g + (row & 15)) + ((row >> 4) & 3);
 }
 
+// Bits of pair i0 + d of a run that is shorter than 2^32: its index passes a multiple of 2^32 at most once.
+struct PairBits {
+  uint32_t lo, here, next;
+  __device__ __forceinline__ PairBits(uint32_t key, int64_t i0)
+      : lo((uint32_t)i0), here(hash_high(key, (uint64_t)i0)), next(hash_high(key, (uint64_t)i0 + (uint64_t(1) << 32))) {}
+  __device__ __forceinline__ uint32_t at(uint32_t d) const { return hash_bits(lo + d < lo ? next : here, lo + d); }
+};
+
+// Two neighbours of a row as they were loaded.
+template <int IT> struct Pair {
+  uint32_t w;                                              // the second in the high half
+  __device__ __forceinline__ void load(const GLOBAL void* x, bool both, bool any) {
+    w = 0;
+    if (both) w = *gcast<u32_u>(static_cast<const GLOBAL uint16_t*>(x));
+    else if (any) w = *static_cast<const GLOBAL uint16_t*>(x);
+  }
+  __device__ __forceinline__ static void load4(Pair (&p)[4], const GLOBAL void* x) {
+    const u32x4_u v = *gcast<u32x4_u>(static_cast<const GLOBAL uint16_t*>(x));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j].w = v[j];
+  }
+  // magnitudes, whose order as integers is that of the values; `bits` makes fp32's of them
+  typedef u16x2 mags;
+  __device__ __forceinline__ mags mag() const { return __builtin_bit_cast(u16x2, w & 0x7fff7fffu); }
+  __device__ __forceinline__ static uint32_t larger(mags m) { return umax(m[0], m[1]); }
+  __device__ __forceinline__ static uint32_t bits(uint32_t m) {
+    if constexpr (IT == G_BF16) return m << 16;
+    else return __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(_Float16, (uint16_t)m));
+  }
+  __device__ __forceinline__ uint32_t nearest(float f) const {                              // byte 0
+    if constexpr (IT == G_BF16) return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(0u, __builtin_bit_cast(bf16x2, w), f, 0);
+    else return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(0u, __builtin_bit_cast(f16x2, w), f, 0);
+  }
+  __device__ __forceinline__ float x() const {
+    if constexpr (IT == G_BF16) return __builtin_bit_cast(float, w << 16);
+    else return (float)__builtin_bit_cast(f16x2, w)[0];
+  }
+  __device__ __forceinline__ float y() const {
+    if constexpr (IT == G_BF16) return __builtin_bit_cast(float, w & 0xffff0000u);
+    else return (float)__builtin_bit_cast(f16x2, w)[1];
+  }
+  // the same column's of two rows
+  __device__ __forceinline__ static Pair first(Pair a, Pair b) { return Pair{__builtin_amdgcn_perm(b.w, a.w, 0x05040100u)}; }
+  __device__ __forceinline__ static Pair second(Pair a, Pair b) { return Pair{__builtin_amdgcn_perm(b.w, a.w, 0x07060302u)}; }
+};
+template <> struct Pair<G_F32> {
+  float v, w;
+  __device__ __forceinline__ float x() const { return v; }
+  __device__ __forceinline__ float y() const { return w; }
+  __device__ __forceinline__ void load(const GLOBAL void* p, bool both, bool any) {
+    v = w = 0.0f;
+    if (both) {
+      const f32x2_u u = *gcast<f32x2_u>(static_cast<const GLOBAL float*>(p));
+      v = u[0];
+      w = u[1];
+    } else if (any) {
+      v = *static_cast<const GLOBAL float*>(p);
+    }
+  }
+  __device__ __forceinline__ static void load4(Pair (&p)[4], const GLOBAL void* x) {
+    const f32x8_u v = *gcast<f32x8_u>(static_cast<const GLOBAL float*>(x));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = Pair{v[2 * j], v[2 * j + 1]};
+  }
+  typedef u32x2 mags;
+  __device__ __forceinline__ mags mag() const { return u32x2{psgd::mag(v), psgd::mag(w)}; }
+  __device__ __forceinline__ static uint32_t larger(mags m) { return umax(m[0], m[1]); }
+  __device__ __forceinline__ static uint32_t bits(uint32_t m) { return m; }
+  __device__ __forceinline__ uint32_t nearest(float f) const { return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v, w, f, 0); }
+  __device__ __forceinline__ static Pair first(Pair a, Pair b) { return Pair{a.v, b.v}; }
+  __device__ __forceinline__ static Pair second(Pair a, Pair b) { return Pair{a.w, b.w}; }
+};
 // ---- rows only: 16 lanes a row and panel, 8 elements a lane; a workgroup takes 64 rows of a panel -----
 template <int IT, bool SR>
 __global__ __launch_bounds__(kThreads)
@@ -77,47 +174,39 @@ void k_mx_rows(MxQuantize a) {
   const uint32_t key = SR ? hash_key(a.seed, a.step ? (uint32_t)*a.step : 0, 0) : 0;
   const int64_t half = (a.n + 1) / 2;
   constexpr int TURNS = kMxGroup / 16;
-  f32x8 v[TURNS];
+  Pair<IT> v[TURNS][4];
 #pragma unroll
   for (int u = 0; u < TURNS; ++u) {
     const int64_t r = r0 + 16 * u + sub;
-    v[u] = f32x8{0, 0, 0, 0, 0, 0, 0, 0};
-    if (r < a.m) {
-      const GLOBAL one* x = gbl(static_cast<const one*>(a.x)) + r * a.ld + c0;
-      if (c0 + 8 <= a.n) {
-        v[u] = __builtin_convertvector(*gcast<typename Elem<IT>::eight>(x), f32x8);
-      } else {
+    const GLOBAL one* x = gbl(static_cast<const one*>(a.x)) + r * a.ld + c0;
+    if (r < a.m && c0 + 8 <= a.n) {
+      Pair<IT>::load4(v[u], x);
+    } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c0 + j < a.n) v[u][j] = (float)x[j];
-      }
+      for (int j = 0; j < 4; ++j) v[u][j].load(x + 2 * j, r < a.m && c0 + 2 * j + 1 < a.n, r < a.m && c0 + 2 * j < a.n);
     }
   }
 #pragma unroll
   for (int u = 0; u < TURNS; ++u) {
     const int64_t r = r0 + 16 * u + sub;
-    uint32_t high = 0;
+    typename Pair<IT>::mags high = v[u][0].mag();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) high = umax(high, mag(v[u][j]));
-    const uint32_t s = block_exponent<SR>(max4(high));
+    for (int j = 1; j < 4; ++j) high = __builtin_elementwise_max(high, v[u][j].mag());
+    const uint32_t s = block_exponent<SR>(Pair<IT>::bits(max4(Pair<IT>::larger(high))));
     const float f = block_factor(s);
-    uint32_t w;
-    if constexpr (SR) {
-      const int64_t i0 = r * half + c0 / 2;
-      uint32_t b[4];
+    uint32_t b[4];
+    const PairBits bits(key, r * half + c0 / 2);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t x = hash_bits(hash_high(key, (uint64_t)(i0 + j)), (uint32_t)(i0 + j));
-        b[j] = pack2_random(v[u][2 * j], v[u][2 * j + 1], f, x, turn16(x));
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (SR) {
+        const uint32_t w = bits.at(j);
+        b[j] = pack2_random(v[u][j].x(), v[u][j].y(), f, w, turn16(w));
+      } else {
+        b[j] = v[u][j].nearest(f);
       }
-      w = join4(b[0], b[1], b[2], b[3]);
-    } else {
-      w = pack2<0>(0, v[u][0], v[u][1], f);
-      w = pack2<1>(w, v[u][2], v[u][3], f);
-      w = pack2<2>(w, v[u][4], v[u][5], f);
-      w = pack2<3>(w, v[u][6], v[u][7], f);
     }
     if (r < a.m) {
+      const uint32_t w = join4(b[0], b[1], b[2], b[3]);
       *gcast<uint32_t>(gbl(a.row.codes) + (panel * a.row.rows + r) * kMxRowBytes + 4 * q) = s == 255 ? 0 : w;
       if ((q & 3) == 0) gbl(a.row.scales)[scale_at(a.row, panel, r, q >> 2)] = (uint8_t)s;
     }
@@ -129,100 +218,85 @@ template <int IT, bool ROWS, bool SR>
 __global__ __launch_bounds__(kThreads)
 void k_mx_cols(MxQuantize a) {
   typedef typename Elem<IT>::one one;
-  typedef typename Elem<IT>::two two;
   const int lane = threadIdx.x & (kWave - 1), wv = threadIdx.x / kWave;
   const int64_t pn = (a.n + kMxPanel - 1) / kMxPanel, panel_m = blockIdx.x / pn, panel_n = blockIdx.x - panel_m * pn;
   const int64_t r0 = panel_m * kMxPanel + 32 * wv, c0 = panel_n * kMxPanel + 2 * lane;
-  const uint32_t key = SR ? hash_key(a.seed, a.step ? (uint32_t)*a.step : 0, 0) : 0;
-  const int64_t half = (a.n + 1) / 2;
-  const int64_t rows = a.m - r0;                         // of the block that exist, maybe none
-  two v[32];
+  const int rows = (int)(a.m - r0 < 32 ? a.m - r0 : 32);     // of the block that exist, maybe none
   const bool both = c0 + 1 < a.n, any = c0 < a.n;
+  Pair<IT> v[32];
+  const GLOBAL one* x = gbl(static_cast<const one*>(a.x)) + r0 * a.ld + c0;
 #pragma unroll
-  for (int r = 0; r < 32; ++r) {
-    v[r] = two{(one)0.0f, (one)0.0f};
-    if (r < rows) {
-      const GLOBAL one* x = gbl(static_cast<const one*>(a.x)) + (r0 + r) * a.ld + c0;
-      if (both) v[r] = *gcast<two>(x);
-      else if (any) v[r][0] = x[0];
-    }
-  }
-  uint32_t h0 = 0, h1 = 0;
+  for (int r = 0; r < 32; ++r) v[r].load(x + r * a.ld, both && r < rows, any && r < rows);
+
+  typename Pair<IT>::mags high{0, 0};
 #pragma unroll
-  for (int r = 0; r < 32; ++r) {
-    h0 = umax(h0, mag((float)v[r][0]));
-    h1 = umax(h1, mag((float)v[r][1]));
-  }
-  const uint32_t s0 = block_exponent<SR>(h0), s1 = block_exponent<SR>(h1);
+  for (int r = 0; r < 32; ++r) high = __builtin_elementwise_max(high, v[r].mag());
+  const uint32_t s0 = block_exponent<SR>(Pair<IT>::bits(high[0])), s1 = block_exponent<SR>(Pair<IT>::bits(high[1]));
   const float f0 = block_factor(s0), f1 = block_factor(s1);
-  u32x4 k0, k1;                                          // the columns' codes
+  uint32_t k0[4], k1[4];                                     // the columns' codes
+  const uint32_t half = (uint32_t)((a.n + 1) / 2);
+  const PairBits bits(SR ? hash_key(a.seed, a.step ? (uint32_t)*a.step : 0, 0) : 0, r0 * (int64_t)half + c0 / 2);
   const uint32_t perm_odd = lane & 1 ? 0x07030501u : 0x02060004u, perm_two = lane & 2 ? 0x07060302u : 0x01000504u;
 #pragma unroll
-  for (int d = 0; d < 4; ++d) {                          // 8 rows: a word of a column, two of row bytes
-    uint32_t b0[4], b1[4];                               // bytes of the columns, by random bits
+  for (int h = 0; h < 2; ++h) {                              // 16 rows
+    uint32_t s = 0, f = 0;                                   // exponent and factor of row lane % 16, block lane / 16
+    bool bad = false;
+    if constexpr (ROWS) {
+      uint32_t m[16];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      uint32_t rs[4], rb[4], w[4];
+      for (int r = 0; r < 16; ++r) m[r] = Pair<IT>::larger(v[16 * h + r].mag());
+      s = block_exponent<SR>(Pair<IT>::bits(max_of_rows(m, lane)));
+      f = __builtin_bit_cast(uint32_t, block_factor(s));
+      const int r = 16 * h + (lane & 15);
+      if (r < rows) gbl(a.row.scales)[scale_at(a.row, panel_n, r0 + r, lane >> 4)] = (uint8_t)s;
+      bad = __builtin_amdgcn_ballot_w64(s == 255) != 0;
+    }
+    each<4>([&](auto dd) {                                   // 4 rows
+      constexpr int D = decltype(dd)::value;
+      const int r = 16 * h + 4 * D;
+      uint32_t w[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int r = 8 * d + 4 * e + t;
-        const float x0 = (float)v[r][0], x1 = (float)v[r][1];
+      for (int t = 0; t < 4; ++t) w[t] = SR ? bits.at((r + t) * half) : 0;
+      uint32_t b0[2], b1[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const Pair<IT>&p = v[r + 2 * t], &q = v[r + 2 * t + 1];
         if constexpr (SR) {
-          const int64_t i = (r0 + r) * half + c0 / 2;
-          w[t] = hash_bits(hash_high(key, (uint64_t)i), (uint32_t)i);
-          if (t & 1) {
-            b0[2 * e + t / 2] = pack2_random((float)v[r - 1][0], x0, f0, w[t - 1], w[t]);
-            b1[2 * e + t / 2] = pack2_random((float)v[r - 1][1], x1, f1, turn16(w[t - 1]), turn16(w[t]));
-          }
-        }
-        if constexpr (ROWS) {
-          const uint32_t s = block_exponent<SR>(max16(umax(mag(x0), mag(x1))));
-          const float f = block_factor(s);
-          rs[t] = s;
-          if constexpr (SR) rb[t] = pack2_random(x0, x1, f, w[t], turn16(w[t]));
-          else rb[t] = pack2<0>(0, x0, x1, f);
-          rb[t] = s == 255 ? 0 : rb[t];
+          b0[t] = pack2_random(p.x(), q.x(), f0, w[2 * t], w[2 * t + 1]);
+          b1[t] = pack2_random(p.y(), q.y(), f1, turn16(w[2 * t]), turn16(w[2 * t + 1]));
+        } else {
+          b0[t] = Pair<IT>::first(p, q).nearest(f0);
+          b1[t] = Pair<IT>::second(p, q).nearest(f1);
         }
       }
+      const uint32_t p0 = __builtin_amdgcn_perm(b0[1], b0[0], 0x0c0c0400u), p1 = __builtin_amdgcn_perm(b1[1], b1[0], 0x0c0c0400u);
+      k0[2 * h + D / 2] = D & 1 ? k0[2 * h + D / 2] | p0 << 16 : p0;
+      k1[2 * h + D / 2] = D & 1 ? k1[2 * h + D / 2] | p1 << 16 : p1;
       if constexpr (ROWS) {
+        uint32_t rb[4];
+        each<4>([&](auto tt) {
+          constexpr int T = decltype(tt)::value;
+          const float fr = __builtin_bit_cast(float, dpp<kBcast + 4 * D + T>(f));
+          if constexpr (SR) rb[T] = pack2_random(v[r + T].x(), v[r + T].y(), fr, w[T], turn16(w[T]));
+          else rb[T] = v[r + T].nearest(fr);
+          if (bad) rb[T] = dpp<kBcast + 4 * D + T>(s) == 255 ? 0 : rb[T];
+        });
         // 4 rows x 4 lanes of bytes, transposed: lane j of 4 gets row j's
         const uint32_t rw = join4(rb[0], rb[1], rb[2], rb[3]);
-        uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)rw, 0xB1, 0xf, 0xf, true);
-        uint32_t y = __builtin_amdgcn_perm(rw, o, perm_odd);
-        o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)y, 0x4E, 0xf, 0xf, true);
-        y = __builtin_amdgcn_perm(y, o, perm_two);
-        const int base = 8 * d + 4 * e, r = base + (lane & 3);
-        if (r < rows) *gcast<uint32_t>(gbl(a.row.codes) + (panel_n * a.row.rows + r0 + r) * kMxRowBytes + 4 * (lane >> 2)) = y;
-        // lane 16 g + t: the exponent of row t, block g
-        const uint32_t s = (lane & 3) == 0 ? rs[0] : (lane & 3) == 1 ? rs[1] : (lane & 3) == 2 ? rs[2] : rs[3];
-        if ((lane & 15) < 4 && r < rows) gbl(a.row.scales)[scale_at(a.row, panel_n, r0 + r, lane >> 4)] = (uint8_t)s;
+        uint32_t y = __builtin_amdgcn_perm(rw, dpp<kXor1>(rw), perm_odd);
+        y = __builtin_amdgcn_perm(y, dpp<kXor2>(y), perm_two);
+        const int row = r + (lane & 3);
+        if (row < rows) *gcast<uint32_t>(gbl(a.row.codes) + (panel_n * a.row.rows + r0 + row) * kMxRowBytes + 4 * (lane >> 2)) = y;
       }
-    }
-    if constexpr (SR) {
-      k0[d] = join4(b0[0], b0[1], b0[2], b0[3]);
-      k1[d] = join4(b1[0], b1[1], b1[2], b1[3]);
-    } else {
-      uint32_t w0 = 0, w1 = 0;
-      const int r = 8 * d;
-      w0 = pack2<0>(w0, (float)v[r][0], (float)v[r + 1][0], f0);
-      w0 = pack2<1>(w0, (float)v[r + 2][0], (float)v[r + 3][0], f0);
-      w0 = pack2<2>(w0, (float)v[r + 4][0], (float)v[r + 5][0], f0);
-      w0 = pack2<3>(w0, (float)v[r + 6][0], (float)v[r + 7][0], f0);
-      w1 = pack2<0>(w1, (float)v[r][1], (float)v[r + 1][1], f1);
-      w1 = pack2<1>(w1, (float)v[r + 2][1], (float)v[r + 3][1], f1);
-      w1 = pack2<2>(w1, (float)v[r + 4][1], (float)v[r + 5][1], f1);
-      w1 = pack2<3>(w1, (float)v[r + 6][1], (float)v[r + 7][1], f1);
-      k0[d] = w0;
-      k1[d] = w1;
-    }
+    });
   }
   GLOBAL uint8_t* o = gbl(a.col.codes) + (panel_m * a.col.rows + c0) * kMxRowBytes + 16 * wv;
   if (any) {
-    *gcast<u32x4>(o) = s0 == 255 ? u32x4{0, 0, 0, 0} : k0;
+    *gcast<u32x4>(o) = s0 == 255 ? u32x4{0, 0, 0, 0} : u32x4{k0[0], k0[1], k0[2], k0[3]};
     gbl(a.col.scales)[scale_at(a.col, panel_m, c0, wv)] = (uint8_t)s0;
   }
   if (both) {
-    *gcast<u32x4>(o + kMxRowBytes) = s1 == 255 ? u32x4{0, 0, 0, 0} : k1;
+    *gcast<u32x4>(o + kMxRowBytes) = s1 == 255 ? u32x4{0, 0, 0, 0} : u32x4{k1[0], k1[1], k1[2], k1[3]};
     gbl(a.col.scales)[scale_at(a.col, panel_m, c0 + 1, wv)] = (uint8_t)s1;
   }
 }
