@@ -160,7 +160,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.psgd_embed_grad_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
     lib.psgd_embed_grad.argtypes = [vp, vp, i64, ctypes.c_int, vp, ctypes.c_int, i64, i64, i64, ctypes.c_float,
                                     vp, i64, ctypes.c_int, vp, i64, vp]
-    u64, cint, mxp = ctypes.c_uint64, ctypes.c_int, ctypes.POINTER(psgd_mx_tensor)
+    u64, cint, mxp = ctypes.c_uint64, ctypes.c_int, vp          # vp: the cheapest to convert to
     lib.psgd_adamw_plan_create.argtypes = [vp, ctypes.POINTER(psgd_adamw_tensor), cint, cint, cint, cint, ctypes.POINTER(vp)]
     lib.psgd_adamw_plan_destroy.argtypes = [vp]
     lib.psgd_adamw_prepare.argtypes = [vp, vp, ctypes.c_float, vp, vp, vp, vp, vp]
@@ -717,7 +717,7 @@ def psgd_mx_bytes(rows: int, k: int) -> int:
 
 
 def _mx(t):
-    return None if t is None else ctypes.byref(psgd_mx_tensor(_ptr(t.data), t.rows, t.k))
+    return None if t is None else ctypes.byref(t.struct)
 
 
 def psgd_mx_quantize(ctx: int, x, row=None, col=None, stochastic: bool = False, seed: int = 0, step=None, stream=None) -> None:
@@ -730,7 +730,7 @@ def psgd_mx_quantize(ctx: int, x, row=None, col=None, stochastic: bool = False, 
     if step is not None and step.dtype != torch.int32:
         raise PsgdError(call, PSGD_EDTYPE, "step must be int32")
     m, n = x.shape
-    _same_device(call, x, *[t.data for t in (row, col) if t is not None], *([] if step is None else [step]), ctx=ctx)
+    _same_device(call, x, *(t for t in (row and row.data, col and col.data, step) if t is not None), ctx=ctx)
     _check(ctx, call, load_library().psgd_mx_quantize(
         ctx, _ptr(x), _row_stride(x, call), m, n, _dtype(x, call), _mx(row), _mx(col), _rounding(stochastic),
         seed & 0xFFFFFFFFFFFFFFFF, _ptr(step), _stream(stream, x.device.index)))

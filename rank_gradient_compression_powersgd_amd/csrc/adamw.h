@@ -28,8 +28,14 @@ struct AdamwArgs {
   uint64_t seed;
 };
 
-hipError_t launch_adamw_norm(const AdamwChunk* chunks, int64_t n, int gt, double* partial, float max_norm, const int32_t* skip_in,
-                             int32_t* skip, int32_t* step, float* norm, hipStream_t s);
+struct AdamwNorm {
+  double* partial;                      // sums of the workgroups
+  float max_norm;
+  const int32_t* skip_in;               // or NULL
+  int32_t* skip; int32_t* step; float* norm;
+};
+
+hipError_t launch_adamw_norm(const AdamwChunk* chunks, int64_t n, int gt, const AdamwNorm& a, hipStream_t s);
 hipError_t launch_adamw(const AdamwChunk* chunks, int64_t n, int pt, int gt, bool low, bool stochastic, const AdamwArgs& a, hipStream_t s);
 hipError_t launch_adamw_moments(const uint8_t* m1, const uint8_t* e1, const uint8_t* m2, const uint8_t* e2, int64_t n, void* out1,
                                 void* out2, int ot, hipStream_t s);

@@ -114,6 +114,30 @@ __device__ __forceinline__ float fast_sqrt(float v) {
   return __builtin_amdgcn_sqrtf(tiny ? v * 0x1p64f : v) * (tiny ? 0x1p-32f : 1.0f);
 }
 
+// Sum of a workgroup's values, in thread 0.
+__device__ __forceinline__ double block_sum(double v, double* red) {
+#pragma unroll
+  for (int w = kWave / 2; w > 0; w >>= 1) v += __shfl_xor(v, w);
+  if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x / kWave] = v;
+  __syncthreads();
+  return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// The skip decision, and on a step that is not skipped t, norm and clipping factor. A sum of squares in
+// fp64 of fp32 values is finite exactly when they all are.
+__device__ __forceinline__ void finish_norm(const AdamwNorm& a, double total) {
+  const bool bad = !(total < __builtin_inf()) || (a.skip_in && *a.skip_in != 0);
+  *a.skip = bad ? 1 : 0;
+  if (bad) return;
+  *a.step = *a.step + 1;
+  const double norm = sqrt(total);
+  a.norm[0] = (float)norm;
+  a.norm[1] = (float)(a.max_norm > 0.0f && norm > (double)a.max_norm ? (double)a.max_norm / norm : 1.0);
+}
+
+// Sums of squares, one per workgroup. Adding them up takes a launch of its own (2 to 4 us): left to the
+// workgroup that is done last, the fences that make the sums visible across XCDs cost each workgroup
+// more (23.6 million elements: 15 -> 77 us).
 template <int GT>
 __global__ __launch_bounds__(kThreads)
 void k_adamw_sqnorm(const AdamwChunk* __restrict__ chunks, int64_t n, double* __restrict__ partial) {
@@ -124,52 +148,39 @@ void k_adamw_sqnorm(const AdamwChunk* __restrict__ chunks, int64_t n, double* __
     const void* g = c.grad;
     const int len = c.n;
     f32x4 v[kTurns];
+    if (len == kAdamwChunk) {
 #pragma unroll
-    for (int u = 0; u < kTurns; ++u) {
-      const int i = (u * kThreads + threadIdx.x) * kPer;
-      if (i + kPer <= len) v[u] = load_four<GT>(g, i);
-      else v[u] = load_some<GT>(g, i, len - i);
+      for (int u = 0; u < kTurns; ++u) v[u] = load_four<GT>(g, (u * kThreads + threadIdx.x) * kPer);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kTurns; ++u) {
+        const int i = (u * kThreads + threadIdx.x) * kPer;
+        if (i + kPer <= len) v[u] = load_four<GT>(g, i);
+        else v[u] = load_some<GT>(g, i, len - i);
+      }
     }
 #pragma unroll
     for (int u = 0; u < kTurns; ++u)
 #pragma unroll
       for (int j = 0; j < kPer; ++j) acc += (double)v[u][j] * (double)v[u][j];
   }
-#pragma unroll
-  for (int w = kWave / 2; w > 0; w >>= 1) acc += __shfl_xor(acc, w);
-  if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x / kWave] = acc;
-  __syncthreads();
-  if (threadIdx.x == 0) partial[blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
+  const double sum = block_sum(acc, red);
+  if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
-// The sums in order; the skip decision, and on a step that is not skipped t, norm and clipping factor.
-// A sum of squares in fp64 of fp32 values is finite exactly when they all are.
 __global__ __launch_bounds__(kThreads)
-void k_adamw_finalize(const double* __restrict__ partial, int n, float max_norm, const int32_t* skip_in, int32_t* skip,
-                      int32_t* __restrict__ step, float* __restrict__ norm_out) {
+void k_adamw_finalize(const double* __restrict__ partial, int n, AdamwNorm a) {
   __shared__ double red[kThreads / kWave];
   double acc = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) acc += partial[i];
-#pragma unroll
-  for (int w = kWave / 2; w > 0; w >>= 1) acc += __shfl_xor(acc, w);
-  if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x / kWave] = acc;
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  const double total = (red[0] + red[1]) + (red[2] + red[3]);
-  const bool bad = !(total < __builtin_inf()) || (skip_in && *skip_in != 0);
-  *skip = bad ? 1 : 0;
-  if (bad) return;
-  *step = *step + 1;
-  const double norm = sqrt(total);
-  norm_out[0] = (float)norm;
-  norm_out[1] = (float)(max_norm > 0.0f && norm > (double)max_norm ? (double)max_norm / norm : 1.0);
+  const double total = block_sum(acc, red);
+  if (threadIdx.x == 0) finish_norm(a, total);
 }
 
-template <int PT, int GT, bool LOW, bool SR>
-__global__ __launch_bounds__(kThreads)
-void k_adamw(const AdamwChunk* __restrict__ chunks, AdamwArgs a) {
-  const AdamwChunk c = chunks[blockIdx.x];
-  if (*a.skip != 0) return;
+// WHOLE: a chunk of kAdamwChunk elements, no bounds to look at (with them the loads wait for one another).
+template <int PT, int GT, bool LOW, bool SR, bool WHOLE>
+__device__ __forceinline__ void adamw_chunk(const AdamwChunk& c, const AdamwArgs& a) {
+  constexpr bool whole = WHOLE;
   const float clip = a.norm ? a.norm[1] : 1.0f;
   const int step = *a.step;
   const int len = c.n, room = (len + kAdamwGroup - 1) / kAdamwGroup * kAdamwGroup;
@@ -179,14 +190,14 @@ void k_adamw(const AdamwChunk* __restrict__ chunks, AdamwArgs a) {
 #pragma unroll
   for (int u = 0; u < kTurns; ++u) {
     const int i = (u * kThreads + threadIdx.x) * kPer;
-    if (i + kPer <= len) {
+    if (whole || i + kPer <= len) {
       p[u] = load_four<PT>(c.param, i);
       g[u] = load_four<GT>(c.grad, i);
     } else {
       p[u] = load_some<PT>(c.param, i, len - i);
       g[u] = load_some<GT>(c.grad, i, len - i);
     }
-    if (i < room) {
+    if (whole || i < room) {
       if constexpr (LOW) {
         c1[u] = *gcast<uint32_t>(gbl(static_cast<const uint8_t*>(c.m1)) + i);
         c2[u] = *gcast<uint32_t>(gbl(static_cast<const uint8_t*>(c.m2)) + i);
@@ -206,7 +217,7 @@ void k_adamw(const AdamwChunk* __restrict__ chunks, AdamwArgs a) {
 #pragma unroll
   for (int u = 0; u < kTurns; ++u) {
     const int i = (u * kThreads + threadIdx.x) * kPer;
-    if (i >= room) continue;
+    if (!whole && i >= room) continue;
     uint32_t r[kPer];
     typename Elem<PT>::one out[kPer];
 #pragma unroll
@@ -223,7 +234,7 @@ void k_adamw(const AdamwChunk* __restrict__ chunks, AdamwArgs a) {
       const float gc = g[u][j] * clip;
       a1 = a1 * a.beta1 + gc * omb1;
       a2 = a2 * a.beta2 + (gc * gc) * omb2;
-      if (i + j >= len) a1 = a2 = 0.0f;
+      if (!whole && i + j >= len) a1 = a2 = 0.0f;
       const float upd = (a1 * rbc1) * __builtin_amdgcn_rcpf(fast_sqrt(a2 * rbc2) + a.eps);
       const float th = p[u][j];
       out[j] = to_param<PT, SR>(th - a.lr * (upd + a.weight_decay * th), SR && PT != G_F32 ? hash_more(r[j]) : 0);
@@ -231,7 +242,7 @@ void k_adamw(const AdamwChunk* __restrict__ chunks, AdamwArgs a) {
       m2[u][j] = a2;
     }
     typename Elem<PT>::one* po = static_cast<typename Elem<PT>::one*>(c.param);
-    if (i + kPer <= len) {
+    if (whole || i + kPer <= len) {
       *gcast<typename Elem<PT>::four>(gbl(po) + i) = typename Elem<PT>::four{out[0], out[1], out[2], out[3]};
     } else {
 #pragma unroll
@@ -257,6 +268,15 @@ void k_adamw(const AdamwChunk* __restrict__ chunks, AdamwArgs a) {
       *gcast<f32x4>(gbl(static_cast<float*>(c.m2)) + i) = m2[u];
     }
   }
+}
+
+template <int PT, int GT, bool LOW, bool SR>
+__global__ __launch_bounds__(kThreads)
+void k_adamw(const AdamwChunk* __restrict__ chunks, AdamwArgs a) {
+  const AdamwChunk c = chunks[blockIdx.x];
+  if (*a.skip != 0) return;
+  if (c.n == kAdamwChunk) adamw_chunk<PT, GT, LOW, SR, true>(c, a);
+  else adamw_chunk<PT, GT, LOW, SR, false>(c, a);
 }
 
 // Values of 8-bit moments, 4 a lane; blockIdx.y picks the moment. bf16 holds every value but those
@@ -294,17 +314,16 @@ void go(const AdamwChunk* chunks, int64_t n, bool low, bool sr, const AdamwArgs&
 
 }  // namespace
 
-hipError_t launch_adamw_norm(const AdamwChunk* chunks, int64_t n, int gt, double* partial, float max_norm, const int32_t* skip_in,
-                             int32_t* skip, int32_t* step, float* norm, hipStream_t s) {
+hipError_t launch_adamw_norm(const AdamwChunk* chunks, int64_t n, int gt, const AdamwNorm& a, hipStream_t s) {
   const int grid = (int)(n < kAdamwNormGrid ? n : kAdamwNormGrid);
   if (grid > 0) {
-    if (gt == G_F32) k_adamw_sqnorm<G_F32><<<dim3(grid), dim3(kThreads), 0, s>>>(chunks, n, partial);
-    else if (gt == G_F16) k_adamw_sqnorm<G_F16><<<dim3(grid), dim3(kThreads), 0, s>>>(chunks, n, partial);
-    else k_adamw_sqnorm<G_BF16><<<dim3(grid), dim3(kThreads), 0, s>>>(chunks, n, partial);
+    if (gt == G_F32) k_adamw_sqnorm<G_F32><<<dim3(grid), dim3(kThreads), 0, s>>>(chunks, n, a.partial);
+    else if (gt == G_F16) k_adamw_sqnorm<G_F16><<<dim3(grid), dim3(kThreads), 0, s>>>(chunks, n, a.partial);
+    else k_adamw_sqnorm<G_BF16><<<dim3(grid), dim3(kThreads), 0, s>>>(chunks, n, a.partial);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  k_adamw_finalize<<<dim3(1), dim3(kThreads), 0, s>>>(partial, grid, max_norm, skip_in, skip, step, norm);
+  k_adamw_finalize<<<dim3(1), dim3(kThreads), 0, s>>>(a.partial, grid, a);
   return hipGetLastError();
 }
 

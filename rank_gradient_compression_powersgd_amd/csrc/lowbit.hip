@@ -153,8 +153,8 @@ psgd_status psgd_adamw_prepare(psgd_ctx* ctx, psgd_adamw_plan* plan, float max_n
   if (std::isnan(max_norm)) return fail(ctx, PSGD_EINVAL, "max_norm is NaN");
   DeviceGuard dev(ctx->device);
   HIPCHK(ctx, dev.err, "hipSetDevice");
-  HIPCHK(ctx, psgd::launch_adamw_norm(plan->chunks, plan->n_chunks, plan->gt, plan->partial, max_norm, skip_in, skip_dev, step_dev,
-                                      norm_dev, stream), "gradient norm");
+  const psgd::AdamwNorm a{plan->partial, max_norm, skip_in, skip_dev, step_dev, norm_dev};
+  HIPCHK(ctx, psgd::launch_adamw_norm(plan->chunks, plan->n_chunks, plan->gt, a, stream), "gradient norm");
   return PSGD_OK;
 }
 

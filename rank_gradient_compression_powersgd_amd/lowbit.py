@@ -74,9 +74,12 @@ class AdamWGroup:
         decided before (PowerSGDGroup.skip, where the gradients are its decompressed ones), or None."""
         if skip is not None:
             B._same_device("psgd_adamw_prepare", self.skip, skip, ctx=self.ctx)
-        stream = B._stream(stream, self.device)
-        B.psgd_adamw_prepare(self.ctx, self.plan, max_norm, skip, self.skip, self.step_count, self.norm, stream)
-        B.psgd_adamw_update(self.ctx, self.plan, self.skip, self.step_count, self.norm, hp, self.stochastic, self.seed, stream)
+        h = B._hparams(hp)
+        lib, st, ctx, plan = B.load_library(), B._stream(stream, self.device.index), self.ctx, self.plan
+        words = self.skip.data_ptr(), self.step_count.data_ptr(), self.norm.data_ptr()
+        B._check(ctx, "psgd_adamw_prepare", lib.psgd_adamw_prepare(ctx, plan, max_norm, B._ptr(skip), *words, st))
+        B._check(ctx, "psgd_adamw_update", lib.psgd_adamw_update(ctx, plan, *words, B.ctypes.byref(h), int(self.stochastic),
+                                                                 self.seed & 0xFFFFFFFFFFFFFFFF, st))
 
     def state(self):
         """The moments, for the constructor's `moments`; step_count belongs to a checkpoint as well."""
@@ -87,10 +90,13 @@ class AdamWGroup:
         import torch
         if self.bits == 32:
             return self.m1, self.m2
-        out = [torch.empty(self.m1.numel(), dtype=dtype or torch.bfloat16, device=self.device) for _ in range(2)]
-        if out[0].numel():
-            B.psgd_adamw_moments(self.ctx, self.m1, self.e1, self.m2, self.e2, *out, B._stream(stream, self.device))
-        return out[0], out[1]
+        kind, n = dtype or torch.bfloat16, self.m1.numel()
+        out1, out2 = torch.empty(n, dtype=kind, device=self.device), torch.empty(n, dtype=kind, device=self.device)
+        call = "psgd_adamw_moments"
+        B._check(self.ctx, call, B.load_library().psgd_adamw_moments(
+            self.ctx, self.m1.data_ptr(), self.e1.data_ptr(), self.m2.data_ptr(), self.e2.data_ptr(), n, out1.data_ptr(), out2.data_ptr(),
+            B._dtype(out1, call), B._stream(stream, self.device.index)))
+        return out1, out2
 
     def close(self):
         if getattr(self, "plan", None):
@@ -113,13 +119,15 @@ class MxTensor:
 
     def __init__(self, rows: int, k: int, device=None, data=None):
         import torch
-        self.rows, self.k = int(rows), int(k)
-        need = B.psgd_mx_bytes(self.rows, self.k)
+        self.rows, self.k = rows, k = int(rows), int(k)
+        # as the library counts (a refused size is its refusal)
+        need = -(-k // 128) * (rows * 64 + -(-rows // 64) * 256) if 0 <= rows <= 1 << 25 and 0 <= k <= 1 << 25 else B.psgd_mx_bytes(rows, k)
         if data is None:
             data = torch.empty(need, dtype=torch.uint8, device=device or "cuda")
         elif data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() < need:
             raise B.PsgdError("psgd_mx_bytes", B.PSGD_EINVAL, f"data must be {need} contiguous bytes")
         self.data = data
+        self.struct = B.psgd_mx_tensor(data.data_ptr(), rows, k)
 
 
 class MxLinear:

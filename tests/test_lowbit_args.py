@@ -115,6 +115,7 @@ class _Data:
 
     def __init__(self, rows, k, index):
         self.rows, self.k, self.data = rows, k, _On(torch.zeros(B.psgd_mx_bytes(rows, k), dtype=torch.uint8), index)
+        self.struct = B.psgd_mx_tensor(0, rows, k)
 
 
 def test_calls_take_the_stream_of_their_device_and_refuse_another(lib, monkeypatch):  # noqa: F811
