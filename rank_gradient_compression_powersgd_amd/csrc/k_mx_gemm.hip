@@ -254,24 +254,26 @@ void k_mx_gemm(MxProduct a, int items) {
     }
   };
   constexpr int PER = TL::LOADS + TL::SLOADS;
-  // loads x = 0 .. PER - 1 of the next stage, in this order; STAY: it is not its item's last
-  auto send = [&](int x, auto stay) {
+  // loads x = 0 .. PER - 1 of the next stage, and then sent()
+  auto send = [&](int x) {
     if (x < TL::LOADS) {
       load_lds16(gcast<uint16_t>(codes), off[x], send_to + lcodes + x * 1024);
     } else {
       const int id = ((wv & 1) * TL::SLOADS + x - TL::LOADS) % (TL::WORDS / 2);
       load_lds4(scales, soff[x - TL::LOADS], send_to + lscales + id * 256);
     }
-    if (x < PER - 1) return;
-    ++ahead;
+  };
+  auto sent = [&] {
     send_to = send_to == (RING - 1) * TL::STAGE ? 0 : send_to + TL::STAGE;
     codes += step;
     scales += sstep;
-    --send_left;
-    if (!decltype(stay)::value && send_left == 0) {
-      send_slot += slots;
-      if (send_slot < end) aim();
-    }
+  };
+  auto sent_one = [&] {                                      // and on to the next item
+    sent();
+    ++ahead;
+    if (--send_left > 0) return;
+    send_slot += slots;
+    if (send_slot < end) aim();
   };
   auto more = [&] { return send_slot < end; };
 
@@ -322,18 +324,15 @@ void k_mx_gemm(MxProduct a, int items) {
   // wave is this far. ahead: stages sent for and not multiplied, this one among them.
   // STEADY: four stages ahead, nothing late.
   auto turn = [&](Frag& now, auto steady) {
-    if (decltype(steady)::value) {
+    if (decltype(steady)::value || (ahead >= 4 && late == 0)) {
       wait_loads<2 * PER>();
+    } else if (ahead >= 4) {
+      wait_loads<LATE ? 2 * PER + STORES : 0>();
+      --late;
+    } else if (ahead == 3) {
+      wait_loads<PER>();
     } else {
-      if (ahead >= 4) {
-        if (LATE && late > 0) wait_loads<LATE ? 2 * PER + STORES : 0>();
-        else wait_loads<2 * PER>();
-      } else if (ahead == 3) {
-        wait_loads<PER>();
-      } else {
-        wait_loads<0>();
-      }
-      if (late > 0) --late;
+      wait_loads<0>();
     }
     if (PAIRS || TL::S < kMxGroup) {
 #pragma unroll
@@ -361,7 +360,7 @@ void k_mx_gemm(MxProduct a, int items) {
       if constexpr (H >= LFIRST) {
         if (sends) {
 #pragma unroll
-          for (int x = (H - LFIRST) * PER / LSTEPS; x < (H - LFIRST + 1) * PER / LSTEPS; ++x) send(x, steady);
+          for (int x = (H - LFIRST) * PER / LSTEPS; x < (H - LFIRST + 1) * PER / LSTEPS; ++x) send(x);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -370,7 +369,12 @@ void k_mx_gemm(MxProduct a, int items) {
       __builtin_amdgcn_sched_barrier(0);
     });
     read_done();
-    --ahead;
+    if (decltype(steady)::value) {
+      sent();
+    } else {
+      if (sends) sent_one();
+      --ahead;
+    }
   };
 
   // ---- results -------------------------------------------------------------------------------------------
@@ -436,7 +440,8 @@ void k_mx_gemm(MxProduct a, int items) {
   for (int j = 0; j < RING; ++j)
     if (more()) {
 #pragma unroll
-      for (int x = 0; x < PER; ++x) send(x, std::false_type{});
+      for (int x = 0; x < PER; ++x) send(x);
+      sent_one();
     }
   if (ahead == 4) wait_loads<3 * PER>();
   else wait_loads<0>();
@@ -452,16 +457,10 @@ void k_mx_gemm(MxProduct a, int items) {
   bool fresh = true;
   // one stage; false behind the last
   auto stage = [&](Frag& now, Frag& next) {
-    using Yes = std::true_type;
     using No = std::false_type;
-    if (!fresh && ahead == 4 && late == 0 && send_left > 1 && more()) {
-      turn(now, Yes{});
-      mul(now, next, No{}, Yes{});
-    } else {
-      turn(now, No{});
-      if (fresh) mul(now, next, Yes{}, No{});
-      else mul(now, next, No{}, No{});
-    }
+    turn(now, No{});
+    if (fresh) mul(now, next, std::true_type{}, No{});
+    else mul(now, next, No{}, No{});
     fresh = --it.stages == 0;
     if (!fresh) return true;
     results(it);
@@ -470,7 +469,22 @@ void k_mx_gemm(MxProduct a, int items) {
     it = locate(slot);
     return true;
   };
-  while (stage(f0, f1) && stage(f1, f0)) {}
+  // Most stages pass through a loop without choices: with one wave a SIMD nothing else runs while a wave
+  // branches.
+  do {
+    if (!fresh && ahead == 4 && late == 0 && more()) {
+      using Yes = std::true_type;
+      const int twos = (min(send_left, it.stages) - 1) / 2;
+      send_left -= 2 * twos;
+      it.stages -= 2 * twos;
+      for (int x = 0; x < twos; ++x) {
+        turn(f0, Yes{});
+        mul(f0, f1, std::false_type{}, Yes{});
+        turn(f1, Yes{});
+        mul(f1, f0, std::false_type{}, Yes{});
+      }
+    }
+  } while (stage(f0, f1) && stage(f1, f0));
 }
 
 // The parts of a split product, added in order.
@@ -524,15 +538,30 @@ hipError_t go(const MxProduct& a, int tile, hipStream_t s) {
 
 }  // namespace
 
+// Tiles and parts by a sum of what they cost, in microseconds: a launch that ends with one tile's results,
+// stages of the CU with most tiles, and the parts' way through memory. Measured, tiles of 256 / 128 / 64:
+//   1280 x 1984, k = 3968    28.3 / 13.8 / 14.1     512 x 4096, k = 4096      27.9 / 13.4 / 11.5
+//   2048 x 2048, k = 2048    19.6 / 10.6 / 12.4     4096 x 4096, k = 4096     40.6 / 49.0 / 69.0
+//   20480 x 1984, k = 3968   88.5 / 95.3 / 144      20480 x 15872, k = 3968    601 /  726 / 1170
+// and in two parts 1280 x 1984, k = 3968: 33.3 / 23.8 / 22.6; 3968 x 1488, k = 20480: 104 / 77.6 / 103 whole,
+// 79.6 / 84.1 / 118 in two parts.
 MxPlan mx_plan(int64_t m, int64_t n, int64_t panels) {
   if (m <= 64) return {0, 1};
-  auto tiles = [&](int64_t t) { return ((m + t - 1) / t) * ((n + t - 1) / t); };
-  int tile = 64;
-  if (tiles(256) >= 192) tile = 256;
-  else if (tiles(128) >= 192 || panels >= 64) tile = 128;
-  int splits = 1;
-  while (splits < 8 && tiles(tile) * splits < 192 && panels / (2 * splits) >= 8) splits *= 2;
-  return {tile, splits};
+  static constexpr struct { int tile; double start, stage; } kinds[] = {{64, 4.9, 0.11}, {128, 4.8, 0.27}, {256, 8.3, 0.80}};
+  MxPlan best{64, 1};
+  double least = 0;
+  for (const auto& k : kinds) {
+    const int64_t tiles = ((m + k.tile - 1) / k.tile) * ((n + k.tile - 1) / k.tile);
+    for (int splits = 1; splits <= 8 && (splits == 1 || panels / splits >= 8); splits *= 2) {
+      double cost = k.start + (double)((tiles * splits + 255) / 256) * (double)((panels + splits - 1) / splits) * k.stage;
+      if (splits > 1) cost += 4.0 + 8.0 * (double)m * (double)n * splits / 2.9e6;
+      if (least == 0 || cost < least) {
+        least = cost;
+        best = {k.tile, splits};
+      }
+    }
+  }
+  return best;
 }
 
 hipError_t launch_mx_product(const MxProduct& a, int tile, int ot, hipStream_t s) {
