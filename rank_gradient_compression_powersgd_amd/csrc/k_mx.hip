@@ -107,6 +107,10 @@ template <int IT> struct Pair {
     if (both) w = *gcast<u32_u>(static_cast<const GLOBAL uint16_t*>(x));
     else if (any) w = *static_cast<const GLOBAL uint16_t*>(x);
   }
+  __device__ __forceinline__ void load_each(const GLOBAL void* x, const GLOBAL void* y, bool first, bool second) {
+    const uint32_t a = *static_cast<const GLOBAL uint16_t*>(x), b = *static_cast<const GLOBAL uint16_t*>(y);
+    w = (first ? a : 0) | (second ? b << 16 : 0);
+  }
   __device__ __forceinline__ static void load4(Pair (&p)[4], const GLOBAL void* x) {
     const u32x4_u v = *gcast<u32x4_u>(static_cast<const GLOBAL uint16_t*>(x));
 #pragma unroll
@@ -149,6 +153,12 @@ template <> struct Pair<G_F32> {
     } else if (any) {
       v = *static_cast<const GLOBAL float*>(p);
     }
+  }
+  __device__ __forceinline__ void load_each(const GLOBAL void* x, const GLOBAL void* y, bool first, bool second) {
+    v = *static_cast<const GLOBAL float*>(x);
+    w = *static_cast<const GLOBAL float*>(y);
+    if (!first) v = 0.0f;
+    if (!second) w = 0.0f;
   }
   __device__ __forceinline__ static void load4(Pair (&p)[4], const GLOBAL void* x) {
     const f32x8_u v = *gcast<f32x8_u>(static_cast<const GLOBAL float*>(x));
@@ -225,8 +235,18 @@ void k_mx_cols(MxQuantize a) {
   const bool both = c0 + 1 < a.n, any = c0 < a.n;
   Pair<IT> v[32];
   const GLOBAL one* x = gbl(static_cast<const one*>(a.x)) + r0 * a.ld + c0;
+  if (rows == 32 && (panel_n + 1) * kMxPanel <= a.n) {       // all of the wave's: loads without a branch between them
 #pragma unroll
-  for (int r = 0; r < 32; ++r) v[r].load(x + r * a.ld, both && r < rows, any && r < rows);
+    for (int r = 0; r < 32; ++r) v[r].load(x + r * a.ld, true, true);
+  } else {                                                   // the matrix's nearest elements in the place of those past it
+    const GLOBAL one* e = gbl(static_cast<const one*>(a.x));
+    const int64_t e0 = any ? c0 : a.n - 1, e1 = both ? c0 + 1 : a.n - 1;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      const int64_t row = (r < rows ? r0 + r : a.m - 1) * a.ld;
+      v[r].load_each(e + row + e0, e + row + e1, any && r < rows, both && r < rows);
+    }
+  }
 
   typename Pair<IT>::mags high{0, 0};
 #pragma unroll
@@ -237,8 +257,9 @@ void k_mx_cols(MxQuantize a) {
   const uint32_t half = (uint32_t)((a.n + 1) / 2);
   const PairBits bits(SR ? hash_key(a.seed, a.step ? (uint32_t)*a.step : 0, 0) : 0, r0 * (int64_t)half + c0 / 2);
   const uint32_t perm_odd = lane & 1 ? 0x07030501u : 0x02060004u, perm_two = lane & 2 ? 0x07060302u : 0x01000504u;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {                              // 16 rows
+  GLOBAL uint8_t* ro = gbl(a.row.codes) + (panel_n * a.row.rows + r0 + (lane & 3)) * kMxRowBytes + 4 * (lane >> 2);
+  each<2>([&](auto hh) {                                     // 16 rows
+    constexpr int h = decltype(hh)::value;
     uint32_t s = 0, f = 0;                                   // exponent and factor of row lane % 16, block lane / 16
     bool bad = false;
     if constexpr (ROWS) {
@@ -253,6 +274,7 @@ void k_mx_cols(MxQuantize a) {
     }
     each<4>([&](auto dd) {                                   // 4 rows
       constexpr int D = decltype(dd)::value;
+      __builtin_amdgcn_sched_barrier(0);                     // the bits of more rows at once take registers of other waves
       const int r = 16 * h + 4 * D;
       uint32_t w[4];
 #pragma unroll
@@ -272,6 +294,7 @@ void k_mx_cols(MxQuantize a) {
       const uint32_t p0 = __builtin_amdgcn_perm(b0[1], b0[0], 0x0c0c0400u), p1 = __builtin_amdgcn_perm(b1[1], b1[0], 0x0c0c0400u);
       k0[2 * h + D / 2] = D & 1 ? k0[2 * h + D / 2] | p0 << 16 : p0;
       k1[2 * h + D / 2] = D & 1 ? k1[2 * h + D / 2] | p1 << 16 : p1;
+      asm volatile("" : "+v"(k0[2 * h + D / 2]), "+v"(k1[2 * h + D / 2]));   // here, not with their store: the bits would stay till then
       if constexpr (ROWS) {
         uint32_t rb[4];
         each<4>([&](auto tt) {
@@ -279,17 +302,16 @@ void k_mx_cols(MxQuantize a) {
           const float fr = __builtin_bit_cast(float, dpp<kBcast + 4 * D + T>(f));
           if constexpr (SR) rb[T] = pack2_random(v[r + T].x(), v[r + T].y(), fr, w[T], turn16(w[T]));
           else rb[T] = v[r + T].nearest(fr);
-          if (bad) rb[T] = dpp<kBcast + 4 * D + T>(s) == 255 ? 0 : rb[T];
         });
         // 4 rows x 4 lanes of bytes, transposed: lane j of 4 gets row j's
         const uint32_t rw = join4(rb[0], rb[1], rb[2], rb[3]);
         uint32_t y = __builtin_amdgcn_perm(rw, dpp<kXor1>(rw), perm_odd);
         y = __builtin_amdgcn_perm(y, dpp<kXor2>(y), perm_two);
-        const int row = r + (lane & 3);
-        if (row < rows) *gcast<uint32_t>(gbl(a.row.codes) + (panel_n * a.row.rows + r0 + row) * kMxRowBytes + 4 * (lane >> 2)) = y;
+        if (bad && __builtin_amdgcn_ds_bpermute(4 * ((lane & 48) + 4 * D + (lane & 3)), (int)s) == 255) y = 0;
+        if (r + (lane & 3) < rows) *gcast<uint32_t>(ro + r * kMxRowBytes) = y;
       }
     });
-  }
+  });
   GLOBAL uint8_t* o = gbl(a.col.codes) + (panel_m * a.col.rows + c0) * kMxRowBytes + 16 * wv;
   if (any) {
     *gcast<u32x4>(o) = s0 == 255 ? u32x4{0, 0, 0, 0} : u32x4{k0[0], k0[1], k0[2], k0[3]};
