@@ -228,7 +228,7 @@ template <int IT, bool ROWS, bool SR>
 __global__ __launch_bounds__(kThreads)
 void k_mx_cols(MxQuantize a) {
   typedef typename Elem<IT>::one one;
-  const int lane = threadIdx.x & (kWave - 1), wv = threadIdx.x / kWave;
+  const int lane = threadIdx.x & (kWave - 1), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int64_t pn = (a.n + kMxPanel - 1) / kMxPanel, panel_m = blockIdx.x / pn, panel_n = blockIdx.x - panel_m * pn;
   const int64_t r0 = panel_m * kMxPanel + 32 * wv, c0 = panel_n * kMxPanel + 2 * lane;
   const int rows = (int)(a.m - r0 < 32 ? a.m - r0 : 32);     // of the block that exist, maybe none

@@ -425,6 +425,25 @@ void k_mx_gemm(MxProduct a, int items) {
         });
         o += 16 * a.ldc;
       });
+    } else if (it.i0 + T <= a.n && it.j0 + T <= a.m) {
+      GLOBAL float* o = gbl(static_cast<float*>(a.c)) + (j0 + c) * a.ldc + i0 + 4 * g;
+      f32x4 old[2][N];                                       // of this row of tiles and the next: their way takes longer than the rest
+      auto get = [&](int y) {
+#pragma unroll
+        for (int x = 0; x < N; ++x) old[y & 1][x] = *gcast<f32x4_u>(o + 16 * y * a.ldc + 16 * x);
+      };
+#pragma unroll
+      for (int x = 0; x < 2 * N; ++x) old[x / N][x % N] = f32x4{0, 0, 0, 0};
+      if (a.accumulate) get(0);
+      each<N>([&](auto yy) {
+        constexpr int Y = decltype(yy)::value;
+        if (Y + 1 < N && a.accumulate) get(Y + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        each<N>([&](auto xx) {
+          constexpr int X = decltype(xx)::value;
+          *gcast<f32x4_u>(o + 16 * Y * a.ldc + 16 * X) = sum_of<X * N + Y>() * scale + old[Y & 1][X];
+        });
+      });
     } else {
       each<N>([&](auto yy) {
         constexpr int Y = decltype(yy)::value;
