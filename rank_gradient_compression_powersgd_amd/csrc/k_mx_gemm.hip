@@ -414,7 +414,7 @@ void k_mx_gemm(MxProduct a, int items) {
           const f32x4 v = sum_of<X * N + Y>() * scale, w = sum_of<(X + 1) * N + Y>() * scale;
           const eight u = __builtin_convertvector(f32x8{v[0], v[1], v[2], v[3], w[0], w[1], w[2], w[3]}, eight);
           if (16 * Y < rows && 16 * X < cols) {
-            if (eights) {
+            if (eights || 16 * X + 8 <= cols) {
               *gcast<eight>(o + 16 * X) = u;
             } else {
 #pragma unroll
@@ -557,24 +557,26 @@ hipError_t go(const MxProduct& a, int tile, hipStream_t s) {
 
 }  // namespace
 
-// Tiles and parts by a sum of what they cost, in microseconds: a launch that ends with one tile's results,
-// stages of the CU with most tiles, and the parts' way through memory. Measured, tiles of 256 / 128 / 64:
+// Kernel, tiles and parts by a sum of what they cost, in microseconds: a launch that ends with one tile's
+// results, stages of the CU with most tiles, and the parts' way through memory; for few rows a launch, and
+// what its workgroups read, at the rate of the L2s. Measured, tiles of 256 / 128 / 64:
 //   1280 x 1984, k = 3968    28.3 / 13.8 / 14.1     512 x 4096, k = 4096      27.9 / 13.4 / 11.5
 //   2048 x 2048, k = 2048    19.6 / 10.6 / 12.4     4096 x 4096, k = 4096     40.6 / 49.0 / 69.0
 //   20480 x 1984, k = 3968   88.5 / 95.3 / 144      20480 x 15872, k = 3968    601 /  726 / 1170
-// and in two parts 1280 x 1984, k = 3968: 33.3 / 23.8 / 22.6; 3968 x 1488, k = 20480: 104 / 77.6 / 103 whole,
-// 79.6 / 84.1 / 118 in two parts.
+// in two parts 1280 x 1984, k = 3968: 33.3 / 23.8 / 22.6; 3968 x 1488, k = 20480: 104 / 77.6 / 103 whole,
+// 79.6 / 84.1 / 118 in two parts; few rows / tiles of 64, 64 x 1984, k = 3968: 4.9 / 8.3; 64 x 11904: 11.8 / 9.0;
+// 16 x 11904: 5.5 / 8.6; 1 x 32768, k = 4096: 18.0 / 14.0.
 MxPlan mx_plan(int64_t m, int64_t n, int64_t panels) {
-  if (m <= 64) return {0, 1};
   static constexpr struct { int tile; double start, stage; } kinds[] = {{64, 4.9, 0.11}, {128, 4.8, 0.27}, {256, 8.3, 0.80}};
-  MxPlan best{64, 1};
-  double least = 0;
+  MxPlan best{0, 1};
+  double least = -1;
+  if (m <= 64) least = 2.6 + (double)((n + 15) / 16) * (double)(((m + 15) / 16 + 1) * panels) * 16 * kMxRowBytes / 13e6;
   for (const auto& k : kinds) {
     const int64_t tiles = ((m + k.tile - 1) / k.tile) * ((n + k.tile - 1) / k.tile);
     for (int splits = 1; splits <= 8 && (splits == 1 || panels / splits >= 8); splits *= 2) {
       double cost = k.start + (double)((tiles * splits + 255) / 256) * (double)((panels + splits - 1) / splits) * k.stage;
       if (splits > 1) cost += 4.0 + 8.0 * (double)m * (double)n * splits / 2.9e6;
-      if (least == 0 || cost < least) {
+      if (least < 0 || cost < least) {
         least = cost;
         best = {k.tile, splits};
       }

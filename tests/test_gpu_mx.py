@@ -249,6 +249,38 @@ def test_products_of_full_tiles_and_long_sums(ctx, mnk):
     _product(ctx, *mnk, scale=0.5, accumulate=True)
 
 
+@pytest.mark.parametrize("mnk,kind", [((64, 20000, 1001), "bf16"), ((1, 32768, 4096), "f16"), ((4090, 4090, 2050), "bf16"),
+                                      ((4090, 4090, 2050), "f32"), ((8192, 8192, 600), "f16"), ((8192, 8192, 600), "f32")],
+                         ids=lambda v: v if isinstance(v, str) else "%dx%dx%d" % v)
+def test_products_of_few_rows_with_many_and_of_several_tiles_a_workgroup(ctx, mnk, kind):
+    _product(ctx, *mnk, kind=kind, accumulate=kind == "f32")
+
+
+def test_products_of_very_long_sums_in_parts(ctx):
+    """Against a product in 64 bits of the values that psgd_mx_dequantize gives."""
+    import torch
+    from rank_gradient_compression_powersgd_amd import MxTensor, psgd_mx_dequantize, psgd_mx_product, psgd_mx_quantize
+    from rank_gradient_compression_powersgd_amd import binding
+    m, n, k = 2000, 2040, 131067
+    assert binding.psgd_mx_product_workspace(m, n, k) >= 2 * 4 * m * n
+    want, sums = (torch.zeros(m, n, dtype=torch.float64, device="cuda") for _ in range(2))
+    values = []
+    for rows in (m, n):
+        x, mx = torch.randn(rows, k, device="cuda"), MxTensor(rows, k)
+        psgd_mx_quantize(ctx, x, mx)
+        psgd_mx_dequantize(ctx, mx, x)
+        values.append((mx, x))
+    (a, av), (b, bv) = values
+    for i in range(0, k, 16384):
+        p, q = av[:, i:i + 16384].double(), bv[:, i:i + 16384].double().t().contiguous()
+        want += p @ q
+        sums += p.abs() @ q.abs()
+    c = torch.full((m, n), 3.0, device="cuda")
+    psgd_mx_product(ctx, a, b, c)
+    tol = ((-(-k // 128) + 8) * 2.0 ** -23) * sums + 2.0 ** -24 * want.abs()
+    assert ((c.double() - want).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("m", [5, 200])
 def test_empty_products(ctx, m):
     import torch
