@@ -559,7 +559,7 @@ psgd_status psgd_adamw_moments(psgd_ctx* ctx, const uint8_t* m1, const uint8_t* 
  *   the device, NULL: 1. Sums run in a fixed order, which the sizes determine.
  *   workspace: psgd_mx_product_workspace(m, n, k) bytes of device memory (0 for most sizes, workspace may
  *   then be NULL), 16-byte aligned, contents ignored and overwritten; calls that may overlap need one each.
- * Pointers to elements need their type's alignment. Outputs must not overlap inputs. All buffers live on
+ * Pointers to elements need their type's alignment. Outputs must not overlap inputs, nor one another. All buffers live on
  * the ctx's device. Asynchronous on stream, no allocation.
  */
 typedef struct psgd_mx_tensor {

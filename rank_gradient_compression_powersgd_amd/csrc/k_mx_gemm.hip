@@ -506,25 +506,27 @@ void k_mx_gemm(MxProduct a, int items) {
   } while (stage(f0, f1) && stage(f1, f0));
 }
 
-// The parts of a split product, added in order.
+// The parts of a split product, added in order; of none, zeros.
 template <int OT>
 __global__ __launch_bounds__(256)
 void k_mx_join(MxProduct a) {
-  const int64_t blocks = (a.n + 1023) / 1024, j = blockIdx.x / blocks;
-  const int64_t i = 4 * ((blockIdx.x - j * blocks) * 256 + threadIdx.x);
-  if (i >= a.n) return;
-  const GLOBAL float* p = gbl(a.partial) + j * a.n + i;
-  const int64_t step = a.m * a.n;
+  const int64_t blocks = (a.n + 1023) / 1024, step = a.m * a.n;
   const int parts = a.p.panels > 0 ? a.splits : 0;
-  f32x4 sum{0, 0, 0, 0};
-  if (i + 4 <= a.n) {
-    for (int s = 0; s < parts; ++s) sum += *gcast<f32x4_u>(p + s * step);
-  } else {
-    for (int s = 0; s < parts; ++s)
-      for (int t = 0; t < 4; ++t)
-        if (i + t < a.n) sum[t] += p[s * step + t];
+  const float scale = a.scale ? *a.scale : 1.0f;
+  for (int64_t block = blockIdx.x; block < blocks * a.m; block += gridDim.x) {
+    const int64_t j = block / blocks, i = 4 * ((block - j * blocks) * 256 + threadIdx.x);
+    if (i >= a.n) continue;
+    const GLOBAL float* p = gbl(a.partial) + j * a.n + i;
+    f32x4 sum{0, 0, 0, 0};
+    if (i + 4 <= a.n) {
+      for (int s = 0; s < parts; ++s) sum += *gcast<f32x4_u>(p + s * step);
+    } else {
+      for (int s = 0; s < parts; ++s)
+        for (int t = 0; t < 4; ++t)
+          if (i + t < a.n) sum[t] += p[s * step + t];
+    }
+    finish<OT>(a, j, i, sum, scale);
   }
-  finish<OT>(a, j, i, sum, a.scale ? *a.scale : 1.0f);
 }
 
 template <int T, int OT>
@@ -538,7 +540,8 @@ hipError_t go_tiles(const MxProduct& a, hipStream_t s) {
 }
 template <int OT>
 hipError_t go_join(const MxProduct& a, hipStream_t s) {
-  k_mx_join<OT><<<dim3((unsigned)((a.n + 1023) / 1024 * a.m)), dim3(256), 0, s>>>(a);
+  const int64_t blocks = (a.n + 1023) / 1024 * a.m;
+  k_mx_join<OT><<<dim3((unsigned)std::min<int64_t>(blocks, 1 << 20)), dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }
 template <int OT>

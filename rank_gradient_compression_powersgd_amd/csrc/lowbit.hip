@@ -59,6 +59,14 @@ bool any_overlap(std::vector<Range>& written, const std::vector<Range>& read) {
   return false;
 }
 
+struct Bytes { const void* data; int64_t size; };
+Bytes strided(const void* p, int64_t rows, int64_t cols, int64_t ld, int size) { return {p, ((rows - 1) * ld + cols) * size}; }
+Bytes bytes_of(const psgd_mx_tensor* t) { return t ? Bytes{t->data, psgd::mx_bytes(t->rows, t->k)} : Bytes{nullptr, 0}; }
+bool meet(Bytes a, Bytes b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.data), y = reinterpret_cast<uintptr_t>(b.data);
+  return a.data && b.data && x < y + b.size && y < x + a.size;
+}
+
 }  // namespace
 
 extern "C" {
@@ -217,6 +225,8 @@ psgd_status psgd_mx_quantize(psgd_ctx* ctx, const void* x, int64_t ld_x, int64_t
   if (!x || !aligned_to(x, type_size(it))) return fail(ctx, PSGD_EINVAL, "x must be a pointer aligned to its element type");
   if ((n + psgd::kMxPanel - 1) / psgd::kMxPanel * ((m + psgd::kMxGroup - 1) / psgd::kMxGroup) >= kMaxBlocks)
     return fail(ctx, PSGD_EUNSUPPORTED, "%lld x %lld is past what one launch takes", (long long)m, (long long)n);
+  const Bytes in = strided(x, m, n, ld_x, type_size(it)), r = bytes_of(row), c = bytes_of(col);
+  if (meet(in, r) || meet(in, c) || meet(r, c)) return fail(ctx, PSGD_EINVAL, "x, row and col must not overlap");
   DeviceGuard dev(ctx->device);
   HIPCHK(ctx, dev.err, "hipSetDevice");
   psgd::MxQuantize a{};
@@ -241,6 +251,8 @@ psgd_status psgd_mx_dequantize(psgd_ctx* ctx, const psgd_mx_tensor* t, void* out
   const psgd::MxView v = psgd::mx_view(t->data, t->rows, t->k);
   if (v.panels * v.groups >= kMaxBlocks)
     return fail(ctx, PSGD_EUNSUPPORTED, "%lld x %lld is past what one launch takes", (long long)t->rows, (long long)t->k);
+  if (meet(strided(out, t->rows, t->k, ld_out, type_size(ot)), bytes_of(t)))
+    return fail(ctx, PSGD_EINVAL, "out must not overlap the matrix");
   DeviceGuard dev(ctx->device);
   HIPCHK(ctx, dev.err, "hipSetDevice");
   HIPCHK(ctx, psgd::launch_mx_dequantize(v, out, ld_out, ot, stream), "4-bit values");
@@ -276,6 +288,10 @@ psgd_status psgd_mx_product(psgd_ctx* ctx, const psgd_mx_tensor* a, const psgd_m
   if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need))
     return fail(ctx, PSGD_EINVAL, "the workspace needs %lld bytes at a 16-byte aligned address, got %lld", (long long)need,
                 (long long)workspace_bytes);
+  const Bytes out = strided(c, m, n, ld_c, type_size(ot)), ws{workspace, need}, s{scale, 4};
+  for (const Bytes& in : {bytes_of(a), bytes_of(b), s})
+    if (meet(out, in) || meet(ws, in)) return fail(ctx, PSGD_EINVAL, "c and the workspace must not overlap a, b or scale");
+  if (meet(out, ws)) return fail(ctx, PSGD_EINVAL, "c must not overlap the workspace");
   p.m = m; p.n = n;
   p.c = c; p.ldc = ld_c;
   p.scale = scale; p.accumulate = accumulate != 0;

@@ -90,9 +90,9 @@ class AdamWGroup:
         import torch
         if self.bits == 32:
             return self.m1, self.m2
-        kind, n = dtype or torch.bfloat16, self.m1.numel()
-        out1, out2 = torch.empty(n, dtype=kind, device=self.device), torch.empty(n, dtype=kind, device=self.device)
-        call = "psgd_adamw_moments"
+        call, n = "psgd_adamw_moments", self.m1.numel()
+        kind = dtype or torch.bfloat16
+        out1, out2 = (B._workspace(n * kind.itemsize, self.device, stream).view(kind) for _ in range(2))
         B._check(self.ctx, call, B.load_library().psgd_adamw_moments(
             self.ctx, self.m1.data_ptr(), self.e1.data_ptr(), self.m2.data_ptr(), self.e2.data_ptr(), n, out1.data_ptr(), out2.data_ptr(),
             B._dtype(out1, call), B._stream(stream, self.device.index)))
@@ -137,7 +137,8 @@ class MxLinear:
             which follows every step on the weight
     seed: of the stochastic rounding of the output's gradient; another one for every layer
 
-    Runs on the current stream of the weight's device.
+    Runs on the current stream of the weight's device. Holds one forward() for backward(): where a layer runs
+    several times before, each but the last has to be run again before its backward().
     """
 
     def __init__(self, weight, seed: int = 0):
@@ -174,12 +175,13 @@ class MxLinear:
         B.psgd_mx_quantize(self.ctx, x2, row, col)
         B.psgd_mx_product(self.ctx, row, self.w_col, y.view(t, self.n_out))
         if train:
-            self.x_col = col
+            self.x_col, self.x_stream = col, B._stream(None, self.device.index)
         return y
 
     def backward(self, dy, err=None, scale=None, step=None):
         """dx = dy W^T, in dy's dtype, and err += scale x^T dy (err: in x out fp32, the error buffer of an
-        in-place matrix of a PowerSGDGroup; scale: its one-element fp32 multiplier, or None). dy is rounded
+        in-place matrix of a PowerSGDGroup; scale: its one-element fp32 multiplier, or None), which uses up
+        the forward() before it: a second such call is refused. dy is rounded
         stochastically by seed and step (one-element int32 device tensor, which the caller advances, or None)."""
         import torch
         dy2 = self._tokens(dy, self.n_out, "dy")
@@ -192,7 +194,10 @@ class MxLinear:
         B.psgd_mx_quantize(self.ctx, dy2, row, col, stochastic=True, seed=self.seed, step=step)
         B.psgd_mx_product(self.ctx, row, self.w_row, dx.view(t, self.n_in))
         if err is not None:
+            if self.x_stream != B._stream(None, self.device.index):         # its memory is not handed out before this product is done
+                self.x_col.data.record_stream(torch.cuda.current_stream(self.device))
             B.psgd_mx_product(self.ctx, self.x_col, col, err, scale=scale, accumulate=True)
+            self.x_col = None
         return dx
 
     def close(self):

@@ -304,6 +304,24 @@ def test_two_groups_on_two_streams():
         assert torch.equal(c.p_all, alone.p_all) and all(torch.equal(a, b) for a, b in zip(c.group.state(), alone.group.state()))
 
 
+def test_moments_of_a_stream_of_their_own():
+    import torch
+    from rank_gradient_compression_powersgd_amd import AdamWGroup
+    p, g = torch.randn(70000, device="cuda"), torch.randn(70000, device="cuda")
+    group = AdamWGroup([p], [g], bits=8)
+    group.step(_hp())
+    want = group.moments()
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    for kind in (torch.bfloat16, torch.float32):
+        got = group.moments(dtype=kind, stream=stream)
+        stream.synchronize()
+        assert all(a.dtype == kind and torch.equal(a.float(), b.float()) for a, b in zip(got, want))
+    got = group.moments(stream=stream.cuda_stream)
+    stream.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_neighbours_of_a_list_are_left_alone():
     import torch
     from rank_gradient_compression_powersgd_amd import AdamWGroup

@@ -596,3 +596,69 @@ def test_refusals(ctx):
     assert lib.psgd_mx_quantize(ctx, x.data_ptr(), 20, 10, 20, 9, B._mx(row), None, 0, 0, None, None) == B.PSGD_EDTYPE
     assert lib.psgd_mx_product(ctx, B._mx(row), B._mx(b), None, c.data_ptr(), 29, 3, 0, None, 0, None) == B.PSGD_EINVAL
     assert lib.psgd_mx_product(ctx, B._mx(row), None, None, c.data_ptr(), 30, 3, 0, None, 0, None) == B.PSGD_EINVAL
+
+
+def test_overlapping_buffers_are_refused(ctx):
+    import torch
+    from rank_gradient_compression_powersgd_amd import MxTensor, binding as B
+    flat = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+
+    def at(rows, k, offset):
+        return MxTensor(rows, k, data=flat[offset:offset + B.psgd_mx_bytes(rows, k)])
+
+    def refused(fn):
+        with pytest.raises(B.PsgdError) as ei:
+            fn()
+        assert ei.value.status == B.PSGD_EINVAL and "overlap" in str(ei.value)
+
+    m, n, k = 100, 200, 300
+    size = B.psgd_mx_bytes(m, k)
+    x = flat[4096:4096 + 4 * m * k].view(torch.float32).view(m, k)
+    end = 4096 + 4 * m * k
+    refused(lambda: B.psgd_mx_quantize(ctx, x, at(m, k, 4080)))
+    refused(lambda: B.psgd_mx_quantize(ctx, x, None, at(k, m, end - 16)))
+    refused(lambda: B.psgd_mx_quantize(ctx, x, at(m, k, end), at(k, m, end + size - 16)))
+    refused(lambda: B.psgd_mx_dequantize(ctx, at(m, k, 4080), x))
+    B.psgd_mx_quantize(ctx, x, at(m, k, end), at(k, m, end + (size + 15) // 16 * 16))      # neighbours
+    B.psgd_mx_dequantize(ctx, at(m, k, end), x)
+    a, b = at(m, k, 0), at(n, k, 1 << 19)
+    c = flat[(1 << 19) - 4 * m * n:1 << 19].view(torch.float32).view(m, n)
+    B.psgd_mx_product(ctx, a, b, c)
+    refused(lambda: B.psgd_mx_product(ctx, a, b, flat[(1 << 19) - 4 * m * n + 4:(1 << 19) + 4].view(torch.float32).view(m, n)))
+    refused(lambda: B.psgd_mx_product(ctx, a, b, flat[size - 16:size - 16 + 4 * m * n].view(torch.float32).view(m, n)))
+    refused(lambda: B.psgd_mx_product(ctx, a, b, c, scale=c[5, 7:8]))
+    B.psgd_mx_product(ctx, a, a, torch.empty(m, m, device="cuda"))                         # an operand may be both
+    p, q = MxTensor(130, 20000), MxTensor(130, 20000)
+    need = B.psgd_mx_product_workspace(130, 130, 20000)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    refused(lambda: B.psgd_mx_product(ctx, p, q, ws[:4 * 130 * 130].view(torch.float32).view(130, 130), workspace=ws))
+    refused(lambda: B.psgd_mx_product(ctx, p, q, torch.empty(130, 130, device="cuda"), workspace=p.data))
+
+
+def test_no_columns_to_sum_over_and_more_rows_than_a_launch_has_workgroups(ctx):
+    import torch
+    from rank_gradient_compression_powersgd_amd import MxTensor, psgd_mx_product
+    m = 2 ** 24 + 70
+    c = torch.full((m, 3), 7.0, device="cuda", dtype=torch.float16)
+    psgd_mx_product(ctx, MxTensor(m, 0), MxTensor(3, 0), c)
+    assert not c.any()
+
+
+def test_backward_uses_up_its_forward_and_may_run_on_another_stream():
+    import torch
+    from rank_gradient_compression_powersgd_amd import MxLinear, binding as B
+    layer = MxLinear(torch.randn(264, 130, device="cuda").bfloat16())
+    x, dy = torch.randn(200, 264, device="cuda").bfloat16(), torch.randn(200, 130, device="cuda").bfloat16()
+    want, err = torch.zeros(264, 130, device="cuda"), torch.zeros(264, 130, device="cuda")
+    layer.forward(x)
+    layer.backward(dy)                                       # the gradient of x alone leaves it
+    layer.backward(dy, want)
+    with pytest.raises(B.PsgdError):
+        layer.backward(dy, err)
+    other = torch.cuda.Stream()
+    layer.forward(x)
+    other.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(other):
+        layer.backward(dy, err)
+    torch.cuda.synchronize()
+    assert torch.equal(err, want)
