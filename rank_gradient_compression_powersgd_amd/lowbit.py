@@ -75,6 +75,9 @@ class AdamWGroup:
         if skip is not None:
             B._same_device("psgd_adamw_prepare", self.skip, skip, ctx=self.ctx)
         h = B._hparams(hp)
+        inf = float("inf")
+        if not (0 <= h.beta1 < 1 and 0 <= h.beta2 < 1 and 0 <= h.lr < inf and 0 <= h.eps < inf and 0 <= h.weight_decay < inf):
+            raise B.PsgdError("psgd_adamw_update", B.PSGD_EINVAL, "betas must lie in [0, 1), lr, eps and weight_decay be finite and >= 0")
         lib, st, ctx, plan = B.load_library(), B._stream(stream, self.device.index), self.ctx, self.plan
         words = self.skip.data_ptr(), self.step_count.data_ptr(), self.norm.data_ptr()
         B._check(ctx, "psgd_adamw_prepare", lib.psgd_adamw_prepare(ctx, plan, max_norm, B._ptr(skip), *words, st))

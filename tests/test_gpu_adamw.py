@@ -354,6 +354,17 @@ def test_elements_past_32_bits():
     assert (p[-tail:] != 0.5).float().mean() > 0.3
 
 
+def test_a_refused_step_counts_nothing():
+    import torch
+    from rank_gradient_compression_powersgd_amd import AdamWGroup, binding as B
+    f = torch.ones(100, device="cuda")
+    group = AdamWGroup([f], [f.clone()])
+    for bad in ((-1.0, 0.9, 0.999, 1e-8, 0.0), (1e-3, 1.0, 0.999, 1e-8, 0.0), (1e-3, 0.9, float("nan"), 1e-8, 0.0), (1e-3, 0.9, 0.999, float("inf"), 0.0)):
+        with pytest.raises(B.PsgdError):
+            group.step(_hp(bad))
+    assert int(group.step_count) == 0 and (f == 1).all()
+
+
 def test_refusals():
     import torch
     from rank_gradient_compression_powersgd_amd import AdamWGroup, binding as B
