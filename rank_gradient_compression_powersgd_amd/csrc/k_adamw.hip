@@ -14,6 +14,12 @@
 // off, its expectation moves as in fp32. The same holds for 16-bit parameters and small lr. Random bits
 // are a hash of seed, step, tensor and element (hash.h).
 //
+// Bound: memory. A chunk's loads are all sent for before its first use, so a workgroup (4096 elements, 256
+// threads) keeps 57 KB under way. 188.9 million elements (fp32 parameters, bf16 gradients, 8-bit moments, 14.06
+// bytes each): 470 us, 5.6 TB/s; their norm 73 to 104 us, their moments' values 256 (4.4 TB/s, mostly
+// writes). 23.6 million (bf16, fp32 gradients, 12.06 bytes): 55, 15 and 27 us. 0.33 million: 7, 3 and 3 us, what
+// four dependent launches of this kind take at least.
+//
 // The moments' arithmetic is rounded operation by operation (no fused multiply-add), so that codes do
 // not depend on how the compiler contracts an expression.
 #include "adamw.h"

@@ -8,6 +8,11 @@
 //
 // Both directions in one pass. A lane holds 2 columns x 32 rows: a column's block is the lane's own, a
 // row's block spans 16 lanes, whose maximum is four DPP steps. No LDS; the input is read once.
+//
+// Bound: to nearest, memory (20480 x 3968 bf16, both directions, 249 MB: 40 us, 6.3 TB/s, 81 MB of it still in
+// the last cache; rows alone 29 us). By random bits the vector instructions come close to it: a conversion of
+// 14 cycles per element and direction and a hash per two elements, 25 of 55 us (4.5 TB/s); 66 to 72 us where
+// nothing is in a cache. Loads of the next block ahead of this one's work cost waves and gained nothing (55 -> 62 us).
 #include <type_traits>
 #include <utility>
 
@@ -174,6 +179,8 @@ template <> struct Pair<G_F32> {
   __device__ __forceinline__ static Pair second(Pair a, Pair b) { return Pair{a.w, b.w}; }
 };
 // ---- rows only: 16 lanes a row and panel, 8 elements a lane; a workgroup takes 64 rows of a panel -----
+// 16-byte loads, where the kernel below takes 4 bytes a lane to have columns in it (20480 x 1984 bf16: 16 us,
+// columns alone 20).
 template <int IT, bool SR>
 __global__ __launch_bounds__(kThreads)
 void k_mx_rows(MxQuantize a) {
@@ -324,6 +331,7 @@ void k_mx_cols(MxQuantize a) {
 }
 
 // ---- back to values: 16 lanes a row and panel, 8 elements a lane ----------------------------------------
+// Bound: memory (20480 x 3968 to bf16, 206 MB: 31 to 42 us, 6.6 to 4.9 TB/s).
 template <int OT>
 __global__ __launch_bounds__(kThreads)
 void k_mx_dequantize(MxView a, void* out, int64_t ld) {
