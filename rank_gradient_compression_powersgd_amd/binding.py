@@ -572,7 +572,10 @@ def _embed_rows(t, n: int, dim: int, name: str, call: str) -> int:
 def _same_device(call: str, *tensors, ctx: int = 0):
     """All on one GPU, and on the context's: its device is the one that the kernels are launched on."""
     device = tensors[0].device
-    if device.type != "cuda" or any(t.device != device for t in tensors):
+    same = device.type == "cuda"
+    for t in tensors[1:]:
+        same = same and t.device == device
+    if not same:
         raise PsgdError(call, PSGD_EINVAL, "tensors must live on one GPU")
     if _ctx_device.get(ctx, device.index) != device.index:
         raise PsgdError(call, PSGD_EINVAL, f"tensors live on {device}, the context on device {_ctx_device[ctx]}")
@@ -723,14 +726,21 @@ def _mx(t):
 def psgd_mx_quantize(ctx: int, x, row=None, col=None, stochastic: bool = False, seed: int = 0, step=None, stream=None) -> None:
     """x (2-D, unit row stride, fp16, bf16 or fp32) to the MxTensor row (x's shape) and, transposed, to col.
     step: one-element int32 device tensor mixed into the random bits, or None."""
-    import torch
     call = "psgd_mx_quantize"
     if x.dim() != 2:
         raise PsgdError(call, PSGD_EINVAL, "x must be a 2-D tensor")
-    if step is not None and step.dtype != torch.int32:
-        raise PsgdError(call, PSGD_EDTYPE, "step must be int32")
+    on = [x]
+    if row is not None:
+        on.append(row.data)
+    if col is not None:
+        on.append(col.data)
+    if step is not None:
+        import torch
+        if step.dtype != torch.int32:
+            raise PsgdError(call, PSGD_EDTYPE, "step must be int32")
+        on.append(step)
     m, n = x.shape
-    _same_device(call, x, *(t for t in (row and row.data, col and col.data, step) if t is not None), ctx=ctx)
+    _same_device(call, *on, ctx=ctx)
     _check(ctx, call, load_library().psgd_mx_quantize(
         ctx, _ptr(x), _row_stride(x, call), m, n, _dtype(x, call), _mx(row), _mx(col), _rounding(stochastic),
         seed & 0xFFFFFFFFFFFFFFFF, _ptr(step), _stream(stream, x.device.index)))
@@ -746,6 +756,7 @@ def psgd_mx_dequantize(ctx: int, a, out, stream=None) -> None:
                                                         _stream(stream, out.device.index)))
 
 
+@functools.lru_cache(maxsize=4096)
 def psgd_mx_product_workspace(m: int, n: int, k: int) -> int:
     """Bytes of device workspace of psgd_mx_product (0 for most sizes)."""
     out = ctypes.c_int64()
@@ -757,13 +768,18 @@ def psgd_mx_product(ctx: int, a, b, out, scale=None, accumulate: bool = False, w
     """out (a.rows x b.rows) = scale * A B^T of two MxTensors of one k, or added to an fp32 out. scale: one-element
     fp32 device tensor or None; workspace: a contiguous device tensor of at least psgd_mx_product_workspace(...)
     bytes, allocated for the call on its stream when None."""
-    import torch
     call = "psgd_mx_product"
     if tuple(out.shape) != (a.rows, b.rows):
         raise PsgdError(call, PSGD_EINVAL, f"out must be {a.rows} x {b.rows}")
-    if scale is not None and (scale.dtype != torch.float32 or scale.numel() < 1):
-        raise PsgdError(call, PSGD_EDTYPE, "scale must be one float32")
-    _same_device(call, out, a.data, b.data, *[t for t in (scale, workspace) if t is not None], ctx=ctx)
+    on = [out, a.data, b.data]
+    if scale is not None:
+        import torch
+        if scale.dtype != torch.float32 or scale.numel() < 1:
+            raise PsgdError(call, PSGD_EDTYPE, "scale must be one float32")
+        on.append(scale)
+    if workspace is not None:
+        on.append(workspace)
+    _same_device(call, *on, ctx=ctx)
     ld, dt = _row_stride(out, call), _dtype(out, call)
     if workspace is None:
         need = psgd_mx_product_workspace(a.rows, b.rows, a.k)
