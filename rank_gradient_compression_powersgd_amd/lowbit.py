@@ -167,19 +167,36 @@ class MxLinear:
             raise B.PsgdError("psgd_mx_quantize", B.PSGD_EINVAL, f"{name} must hold one row of {width} values per token")
         return t if t.dim() == 2 else t.reshape(-1, width)
 
+    # The calls of psgd_mx_quantize and psgd_mx_product, their tensors' device and shapes checked before.
+    def _quantize(self, x, row, col, rounding, step, stream):
+        call = "psgd_mx_quantize"
+        m, n = x.shape
+        B._check(self.ctx, call, B.load_library().psgd_mx_quantize(
+            self.ctx, x.data_ptr(), B._row_stride(x, call), m, n, B._dtype(x, call), B._mx(row), B._mx(col), rounding,
+            self.seed & 0xFFFFFFFFFFFFFFFF, B._ptr(step), stream))
+
+    def _product(self, a, b, out, scale, accumulate, stream):
+        call = "psgd_mx_product"
+        need = B.psgd_mx_product_workspace(a.rows, b.rows, a.k)
+        room = B._workspace(need, self.device, None) if need else None
+        B._check(self.ctx, call, B.load_library().psgd_mx_product(
+            self.ctx, B._mx(a), B._mx(b), B._ptr(scale), out.data_ptr(), B._row_stride(out, call), B._dtype(out, call), accumulate,
+            B._ptr(room), need, stream))
+
     def forward(self, x, train: bool = True):
         """y = x W, in x's dtype; x [..., in] to nearest. With train, x's 4-bit transpose is kept for backward()."""
         import torch
         x2 = self._tokens(x, self.n_in, "x")
-        t = x2.shape[0]
+        B._same_device("psgd_mx_quantize", self.w_col.data, x2)
+        t, stream = x2.shape[0], B._stream(None, self.device.index)
         row = MxTensor(t, self.n_in, self.device)
         col = MxTensor(self.n_in, t, self.device) if train else None
-        y = torch.empty(*x.shape[:-1], self.n_out, dtype=x.dtype, device=self.device)
-        B.psgd_mx_quantize(self.ctx, x2, row, col)
-        B.psgd_mx_product(self.ctx, row, self.w_col, y.view(t, self.n_out))
+        y = torch.empty(t, self.n_out, dtype=x.dtype, device=self.device)
+        self._quantize(x2, row, col, B.PSGD_NEAREST, None, stream)
+        self._product(row, self.w_col, y, None, 0, stream)
         if train:
-            self.x_col, self.x_stream = col, B._stream(None, self.device.index)
-        return y
+            self.x_col, self.x_stream = col, stream
+        return y if x.dim() == 2 else y.view(*x.shape[:-1], self.n_out)
 
     def backward(self, dy, err=None, scale=None, step=None):
         """dx = dy W^T, in dy's dtype, and err += scale x^T dy (err: in x out fp32, the error buffer of an
@@ -188,20 +205,30 @@ class MxLinear:
         stochastically by seed and step (one-element int32 device tensor, which the caller advances, or None)."""
         import torch
         dy2 = self._tokens(dy, self.n_out, "dy")
-        t = dy2.shape[0]
-        if err is not None and (self.x_col is None or self.x_col.k != t):
-            raise B.PsgdError("psgd_mx_product", B.PSGD_EINVAL, "backward() needs the forward() of the same tokens before it")
+        t, stream = dy2.shape[0], B._stream(None, self.device.index)
+        B._same_device("psgd_mx_product", self.w_row.data, *[v for v in (dy2, err, scale, step) if v is not None])
+        if step is not None and step.dtype != torch.int32:
+            raise B.PsgdError("psgd_mx_quantize", B.PSGD_EDTYPE, "step must be int32")
+        if err is not None:
+            if self.x_col is None or self.x_col.k != t:
+                raise B.PsgdError("psgd_mx_product", B.PSGD_EINVAL, "backward() needs the forward() of the same tokens before it")
+            if err.shape != self.weight.shape:
+                raise B.PsgdError("psgd_mx_product", B.PSGD_EINVAL, f"err must be {self.n_in} x {self.n_out}")
+            if err.dtype != torch.float32:
+                raise B.PsgdError("psgd_mx_product", B.PSGD_EDTYPE, "products are added to fp32 only")
+            if scale is not None and (scale.dtype != torch.float32 or scale.numel() < 1):
+                raise B.PsgdError("psgd_mx_product", B.PSGD_EDTYPE, "scale must be one float32")
         row = MxTensor(t, self.n_out, self.device)
         col = MxTensor(self.n_out, t, self.device) if err is not None else None
-        dx = torch.empty(*dy.shape[:-1], self.n_in, dtype=dy.dtype, device=self.device)
-        B.psgd_mx_quantize(self.ctx, dy2, row, col, stochastic=True, seed=self.seed, step=step)
-        B.psgd_mx_product(self.ctx, row, self.w_row, dx.view(t, self.n_in))
+        dx = torch.empty(t, self.n_in, dtype=dy.dtype, device=self.device)
+        self._quantize(dy2, row, col, B.PSGD_STOCHASTIC, step, stream)
+        self._product(row, self.w_row, dx, None, 0, stream)
         if err is not None:
-            if self.x_stream != B._stream(None, self.device.index):         # its memory is not handed out before this product is done
+            if self.x_stream != stream:                      # its memory is not handed out before this product is done
                 self.x_col.data.record_stream(torch.cuda.current_stream(self.device))
-            B.psgd_mx_product(self.ctx, self.x_col, col, err, scale=scale, accumulate=True)
+            self._product(self.x_col, col, err, scale, 1, stream)
             self.x_col = None
-        return dx
+        return dx if dy.dim() == 2 else dx.view(*dy.shape[:-1], self.n_in)
 
     def close(self):
         if getattr(self, "ctx", None):

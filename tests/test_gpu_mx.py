@@ -662,3 +662,31 @@ def test_backward_uses_up_its_forward_and_may_run_on_another_stream():
         layer.backward(dy, err)
     torch.cuda.synchronize()
     assert torch.equal(err, want)
+
+
+def test_refusals_of_a_layer():
+    import torch
+    from rank_gradient_compression_powersgd_amd import MxLinear, binding as B
+
+    def refused(status, fn):
+        with pytest.raises(B.PsgdError) as ei:
+            fn()
+        assert ei.value.status == status, str(ei.value)
+
+    layer = MxLinear(torch.randn(40, 24, device="cuda"))
+    x, dy, err = torch.randn(5, 40, device="cuda"), torch.randn(5, 24, device="cuda"), torch.zeros(40, 24, device="cuda")
+    refused(B.PSGD_EINVAL, lambda: layer.forward(x.cpu()))
+    refused(B.PSGD_EDTYPE, lambda: layer.forward(x.double()))
+    refused(B.PSGD_EINVAL, lambda: layer.forward(torch.randn(40, 5, device="cuda").t()))
+    refused(B.PSGD_EINVAL, lambda: layer.forward(x[0]))
+    layer.forward(x)
+    refused(B.PSGD_EINVAL, lambda: layer.backward(dy.cpu(), err))
+    refused(B.PSGD_EINVAL, lambda: layer.backward(dy, err.cpu()))
+    refused(B.PSGD_EINVAL, lambda: layer.backward(dy, err.t()))
+    refused(B.PSGD_EDTYPE, lambda: layer.backward(dy, err.half()))
+    refused(B.PSGD_EDTYPE, lambda: layer.backward(dy, err, torch.ones(1, device="cuda", dtype=torch.float64)))
+    refused(B.PSGD_EDTYPE, lambda: layer.backward(dy, err, step=torch.ones(1, device="cuda", dtype=torch.int64)))
+    refused(B.PSGD_EDTYPE, lambda: layer.backward(dy.double(), err))
+    assert not err.any()
+    layer.backward(dy, err)                                  # no refusal used up the forward
+    assert err.any()
