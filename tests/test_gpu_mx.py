@@ -690,3 +690,36 @@ def test_refusals_of_a_layer():
     assert not err.any()
     layer.backward(dy, err)                                  # no refusal used up the forward
     assert err.any()
+
+
+def test_a_captured_layer_replays_as_the_eager_one():
+    import torch
+    from rank_gradient_compression_powersgd_amd import MxLinear
+    w = torch.randn(333, 200, device="cuda").bfloat16()
+    x, dy = torch.zeros(150, 333, device="cuda").bfloat16(), torch.zeros(150, 200, device="cuda").bfloat16()
+    step, scale = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.tensor([0.5], device="cuda")
+    err, want = torch.zeros(333, 200, device="cuda"), torch.zeros(333, 200, device="cuda")
+    captured, eager = MxLinear(w, seed=9), MxLinear(w, seed=9)
+
+    def both(layer, e):
+        layer.refresh()
+        return layer.forward(x), layer.backward(dy, e, scale, step=step)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both(captured, err)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, dx = both(captured, err)
+    err.zero_()
+    for t in range(1, 5):
+        x.copy_(torch.randn(150, 333, device="cuda"))
+        dy.copy_(torch.randn(150, 200, device="cuda"))
+        w.copy_(torch.randn(333, 200, device="cuda"))
+        step.fill_(t)
+        y2, dx2 = both(eager, want)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(dx, dx2) and torch.equal(err, want) and want.any(), t
