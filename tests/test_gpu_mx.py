@@ -281,6 +281,25 @@ def test_products_of_very_long_sums_in_parts(ctx):
     assert ((c.double() - want).abs() <= tol).all()
 
 
+def test_products_of_very_long_sums_in_parts_of_middle_tiles(ctx):
+    """Exactly: on values of one magnitude fp32 sums below 2^24 of them round nothing."""
+    import torch
+    from rank_gradient_compression_powersgd_amd import MxTensor, psgd_mx_product, psgd_mx_quantize
+    from rank_gradient_compression_powersgd_amd import binding
+    m, n, k = 1000, 1020, 200059
+    assert binding.psgd_mx_product_workspace(m, n, k) == 4 * 4 * m * n
+    x, w = (torch.randint(-1, 2, (r, k), device="cuda").to(torch.bfloat16) for r in (m, n))
+    a, b = MxTensor(m, k), MxTensor(n, k)
+    psgd_mx_quantize(ctx, x, a)
+    psgd_mx_quantize(ctx, w, b)
+    c = torch.full((m, n), 3.0, device="cuda")
+    psgd_mx_product(ctx, a, b, c)
+    want = torch.zeros(m, n, dtype=torch.float64, device="cuda")
+    for i in range(0, k, 16384):
+        want += x[:, i:i + 16384].double() @ w[:, i:i + 16384].double().t().contiguous()
+    assert torch.equal(c.double(), want)
+
+
 @pytest.mark.parametrize("m", [5, 200])
 def test_empty_products(ctx, m):
     import torch
