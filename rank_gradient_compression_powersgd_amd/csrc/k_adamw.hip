@@ -16,9 +16,9 @@
 //
 // Bound: memory. A chunk's loads are all sent for before its first use, so a workgroup (4096 elements, 256
 // threads) keeps 57 KB under way. 188.9 million elements (fp32 parameters, bf16 gradients, 8-bit moments, 14.06
-// bytes each): 470 us, 5.6 TB/s; their norm 73 to 104 us, their moments' values 256 (4.4 TB/s, mostly
-// writes). 23.6 million (bf16, fp32 gradients, 12.06 bytes): 55, 15 and 27 us. 0.33 million: 7, 3 and 3 us, what
-// four dependent launches of this kind take at least.
+// bytes each): 470 us, 5.6 TB/s; their norm 71 to 104 us, their moments' values 200 (5.7 TB/s). 23.6 million
+// (bf16, fp32 gradients, 12.06 bytes): 55, 15 and 23 us. 0.76 million: 7, 3 and 3 us, what dependent launches of
+// this kind take at least.
 //
 // The moments' arithmetic is rounded operation by operation (no fused multiply-add), so that codes do
 // not depend on how the compiler contracts an expression.
@@ -39,10 +39,14 @@ typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
 typedef _Float16 f16x4_u __attribute__((ext_vector_type(4), aligned(2)));
 typedef __bf16 bf16x4_u __attribute__((ext_vector_type(4), aligned(2)));
 
+typedef _Float16 f16x8_u __attribute__((ext_vector_type(8), aligned(2)));
+typedef __bf16 bf16x8_u __attribute__((ext_vector_type(8), aligned(2)));
+
+// wide: what 16 bytes hold
 template <int T> struct Elem;
-template <> struct Elem<G_F32> { typedef float one; typedef f32x4_u four; };
-template <> struct Elem<G_F16> { typedef _Float16 one; typedef f16x4_u four; };
-template <> struct Elem<G_BF16> { typedef __bf16 one; typedef bf16x4_u four; };
+template <> struct Elem<G_F32> { typedef float one; typedef f32x4_u four; typedef f32x4_u wide; static constexpr int WIDE = 4; };
+template <> struct Elem<G_F16> { typedef _Float16 one; typedef f16x4_u four; typedef f16x8_u wide; static constexpr int WIDE = 8; };
+template <> struct Elem<G_BF16> { typedef __bf16 one; typedef bf16x4_u four; typedef bf16x8_u wide; static constexpr int WIDE = 8; };
 
 template <int T> __device__ __forceinline__ f32x4 load_four(const void* p, int i) {
   const auto v = *gcast<typename Elem<T>::four>(gbl(static_cast<const typename Elem<T>::one*>(p)) + i);
@@ -147,28 +151,40 @@ __device__ __forceinline__ void finish_norm(const AdamwNorm& a, double total) {
 template <int GT>
 __global__ __launch_bounds__(kThreads)
 void k_adamw_sqnorm(const AdamwChunk* __restrict__ chunks, int64_t n, double* __restrict__ partial) {
+  typedef typename Elem<GT>::one one;
+  typedef typename Elem<GT>::wide wide;
+  constexpr int WIDE = Elem<GT>::WIDE, TURNS = kAdamwChunk / (kThreads * WIDE);
   __shared__ double red[kThreads / kWave];
   double acc = 0.0;
-  for (int64_t b = blockIdx.x; b < n; b += gridDim.x) {
-    const AdamwChunk& c = chunks[b];
-    const void* g = c.grad;
-    const int len = c.n;
-    f32x4 v[kTurns];
-    if (len == kAdamwChunk) {
+  int64_t b = blockIdx.x;
+  const void* at = chunks[b].grad;                         // the grid is no larger than the list
+  int len = chunks[b].n;
+  while (b < n) {
+    const GLOBAL one* g = gbl(static_cast<const one*>(at));
+    const int left = len;
+    wide v[TURNS];
+    if (left == kAdamwChunk) {
 #pragma unroll
-      for (int u = 0; u < kTurns; ++u) v[u] = load_four<GT>(g, (u * kThreads + threadIdx.x) * kPer);
+      for (int u = 0; u < TURNS; ++u) v[u] = *gcast<wide>(g + (u * kThreads + threadIdx.x) * WIDE);
     } else {
 #pragma unroll
-      for (int u = 0; u < kTurns; ++u) {
-        const int i = (u * kThreads + threadIdx.x) * kPer;
-        if (i + kPer <= len) v[u] = load_four<GT>(g, i);
-        else v[u] = load_some<GT>(g, i, len - i);
+      for (int u = 0; u < TURNS; ++u) {
+        const int i = (u * kThreads + threadIdx.x) * WIDE;
+        v[u] = wide(0);
+#pragma unroll
+        for (int j = 0; j < WIDE; ++j)
+          if (i + j < left) v[u][j] = g[i + j];
       }
     }
+    b += gridDim.x;
+    if (b < n) {                                           // the next chunk's place, while this one arrives
+      at = chunks[b].grad;
+      len = chunks[b].n;
+    }
 #pragma unroll
-    for (int u = 0; u < kTurns; ++u)
+    for (int u = 0; u < TURNS; ++u)
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) acc += (double)v[u][j] * (double)v[u][j];
+      for (int j = 0; j < WIDE; ++j) acc += (double)(float)v[u][j] * (double)(float)v[u][j];
   }
   const double sum = block_sum(acc, red);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
@@ -285,26 +301,43 @@ void k_adamw(const AdamwChunk* __restrict__ chunks, AdamwArgs a) {
   else adamw_chunk<PT, GT, LOW, SR, false>(c, a);
 }
 
-// Values of 8-bit moments, 4 a lane; blockIdx.y picks the moment. bf16 holds every value but those
-// below its subnormals.
-template <int OT>
+// Values of 8-bit moments, 16 bytes of them a lane and turn; blockIdx.y picks the moment. bf16 holds every
+// value but those below its subnormals. Four turns, whose loads are all sent for first, where that leaves four
+// workgroups a CU (188.9 million elements: 200 us, 5.7 TB/s; one turn of 8 bytes 256), one elsewhere
+// (0.76 million: 3.0 us, with four 4.3).
+template <int OT, int TURNS>
 __global__ __launch_bounds__(kThreads)
 void k_adamw_moments(const uint8_t* m1, const uint8_t* e1, const uint8_t* m2, const uint8_t* e2, int64_t n, void* out1, void* out2) {
-  const bool second = blockIdx.y != 0;
   typedef typename Elem<OT>::one one;
+  constexpr int WIDE = Elem<OT>::WIDE;
+  const bool second = blockIdx.y != 0;
   const GLOBAL uint8_t* m = gbl(second ? m2 : m1);
   const GLOBAL uint8_t* ex = gbl(second ? e2 : e1);
   GLOBAL one* out = gbl(static_cast<one*>(second ? out2 : out1));
-  for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kPer; i < n; i += (int64_t)gridDim.x * kThreads * kPer) {
-    const uint32_t w = *gcast<uint32_t>(m + i);
-    const int e = ex[i / kAdamwGroup];
-    f32x4 v;
+  const int64_t i0 = ((int64_t)blockIdx.x * TURNS * kThreads + threadIdx.x) * WIDE;
+  uint32_t w[TURNS][WIDE / 4];
+  int e[TURNS];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) v[j] = second ? decode8<true>(w >> (8 * j) & 255, e) : decode8<false>(w >> (8 * j) & 255, e);
-    if (i + kPer <= n) {
-      *gcast<typename Elem<OT>::four>(out + i) = __builtin_convertvector(v, typename Elem<OT>::four);
+  for (int u = 0; u < TURNS; ++u) {
+    const int64_t i = i0 + u * kThreads * WIDE;            // codes reach to the end of its group
+    e[u] = 0;
+#pragma unroll
+    for (int q = 0; q < WIDE / 4; ++q) w[u][q] = i < n ? gcast<uint32_t>(m + i)[q] : 0;
+    if (i < n) e[u] = ex[i / kAdamwGroup];
+  }
+#pragma unroll
+  for (int u = 0; u < TURNS; ++u) {
+    const int64_t i = i0 + u * kThreads * WIDE;
+    typename Elem<OT>::wide v;
+#pragma unroll
+    for (int j = 0; j < WIDE; ++j) {
+      const uint32_t c = w[u][j / 4] >> (8 * (j % 4)) & 255;
+      v[j] = (one)(second ? decode8<true>(c, e[u]) : decode8<false>(c, e[u]));
+    }
+    if (i + WIDE <= n) {
+      *gcast<typename Elem<OT>::wide>(out + i) = v;
     } else {
-      for (int j = 0; i + j < n; ++j) out[i + j] = (one)v[j];
+      for (int j = 0; i + j < n; ++j) out[i + j] = v[j];
     }
   }
 }
@@ -354,10 +387,16 @@ hipError_t launch_adamw(const AdamwChunk* chunks, int64_t n, int pt, int gt, boo
 hipError_t launch_adamw_moments(const uint8_t* m1, const uint8_t* e1, const uint8_t* m2, const uint8_t* e2, int64_t n, void* out1,
                                 void* out2, int ot, hipStream_t s) {
   if (n <= 0) return hipSuccess;
-  const int64_t need = (n + kThreads * kPer - 1) / (kThreads * kPer);
-  const dim3 grid((unsigned)(need < 65536 ? need : 65536), 2), block(kThreads);
-  if (ot == G_F32) k_adamw_moments<G_F32><<<grid, block, 0, s>>>(m1, e1, m2, e2, n, out1, out2);
-  else k_adamw_moments<G_BF16><<<grid, block, 0, s>>>(m1, e1, m2, e2, n, out1, out2);
+  const int64_t per = kThreads * (ot == G_F32 ? Elem<G_F32>::WIDE : Elem<G_BF16>::WIDE), blocks = (n + per - 1) / per;
+  const bool four = 2 * blocks / 4 >= 1024;
+  const dim3 grid((unsigned)(four ? (blocks + 3) / 4 : blocks), 2), block(kThreads);
+  if (ot == G_F32) {
+    if (four) k_adamw_moments<G_F32, 4><<<grid, block, 0, s>>>(m1, e1, m2, e2, n, out1, out2);
+    else k_adamw_moments<G_F32, 1><<<grid, block, 0, s>>>(m1, e1, m2, e2, n, out1, out2);
+  } else {
+    if (four) k_adamw_moments<G_BF16, 4><<<grid, block, 0, s>>>(m1, e1, m2, e2, n, out1, out2);
+    else k_adamw_moments<G_BF16, 1><<<grid, block, 0, s>>>(m1, e1, m2, e2, n, out1, out2);
+  }
   return hipGetLastError();
 }
 

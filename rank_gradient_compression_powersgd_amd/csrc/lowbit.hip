@@ -190,6 +190,7 @@ psgd_status psgd_adamw_moments(psgd_ctx* ctx, const uint8_t* m1, const uint8_t* 
   if (out_dtype != PSGD_F32 && out_dtype != PSGD_BF16) return fail(ctx, PSGD_EDTYPE, "moments come as fp32 or bf16, not dtype %d", (int)out_dtype);
   const int ot = grad_type(out_dtype);
   if (n < 0) return fail(ctx, PSGD_EINVAL, "negative size");
+  if (n > int64_t(1) << 35) return fail(ctx, PSGD_EUNSUPPORTED, "more than 2^35 values in a call");
   if (n == 0) return PSGD_OK;
   if (!m1 || !e1 || !m2 || !e2 || !out1 || !out2) return fail(ctx, PSGD_EINVAL, "NULL pointer");
   if (!aligned16(m1) || !aligned16(m2) || !aligned_to(out1, type_size(ot)) || !aligned_to(out2, type_size(ot)))

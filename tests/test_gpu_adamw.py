@@ -322,6 +322,29 @@ def test_moments_of_a_stream_of_their_own():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("n", [64, 1003, 4_300_001])
+def test_moments_of_short_and_long_lists(n):
+    """Against the oracle's values, of any codes and any exponents that keep them out of the subnormals."""
+    import torch
+    from rank_gradient_compression_powersgd_amd import binding as B
+    rng = np.random.default_rng(n)
+    room = (n + 63) // 64 * 64
+    codes = [torch.from_numpy(rng.integers(0, 256, room, dtype=np.uint8)).cuda() for _ in range(2)]
+    exps = [torch.from_numpy(rng.integers(40, 256, room // 64).astype(np.uint8)).cuda() for _ in range(2)]       # no fp32 subnormals
+    ctx = B.psgd_create(0, 1)
+    for dtype in (torch.float32, torch.bfloat16):
+        flat = [torch.full((n + 7,), 7.0, dtype=dtype, device="cuda") for _ in range(2)]
+        outs = [f[1:n + 1] for f in flat]
+        B.psgd_adamw_moments(ctx, codes[0], exps[0], codes[1], exps[1], *outs)
+        for i, second in ((0, False), (1, True)):
+            want = torch.from_numpy(L.decode8(codes[i].cpu().numpy(), exps[i].cpu().numpy(), second)[:n].astype(np.float32)).to(dtype)
+            got = outs[i].cpu()
+            assert torch.equal(torch.isnan(got), torch.isnan(want))
+            assert torch.equal(torch.nan_to_num(got, 0.0), torch.nan_to_num(want, 0.0))
+            assert float(flat[i][0]) == 7.0 and (flat[i][n + 1:] == 7).all()
+    B.psgd_destroy(ctx)
+
+
 def test_neighbours_of_a_list_are_left_alone():
     import torch
     from rank_gradient_compression_powersgd_amd import AdamWGroup
