@@ -409,6 +409,9 @@ def test_refusals():
     refused(B.PSGD_EINVAL, lambda: B.psgd_adamw_update(other, group.plan, word, word, norm, _hp()))
     lib = B.load_library()
     assert lib.psgd_adamw_update(group.ctx, group.plan, word.data_ptr(), word.data_ptr(), None, B.ctypes.byref(_hp()), 2, 0, None) == B.PSGD_EINVAL
+    args = [t.data_ptr() for t in (group.m1, group.e1, group.m2, group.e2)]
+    assert lib.psgd_adamw_moments(group.ctx, *args, 2 ** 35 + 1, f.data_ptr(), f.data_ptr(), 3, None) == B.PSGD_EUNSUPPORTED
+    assert lib.psgd_adamw_moments(group.ctx, *args, -1, f.data_ptr(), f.data_ptr(), 3, None) == B.PSGD_EINVAL
     t = B.make_adamw_tensor(f, f.clone(), group.m1, group.m2, group.e1, group.e2)
     refused(B.PSGD_EDTYPE, lambda: B.psgd_adamw_plan_create(other, [t], 7, 3, 1))
     refused(B.PSGD_EDTYPE, lambda: B.psgd_adamw_plan_create(other, [t], 3, 0, 1))
