@@ -4,7 +4,8 @@
 
 Every HIP source under csrc/ is compiled to an object file in csrc/_build/ and linked into
 rank_gradient_compression_powersgd_amd/libpsgd.so. Packed fp32 instructions are disabled for
-device code (-Xclang -target-feature -Xclang -packed-fp32-ops).
+device code (-Xclang -target-feature -Xclang -packed-fp32-ops). The objects of sources that
+name accumulation registers in asm are disassembled and refused if anything else writes those.
 """
 from __future__ import annotations
 
@@ -12,9 +13,11 @@ import argparse
 import concurrent.futures as cf
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -28,6 +31,11 @@ COMMON = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wno-unused-command-line-argument", "-I", INCLUDE,
 ]
+
+# Sources whose sums stand in accumulation registers by name. The compiler does not know what these hold: it
+# has to keep out of them.
+NAMED_SUMS = ("k_mx_gemm.hip",)
+ACCUMULATION = re.compile(r"(?<![\w.])a(?:\d+|\[\d+(?::\d+)?\])")
 
 
 def hipcc() -> str:
@@ -48,6 +56,43 @@ def _run(cmd, verbose):
         print(out)
 
 
+def foreign_accumulation(assembly: str):
+    """Lines of a disassembly that use an accumulation register otherwise than an MFMA, or a move from it to an
+    ordinary one."""
+    found = []
+    for line in assembly.splitlines():
+        code = line.split("//", 1)[0].strip()
+        op, _, operands = code.partition(" ")
+        if line[:1] in "\t " and ACCUMULATION.search(operands) and not op.startswith("v_mfma_"):
+            if op != "v_accvgpr_read_b32" or ACCUMULATION.search(operands.split(",")[0]):
+                found.append(code)
+    return found
+
+
+def disassembly(obj: str) -> str:
+    """Device code of an object file made here."""
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+
+    def tool(name):
+        for c in (os.path.join(r, "lib", "llvm", "bin", name) for r in (rocm, "/opt/rocm")):
+            if os.path.exists(c):
+                return c
+        raise RuntimeError(f"{name} not found: the built kernels cannot be looked at")
+
+    with tempfile.TemporaryDirectory() as d:
+        bundle, code = os.path.join(d, "bundle"), os.path.join(d, "code")
+        _run([tool("llvm-objcopy"), "--dump-section", f".hip_fatbin={bundle}", obj, os.path.join(d, "copy")], False)
+        _run([tool("clang-offload-bundler"), "--unbundle", "--type=o", f"--input={bundle}", f"--output={code}",
+              f"--targets=hipv4-amdgcn-amd-amdhsa--{ARCH}"], False)
+        return subprocess.run([tool("llvm-objdump"), "-d", code], stdout=subprocess.PIPE, text=True, check=True).stdout
+
+
+def check_named_sums(obj: str) -> None:
+    found = foreign_accumulation(disassembly(obj))
+    if found:
+        raise RuntimeError(f"{obj}: the compiler uses accumulation registers that hold sums: {found[:4]}")
+
+
 def build(jobs: int = 0, verbose: bool = False, defines=(), out: str = "") -> str:
     """Compile every csrc/*.hip and link libpsgd.so (or `out`). `defines` are extra -D macros
     (kernel tile parameters) for alternative builds."""
@@ -63,6 +108,9 @@ def build(jobs: int = 0, verbose: bool = False, defines=(), out: str = "") -> st
         futs = [ex.submit(_run, [cc, *COMMON, *dflags, "-c", s, "-o", o], verbose) for s, o in zip(srcs, objs)]
         for f in futs:
             f.result()
+    for s, o in zip(srcs, objs):
+        if os.path.basename(s) in NAMED_SUMS:
+            check_named_sums(o)
     tmp = lib + ".tmp"
     _run([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp], verbose)
     os.replace(tmp, lib)

@@ -37,9 +37,12 @@ template <int SP, int SQ> __device__ __forceinline__ f32x4 mfma_mx(u32x4 p, u32x
 
 // The same with sum I of a tile of N x N in the accumulation registers 4 I .. 4 I + 3; NEW: what the sum
 // held is not read. As asm, since the compiler keeps sums of this many registers in ordinary ones, with
-// a move for every use, and on registers by name: every statement marks all of the tile's as written, so
-// the compiler keeps nothing of its own there and never moves a sum. Consecutive uses of one sum are a
-// whole row of MFMAs apart; settle() stands between the last of them and the first read of a sum.
+// a move for every use (as operands "+a" of these statements 256 of them spill), and on registers by name.
+// Every statement that writes or reads sums, and settle() between the two, marks all of the tile's as written,
+// so the compiler keeps nothing across any of them there and never moves a sum. What it might keep there
+// between two of them the build looks for in the object (build.py: only MFMAs write accumulation
+// registers in this file). Consecutive uses of one sum are a whole row of MFMAs apart; settle() stands
+// between the last of them and the first read of a sum.
 #define MX_A10(p) "a" #p "0", "a" #p "1", "a" #p "2", "a" #p "3", "a" #p "4", "a" #p "5", "a" #p "6", "a" #p "7", "a" #p "8", "a" #p "9"
 #define MX_A16 "a0", "a1", "a2", "a3", "a4", "a5", "a6", "a7", "a8", "a9", "a10", "a11", "a12", "a13", "a14", "a15"
 #define MX_A64 MX_A16, "a16", "a17", "a18", "a19", MX_A10(2), MX_A10(3), MX_A10(4), MX_A10(5), "a60", "a61", "a62", "a63"
@@ -74,11 +77,20 @@ template <int N, int I, int Y, int SP, bool NEW> __device__ __forceinline__ void
   else if constexpr (NEW) MX_ROW2(MX_ZERO);
   else MX_ROW2(MX_KEEP);
 }
-__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
-template <int I> __device__ __forceinline__ f32x4 sum_of() {
+template <int N> __device__ __forceinline__ void settle() {
+  if constexpr (N == 8) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory", MX_A256);
+  else if constexpr (N == 4) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory", MX_A64);
+  else asm volatile("s_nop 15\n\ts_nop 15" ::: "memory", MX_A16);
+}
+#define MX_READ(CLOBBER)                                                                                               \
+  asm volatile("v_accvgpr_read_b32 %0, a[%4]\n\tv_accvgpr_read_b32 %1, a[%5]\n\tv_accvgpr_read_b32 %2, a[%6]\n\t"     \
+               "v_accvgpr_read_b32 %3, a[%7]" : "=v"(v0), "=v"(v1), "=v"(v2), "=v"(v3)                                 \
+               : "n"(4 * I), "n"(4 * I + 1), "n"(4 * I + 2), "n"(4 * I + 3) : CLOBBER)
+template <int N, int I> __device__ __forceinline__ f32x4 sum_of() {
   float v0, v1, v2, v3;
-  asm volatile("v_accvgpr_read_b32 %0, a[%4]\n\tv_accvgpr_read_b32 %1, a[%5]\n\tv_accvgpr_read_b32 %2, a[%6]\n\tv_accvgpr_read_b32 %3, a[%7]"
-               : "=v"(v0), "=v"(v1), "=v"(v2), "=v"(v3) : "n"(4 * I), "n"(4 * I + 1), "n"(4 * I + 2), "n"(4 * I + 3));
+  if constexpr (N == 8) MX_READ(MX_A256);
+  else if constexpr (N == 4) MX_READ(MX_A64);
+  else MX_READ(MX_A16);
   return f32x4{v0, v1, v2, v3};
 }
 
@@ -393,7 +405,7 @@ void k_mx_gemm(MxProduct a, int items) {
   // ---- results -------------------------------------------------------------------------------------------
   const float scale = !SPLIT && a.scale ? *a.scale : 1.0f;
   auto results = [&](const Item& it) {
-    settle();
+    settle<N>();
     const int64_t i0 = it.i0 + wi0, j0 = it.j0 + wj0;
     if constexpr (SPLIT) {
       GLOBAL float* o = gbl(a.partial) + ((int64_t)it.split * a.m + j0 + c) * a.n + i0 + 4 * g;
@@ -402,7 +414,7 @@ void k_mx_gemm(MxProduct a, int items) {
         constexpr int Y = decltype(yy)::value;
         each<N>([&](auto xx) {
           constexpr int X = decltype(xx)::value;
-          const f32x4 v = sum_of<X * N + Y>();
+          const f32x4 v = sum_of<N, X * N + Y>();
           if (16 * Y < rows && 16 * X < cols) {
             if (16 * X + 4 <= cols) *gcast<f32x4_u>(o + 16 * X) = v;
             else
@@ -424,7 +436,7 @@ void k_mx_gemm(MxProduct a, int items) {
         constexpr int Y = decltype(yy)::value;
         each<N / 2>([&](auto xx) {
           constexpr int X = 2 * decltype(xx)::value;
-          const f32x4 v = sum_of<X * N + Y>() * scale, w = sum_of<(X + 1) * N + Y>() * scale;
+          const f32x4 v = sum_of<N, X * N + Y>() * scale, w = sum_of<N, (X + 1) * N + Y>() * scale;
           const eight u = __builtin_convertvector(f32x8{v[0], v[1], v[2], v[3], w[0], w[1], w[2], w[3]}, eight);
           if (16 * Y < rows && 16 * X < cols) {
             if (eights || 16 * X + 8 <= cols) {
@@ -454,7 +466,7 @@ void k_mx_gemm(MxProduct a, int items) {
         __builtin_amdgcn_sched_barrier(0);
         each<N>([&](auto xx) {
           constexpr int X = decltype(xx)::value;
-          *gcast<f32x4_u>(o + 16 * Y * a.ldc + 16 * X) = sum_of<X * N + Y>() * scale + old[Y & 1][X];
+          *gcast<f32x4_u>(o + 16 * Y * a.ldc + 16 * X) = sum_of<N, X * N + Y>() * scale + old[Y & 1][X];
         });
       });
     } else {
@@ -462,7 +474,7 @@ void k_mx_gemm(MxProduct a, int items) {
         constexpr int Y = decltype(yy)::value;
         each<N>([&](auto xx) {
           constexpr int X = decltype(xx)::value;
-          finish<OT>(a, j0 + 16 * Y + c, i0 + 16 * X + 4 * g, sum_of<X * N + Y>(), scale);
+          finish<OT>(a, j0 + 16 * Y + c, i0 + 16 * X + 4 * g, sum_of<N, X * N + Y>(), scale);
         });
       });
     }
