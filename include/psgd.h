@@ -481,7 +481,9 @@ typedef enum psgd_rounding { PSGD_NEAREST = 0, PSGD_STOCHASTIC = 1 } psgd_roundi
  *     64 elements, of their largest magnitude (one more from 1.875 times its power of two on). m1: sign,
  *     4 exponent and 3 fraction bits; m2: 5 exponent and 3 fraction bits, the largest field standing for
  *     the byte's exponent, both with subnormals: 3 fraction bits down to 2^-14 (m1) and 2^-30 (m2) of the
- *     largest. A positive m2 never becomes 0. Byte 255: all 64 are NaN (a moment from 1.875 2^127 on).
+ *     largest. A positive m2 never becomes 0. Byte 255: a moment of the 64 was past 1.875 2^127 (m2 where |c g| is
+ *     past 1.8e19), and psgd_adamw_moments gives NaN for all of them. The next step takes m1 as 0 and, of such m2,
+ *     m2 as 1.875 2^127: the 64 parameters stand still, but for weight decay, until m2 has decayed.
  * All zero is the state before the first step, in both forms. Elements past numel are written as 0.
  * Moments rounded to nearest stand still once a step changes them by less than half a code; with
  * PSGD_STOCHASTIC their expectation moves as in fp32.

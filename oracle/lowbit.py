@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import numpy as np
 
-__all__ = ["adamw_param", "bias_free", "code_values", "decode8", "encode8", "hash_bits", "hash_key", "hash_more", "moments32",
+__all__ = ["adamw_param", "bias_free", "carried8", "code_values", "decode8", "encode8", "hash_bits", "hash_key", "hash_more", "moments32",
            "mx_quantize", "mx_unpack", "mx_values", "round16"]
 
 GRID = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
@@ -56,6 +56,14 @@ def decode8(codes, exps, second: bool) -> np.ndarray:
     v = v if second else np.where(c > 127, -v, v)
     with np.errstate(over="ignore"):
         return np.where(e == 255, np.nan, v * 2.0 ** (e - 127.0)).reshape(-1)
+
+
+def carried8(c1, e1, c2, e2):
+    """(m1, m2) as a step takes them up: those of a group whose m2 were lost (byte 255) as 0 and the format's largest
+    value, lost m1 as 0."""
+    m1, m2 = decode8(c1, e1, False), decode8(c2, e2, True)
+    lost1, lost2 = (np.repeat(np.asarray(e) == 255, 64) for e in (e1, e2))
+    return np.where(lost1 | lost2, 0.0, m1), np.where(lost2, 1.875 * 2.0 ** 127, m2)
 
 
 def encode8(v, second: bool, u=None):

@@ -78,10 +78,14 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
 
 template <bool SECOND> constexpr int kTop = SECOND ? 31 : 15;
 
-template <bool SECOND> __device__ __forceinline__ float decode8(uint32_t c, int e) {
+// lost: what a group of byte 255 reads as. A step takes the largest value for its second moments, and 0 for the
+// first ones (theirs would move a parameter by up to 1e19 lr against it): 64 parameters stand still till the second
+// moments have decayed, instead of being NaN from the next step on.
+constexpr float kLargest8 = 1.875f * 0x1p127f;
+template <bool SECOND> __device__ __forceinline__ float decode8(uint32_t c, int e, float lost) {
   const float v = __builtin_amdgcn_ldexpf(float_of((SECOND ? c : c & 127) << 20), e - kTop<SECOND>);
   const float s = SECOND ? v : float_of(bits_of(v) | (c & 128) << 24);
-  return e == 255 ? __builtin_nanf("") : s;
+  return e == 255 ? lost : s;
 }
 // r: 16 random bits (read where SR)
 template <bool SECOND, bool SR> __device__ __forceinline__ uint32_t encode8(float v, int e, uint32_t r) {
@@ -240,6 +244,7 @@ __device__ __forceinline__ void adamw_chunk(const AdamwChunk& c, const AdamwArgs
   for (int u = 0; u < kTurns; ++u) {
     const int i = (u * kThreads + threadIdx.x) * kPer;
     if (!whole && i >= room) continue;
+    if (LOW && x2[u] == 255) x1[u] = 255;
     uint32_t r[kPer];
     typename Elem<PT>::one out[kPer];
 #pragma unroll
@@ -247,8 +252,8 @@ __device__ __forceinline__ void adamw_chunk(const AdamwChunk& c, const AdamwArgs
       r[j] = SR ? hash_bits(high, (uint32_t)c.first + i + j) : 0;
       float a1, a2;
       if constexpr (LOW) {
-        a1 = decode8<false>(c1[u] >> (8 * j) & 255, (int)x1[u]);
-        a2 = decode8<true>(c2[u] >> (8 * j) & 255, (int)x2[u]);
+        a1 = decode8<false>(c1[u] >> (8 * j) & 255, (int)x1[u], 0.0f);
+        a2 = decode8<true>(c2[u] >> (8 * j) & 255, (int)x2[u], kLargest8);
       } else {
         a1 = m1[u][j];
         a2 = m2[u][j];
@@ -315,6 +320,7 @@ void k_adamw_moments(const uint8_t* m1, const uint8_t* e1, const uint8_t* m2, co
   const GLOBAL uint8_t* ex = gbl(second ? e2 : e1);
   GLOBAL one* out = gbl(static_cast<one*>(second ? out2 : out1));
   const int64_t i0 = ((int64_t)blockIdx.x * TURNS * kThreads + threadIdx.x) * WIDE;
+  const float nan = __builtin_nanf("");
   uint32_t w[TURNS][WIDE / 4];
   int e[TURNS];
 #pragma unroll
@@ -332,7 +338,7 @@ void k_adamw_moments(const uint8_t* m1, const uint8_t* e1, const uint8_t* m2, co
 #pragma unroll
     for (int j = 0; j < WIDE; ++j) {
       const uint32_t c = w[u][j / 4] >> (8 * (j % 4)) & 255;
-      v[j] = (one)(second ? decode8<true>(c, e[u]) : decode8<false>(c, e[u]));
+      v[j] = (one)(second ? decode8<true>(c, e[u], nan) : decode8<false>(c, e[u], nan));
     }
     if (i + WIDE <= n) {
       *gcast<typename Elem<OT>::wide>(out + i) = v;

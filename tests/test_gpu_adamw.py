@@ -430,3 +430,54 @@ def test_refusals():
     refused(B.PSGD_EINVAL, lambda: AdamWGroup([f], [f]))
     refused(B.PSGD_EINVAL, lambda: B.psgd_adamw_plan_create(other, [t, B.make_adamw_tensor(g2, g2.clone(), m[0], group.m1, *e)], 3, 3, 1))
     B.psgd_destroy(other)
+
+
+class _AfterALoss(Case):
+    """Reads groups of byte 255 as a step does."""
+
+    def moments(self):
+        g = self.group
+        m1, m2 = L.carried8(*(x.cpu().numpy() for x in (g.m1, g.e1, g.m2, g.e2)))
+        ends = [o + len(_pad(np.zeros(n))) for o, n in zip(g.offsets, self.sizes)]
+        return [(m1[o:e], m2[o:e]) for o, e in zip(g.offsets, ends)]
+
+
+@pytest.mark.parametrize("stochastic", [True, False])
+@pytest.mark.parametrize("sizes", [[192], [4096 + 200, 70]], ids=lambda s: "_".join(map(str, s)))
+def test_a_gradient_whose_square_is_past_fp32_leaves_its_neighbours_finite(sizes, stochastic):
+    """The step after it and later ones: bit by bit, and every parameter stays a number."""
+    import torch
+    c = _AfterALoss(sizes, "f32", "f32", 8, stochastic, seed=4)
+    good = c.g_all.clone()
+    c.grads[0][70] = 1e25
+    c.group.step(_hp())
+    c.t += 1
+    assert int(c.group.e2[1]) == 255 and c.group.skip.item() == 0 and torch.isfinite(c.p_all).all()
+    c.g_all.copy_(good)
+    for _ in range(3):
+        c.step_and_check()
+        assert torch.isfinite(c.p_all).all() and int(c.group.e2[1]) == 254
+    c.grads[0][70] = -1e25                                         # and once more
+    c.group.step(_hp())
+    c.t += 1
+    c.g_all.copy_(good)
+    c.step_and_check()
+    assert torch.isfinite(c.p_all).all()
+
+
+def test_a_lost_group_moves_again_once_its_second_moment_has_decayed():
+    import torch
+    from rank_gradient_compression_powersgd_amd import AdamWGroup
+    p, g = torch.zeros(192, device="cuda"), torch.ones(192, device="cuda")
+    g[70] = 1e25
+    group = AdamWGroup([p], [g])
+    hp = _hp((1e-3, 0.9, 0.5, 1e-8, 0.0))
+    group.step(hp)
+    g[70] = 1.0
+    still = p[64:128].clone()
+    for _ in range(20):                                            # 1.875 2^127 halves in a step
+        group.step(hp)
+    assert (p[64:128] - still).abs().max() < 1e-9 and torch.isfinite(p).all()
+    for _ in range(200):
+        group.step(hp)
+    assert torch.isfinite(p).all() and (p[64:128] < still - 0.05).all() and torch.isfinite(group.moments(torch.float32)[1]).all()

@@ -81,3 +81,13 @@ def test_stochastic_rounding_keeps_the_expectation():
         w = L.round16(y, kind, u.reshape(-1))
         assert set(np.unique(w)) == {1.0, 1.0 + 2.0 ** -bits}
         assert abs(w.mean() - y[0]) < 5 * 0.5 * 2.0 ** -bits / np.sqrt(n)
+
+
+def test_a_lost_group_reads_as_nan_and_is_taken_up_as_the_largest_value():
+    c = np.full(192, 77, np.uint8)
+    e1, e2 = np.array([130, 140, 255], np.uint8), np.array([131, 255, 140], np.uint8)
+    assert np.isnan(L.decode8(c, e1, False)[128:]).all() and np.isnan(L.decode8(c, e2, True)[64:128]).all()
+    m1, m2 = L.carried8(c, e1, c, e2)
+    assert np.array_equal(m1[:64], L.decode8(c, e1, False)[:64]) and (m1[64:] == 0).all()
+    assert np.array_equal(m2[:64], L.decode8(c, e2, True)[:64]) and (m2[64:128] == 1.875 * 2.0 ** 127).all()
+    assert np.array_equal(m2[128:], L.decode8(c, e2, True)[128:])
