@@ -521,7 +521,8 @@ psgd_status psgd_adamw_prepare(psgd_ctx* ctx, psgd_adamw_plan* plan, float max_n
 /* One step on the list with the scalars of psgd_adamw_prepare (or psgd_adam_prepare, where the clipping
  * factor covers more than this list). norm_dev may be NULL (no clipping). A step whose skip word is set
  * changes nothing. rounding applies to 8-bit moments and 16-bit parameters; seed is not read with
- * PSGD_NEAREST. Moments are computed in fp32, each operation rounded; the quotient is within 2^-21. */
+ * PSGD_NEAREST. Moments are computed in fp32, each operation rounded; the quotient is within 2^-21, and
+ * a denominator below 2^-126 (eps is, and m2 is 0) counts as 2^-126: a parameter of moments 0 stands still with any eps. */
 psgd_status psgd_adamw_update(psgd_ctx* ctx, psgd_adamw_plan* plan, const int32_t* skip_dev, const int32_t* step_dev,
                               const float* norm_dev, const psgd_adam_hparams* hp, psgd_rounding rounding, uint64_t seed,
                               hipStream_t stream);

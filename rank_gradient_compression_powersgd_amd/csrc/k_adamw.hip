@@ -262,7 +262,10 @@ __device__ __forceinline__ void adamw_chunk(const AdamwChunk& c, const AdamwArgs
       a1 = a1 * a.beta1 + gc * omb1;
       a2 = a2 * a.beta2 + (gc * gc) * omb2;
       if (!whole && i + j >= len) a1 = a2 = 0.0f;
-      const float upd = (a1 * rbc1) * __builtin_amdgcn_rcpf(fast_sqrt(a2 * rbc2) + a.eps);
+      // The reciprocal takes no subnormals: below them (eps is, and a2 0) a denominator counts as 2^-126, so that a
+      // moment of 0 moves nothing. rbc1 comes last, since it could take a1 past fp32, where a2 is an infinity.
+      const float den = fast_sqrt(a2 * rbc2) + a.eps;
+      const float upd = a1 * __builtin_amdgcn_rcpf(den < 0x1p-126f ? 0x1p-126f : den) * rbc1;
       const float th = p[u][j];
       out[j] = to_param<PT, SR>(th - a.lr * (upd + a.weight_decay * th), SR && PT != G_F32 ? hash_more(r[j]) : 0);
       m1[u][j] = a1;

@@ -481,3 +481,36 @@ def test_a_lost_group_moves_again_once_its_second_moment_has_decayed():
     for _ in range(200):
         group.step(hp)
     assert torch.isfinite(p).all() and (p[64:128] < still - 0.05).all() and torch.isfinite(group.moments(torch.float32)[1]).all()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-40, 1.1e-38, 1.2e-38])
+def test_an_eps_among_the_subnormals_leaves_parameters_without_a_gradient(bits, eps):
+    """0 of any eps > 0 is 0, and of eps = 0 counts as that."""
+    import torch
+    from rank_gradient_compression_powersgd_amd import AdamWGroup
+    p, g = torch.ones(200, device="cuda"), torch.zeros(200, device="cuda")
+    g[150:] = 0.5
+    group = AdamWGroup([p], [g], bits=bits)
+    for t in range(1, 4):
+        group.step(_hp((0.1, 0.9, 0.999, eps, 0.0)))
+        assert (p[:150] == 1).all() and torch.isfinite(p).all()
+        assert t > 1 or (p[150:] - 0.9).abs().max() < 1e-5         # |update| 1 in the first step
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("b1", [0.9, 0.95])
+def test_a_gradient_at_the_end_of_fp32_leaves_its_parameter_a_number(bits, b1):
+    """Its second moment is an infinity: no update. Its first moment, bias corrected, rounds past fp32 for these b1."""
+    import torch
+    from rank_gradient_compression_powersgd_amd import AdamWGroup
+    top = torch.finfo(torch.float32).max
+    f = np.float32
+    with np.errstate(over="ignore"):
+        assert np.isinf(f(top) * (f(1) - f(b1)) * f(L.bias_free(b1, 1)))
+    p, g = torch.ones(200, device="cuda"), torch.full((200,), 1e-3, device="cuda")
+    g[7], g[100] = top, -top
+    group = AdamWGroup([p], [g], bits=bits)
+    for _ in range(4):
+        group.step(_hp((0.1, b1, 0.999, 1e-8, 0.0)))
+        assert group.skip.item() == 0 and torch.isfinite(p).all() and (p[[7, 100]] == 1).all()
