@@ -677,9 +677,27 @@ def psgd_adamw_plan_destroy(plan: int) -> None:
     load_library().psgd_adamw_plan_destroy(plan)
 
 
+def _words(call: str, ctx: int, norm, **words):
+    """Device words of a step: one int32 each, a norm of two fp32, on the context's device. None is the library's to
+    take or refuse."""
+    import torch
+    given = [t for t in (norm, *words.values()) if t is not None]
+    for name, t, dtype, n in (("norm_dev", norm, torch.float32, 2), *((k, t, torch.int32, 1) for k, t in words.items())):
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise PsgdError(call, PSGD_EDTYPE, f"{name} must be {dtype}, got {t.dtype}")
+        if t.numel() < n or not t.is_contiguous():
+            raise PsgdError(call, PSGD_EINVAL, f"{name} must hold {n} contiguous value{'s' if n > 1 else ''}")
+    if given:
+        _same_device(call, *given, ctx=ctx)
+
+
 def psgd_adamw_prepare(ctx: int, plan: int, max_norm: float, skip_in, skip_dev, step_dev, norm_dev, stream=None) -> None:
     """Skip word, step count, norm and clipping factor of a step from the list's gradients (skip_in: a skip word
-    decided before, or None), on the current stream of the context's device by default."""
+    decided before, or None), on the current stream of the context's device by default. skip_in, skip_dev and step_dev:
+    int32, one value; norm_dev: fp32, two."""
+    _words("psgd_adamw_prepare", ctx, norm_dev, skip_in=skip_in, skip_dev=skip_dev, step_dev=step_dev)
     _check(ctx, "psgd_adamw_prepare", load_library().psgd_adamw_prepare(
         ctx, plan, float(max_norm), _ptr(skip_in), _ptr(skip_dev), _ptr(step_dev), _ptr(norm_dev),
         _stream(stream, _ctx_device.get(ctx))))
@@ -687,8 +705,9 @@ def psgd_adamw_prepare(ctx: int, plan: int, max_norm: float, skip_in, skip_dev, 
 
 def psgd_adamw_update(ctx: int, plan: int, skip_dev, step_dev, norm_dev, hp, stochastic: bool = False, seed: int = 0,
                       stream=None) -> None:
-    """One AdamW step of the plan's list (norm_dev may be None: no clipping)."""
+    """One AdamW step of the plan's list (norm_dev may be None: no clipping), by words as psgd_adamw_prepare writes them."""
     h = _hparams(hp)
+    _words("psgd_adamw_update", ctx, norm_dev, skip_dev=skip_dev, step_dev=step_dev)
     _check(ctx, "psgd_adamw_update", load_library().psgd_adamw_update(
         ctx, plan, _ptr(skip_dev), _ptr(step_dev), _ptr(norm_dev), ctypes.byref(h), _rounding(stochastic),
         seed & 0xFFFFFFFFFFFFFFFF, _stream(stream, _ctx_device.get(ctx))))

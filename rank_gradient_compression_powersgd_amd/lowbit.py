@@ -71,9 +71,9 @@ class AdamWGroup:
 
     def step(self, hp, max_norm: float = 0.0, skip=None, stream=None):
         """One step: skip word, norm and clipping factor from the gradients, then the update. skip: a skip word
-        decided before (PowerSGDGroup.skip, where the gradients are its decompressed ones), or None."""
+        decided before (int32; PowerSGDGroup.skip, where the gradients are its decompressed ones), or None."""
         if skip is not None:
-            B._same_device("psgd_adamw_prepare", self.skip, skip, ctx=self.ctx)
+            B._words("psgd_adamw_prepare", self.ctx, None, skip_in=skip)
         h = B._hparams(hp)
         inf = float("inf")
         if not (0 <= h.beta1 < 1 and 0 <= h.beta2 < 1 and 0 <= h.lr < inf and 0 <= h.eps < inf and 0 <= h.weight_decay < inf):
@@ -85,7 +85,8 @@ class AdamWGroup:
                                                                  self.seed & 0xFFFFFFFFFFFFFFFF, st))
 
     def state(self):
-        """The moments, for the constructor's `moments`; step_count belongs to a checkpoint as well."""
+        """The moments, for the constructor's `moments`; step_count belongs to a checkpoint as well, and is restored in
+        place (step_count.copy_)."""
         return (self.m1, self.m2, self.e1, self.e2) if self.bits == 8 else (self.m1, self.m2)
 
     def moments(self, dtype=None, stream=None):

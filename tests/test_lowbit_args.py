@@ -142,3 +142,41 @@ def test_calls_take_the_stream_of_their_device_and_refuse_another(lib, monkeypat
     _raises(B.PSGD_EINVAL, lambda: B.psgd_mx_dequantize(ctx, a, here), "one GPU")
     _raises(B.PSGD_EINVAL, lambda: B.psgd_mx_product(ctx, a, _Data(30, 20, 0), _On(torch.zeros(10, 30), 1)), "one GPU")
     assert len(lib.args("psgd_mx_quantize")) == 2 and len(lib.args("psgd_mx_product")) == 1
+
+
+def _group_of(lib):  # noqa: F811
+    """A group on device 1 of the recording library."""
+    group = lowbit.AdamWGroup.__new__(lowbit.AdamWGroup)
+    group.ctx, group.plan, group.device, group.stochastic, group.seed = B.psgd_create(1, 1), 7, torch.device("cuda", 1), True, 0
+    group.skip, group.step_count = (_On(torch.zeros(1, dtype=torch.int32), 1) for _ in range(2))
+    group.norm = _On(torch.zeros(2), 1)
+    return group
+
+
+def test_the_words_of_a_step_have_their_type_size_and_device(lib):  # noqa: F811
+    """The kernels read and write 4 bytes per word and 8 for the norm, whatever the tensor holds."""
+    ctx = B.psgd_create(1, 1)
+    on = lambda n, dtype, device=1: _On(torch.zeros(n, dtype=dtype), device)  # noqa: E731
+    word, norm, hp = on(1, torch.int32), on(2, torch.float32), B.psgd_adam_hparams(0.1, 0.9, 0.9, 1e-8, 0.0)
+    group = _group_of(lib)
+    wrong = [(B.PSGD_EDTYPE, on(1, d), "int32") for d in (torch.bool, torch.uint8, torch.float32, torch.int64)]
+    wrong += [(B.PSGD_EINVAL, on(0, torch.int32), "1 contiguous"), (B.PSGD_EINVAL, on(1, torch.int32, 0), ""),
+              (B.PSGD_EINVAL, torch.zeros(1, dtype=torch.int32), "GPU")]
+    for status, bad, text in wrong:
+        _raises(status, lambda: B.psgd_adamw_prepare(ctx, 7, 0.0, bad, word, word, norm), text)
+        _raises(status, lambda: B.psgd_adamw_prepare(ctx, 7, 0.0, None, bad, word, norm), text)
+        _raises(status, lambda: B.psgd_adamw_prepare(ctx, 7, 0.0, None, word, bad, norm), text)
+        _raises(status, lambda: B.psgd_adamw_update(ctx, 7, bad, word, norm, hp), text)
+        _raises(status, lambda: B.psgd_adamw_update(ctx, 7, word, bad, norm, hp), text)
+        _raises(status, lambda: group.step(hp, skip=bad), text)
+    for status, bad in ((B.PSGD_EINVAL, on(1, torch.float32)), (B.PSGD_EDTYPE, on(2, torch.float64)), (B.PSGD_EINVAL, on(2, torch.float32, 0)),
+                        (B.PSGD_EINVAL, _On(torch.zeros(4)[::2], 1))):
+        _raises(status, lambda: B.psgd_adamw_prepare(ctx, 7, 0.0, None, word, word, bad))
+        _raises(status, lambda: B.psgd_adamw_update(ctx, 7, word, word, bad, hp))
+    assert not lib.args("psgd_adamw_prepare") and not lib.args("psgd_adamw_update")
+    B.psgd_adamw_prepare(ctx, 7, 0.0, word, word, word, norm)
+    B.psgd_adamw_update(ctx, 7, word, word, None, hp)
+    group.step(hp, skip=word)
+    group.step(hp)
+    assert len(lib.args("psgd_adamw_prepare")) == len(lib.args("psgd_adamw_update")) == 3
+    group.plan = group.ctx = None
