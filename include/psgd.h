@@ -529,7 +529,8 @@ psgd_status psgd_adamw_update(psgd_ctx* ctx, psgd_adamw_plan* plan, const int32_
 
 /* The values of 8-bit moments, for checkpoints and monitoring: out1, out2 [n] in out_dtype PSGD_F32 or
  * PSGD_BF16 (which hold them exactly, down to their subnormals). m1 and m2 16-byte aligned, out aligned
- * to its type; 0 <= n <= 2^35 elements from the start of a group of 64 on. */
+ * to its type; 0 <= n <= 2^35 elements from the start of a group of 64 on. out1 and out2 overlap neither one
+ * another nor the moments. */
 psgd_status psgd_adamw_moments(psgd_ctx* ctx, const uint8_t* m1, const uint8_t* e1, const uint8_t* m2, const uint8_t* e2,
                                int64_t n, void* out1, void* out2, psgd_dtype out_dtype, hipStream_t stream);
 

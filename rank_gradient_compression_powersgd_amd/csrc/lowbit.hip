@@ -195,6 +195,11 @@ psgd_status psgd_adamw_moments(psgd_ctx* ctx, const uint8_t* m1, const uint8_t* 
   if (!m1 || !e1 || !m2 || !e2 || !out1 || !out2) return fail(ctx, PSGD_EINVAL, "NULL pointer");
   if (!aligned16(m1) || !aligned16(m2) || !aligned_to(out1, type_size(ot)) || !aligned_to(out2, type_size(ot)))
     return fail(ctx, PSGD_EINVAL, "m1 and m2 must be 16-byte aligned, the outputs aligned to their element type");
+  const int64_t groups = rup(n, psgd::kAdamwGroup) / psgd::kAdamwGroup;
+  const Bytes o1{out1, n * type_size(ot)}, o2{out2, n * type_size(ot)};
+  for (const Bytes& in : {Bytes{m1, groups * psgd::kAdamwGroup}, Bytes{e1, groups}, Bytes{m2, groups * psgd::kAdamwGroup}, Bytes{e2, groups}})
+    if (meet(o1, in) || meet(o2, in)) return fail(ctx, PSGD_EINVAL, "the outputs must not overlap the moments");
+  if (meet(o1, o2)) return fail(ctx, PSGD_EINVAL, "the outputs must not overlap");
   DeviceGuard dev(ctx->device);
   HIPCHK(ctx, dev.err, "hipSetDevice");
   HIPCHK(ctx, psgd::launch_adamw_moments(m1, e1, m2, e2, n, out1, out2, ot, stream), "moments");

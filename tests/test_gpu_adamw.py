@@ -514,3 +514,32 @@ def test_a_gradient_at_the_end_of_fp32_leaves_its_parameter_a_number(bits, b1):
     for _ in range(4):
         group.step(_hp((0.1, b1, 0.999, 1e-8, 0.0)))
         assert group.skip.item() == 0 and torch.isfinite(p).all() and (p[[7, 100]] == 1).all()
+
+
+def test_moments_refuse_outputs_over_their_inputs_and_one_another():
+    import torch
+    from rank_gradient_compression_powersgd_amd import binding as B
+    n = 1000
+    flat = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    at = lambda o, size: flat[o:o + size]  # noqa: E731
+    m1, m2, e1, e2 = at(0, 1024), at(1024, 1024), at(2048, 16), at(2064, 16)
+    ctx = B.psgd_create(0, 1)
+
+    def out(o, dtype):
+        return at(o, n * dtype.itemsize).view(dtype)
+
+    for dtype in (torch.float32, torch.bfloat16):
+        size = n * dtype.itemsize
+        free, second = 4096, 4096 + size
+        B.psgd_adamw_moments(ctx, m1, e1, m2, e2, out(free, dtype), out(second, dtype))               # neighbours
+        B.psgd_adamw_moments(ctx, m1, e1, m2, e2, out(2080, dtype), out(2080 + size, dtype))          # right behind the exponents
+        for bad in (0, 1020, 2044, 2060, 2076):                                                        # over m1, m1 and m2, m2, e1, e2
+            for outs in ((out(bad, dtype), out(second, dtype)), (out(free, dtype), out(bad, dtype))):
+                with pytest.raises(B.PsgdError) as ei:
+                    B.psgd_adamw_moments(ctx, m1, e1, m2, e2, *outs)
+                assert ei.value.status == B.PSGD_EINVAL and "overlap the moments" in str(ei.value), bad
+        with pytest.raises(B.PsgdError) as ei:
+            B.psgd_adamw_moments(ctx, m1, e1, m2, e2, out(free, dtype), out(second - 4, dtype))
+        assert ei.value.status == B.PSGD_EINVAL and "overlap" in str(ei.value)
+    assert not flat[:2080].any()
+    B.psgd_destroy(ctx)
