@@ -662,13 +662,33 @@ def make_adamw_tensor(param, grad, m1, m2, e1=None, e2=None) -> psgd_adamw_tenso
             raise PsgdError(call, PSGD_EINVAL, f"{name} must be contiguous with at least {want} elements")
         if dtype is not None and t.dtype != dtype:
             raise PsgdError(call, PSGD_EDTYPE, f"{name} must be {dtype}, got {t.dtype}")
-    return psgd_adamw_tensor(_ptr(param), _ptr(grad), _ptr(m1), _ptr(m2), _ptr(e1), _ptr(e2), n)
+    t = psgd_adamw_tensor(_ptr(param), _ptr(grad), _ptr(m1), _ptr(m2), _ptr(e1), _ptr(e2), n)
+    # what a list's codes and context are compared with
+    device = param.device
+    if grad.device != device or m1.device != device or m2.device != device or (e1 is not None and (e1.device != device or e2.device != device)):
+        raise PsgdError(call, PSGD_EINVAL, "tensors must live on one GPU")
+    t.types = _dtype(param, call), _dtype(grad, call), PSGD_STATE_F32 if e1 is None else PSGD_STATE_BYTE
+    t.device = device
+    return t
 
 
 def psgd_adamw_plan_create(ctx: int, tensors: Sequence[psgd_adamw_tensor], param_dtype: int, grad_dtype: int, state: int) -> int:
+    """A list stepped together. The codes are those of every tensor that make_adamw_tensor made, which live on the
+    context's device."""
+    call = "psgd_adamw_plan_create"
+    want, at = (param_dtype, grad_dtype, state), _ctx_device.get(ctx)
+    for t in tensors:
+        types = getattr(t, "types", want)
+        if types[:2] != want[:2]:
+            raise PsgdError(call, PSGD_EDTYPE, f"param and grad have dtypes {types[:2]}, the list {want[:2]}")
+        if types != want:
+            raise PsgdError(call, PSGD_EINVAL, f"the moments are of state {types[2]}, the list of {state}")
+        device = getattr(t, "device", None)
+        if device is not None and (device.type != "cuda" or at not in (None, device.index)):
+            raise PsgdError(call, PSGD_EINVAL, f"tensors live on {device}, the context on device {at}")
     arr = (psgd_adamw_tensor * max(1, len(tensors)))(*tensors)
     h = ctypes.c_void_p()
-    _check(ctx, "psgd_adamw_plan_create", load_library().psgd_adamw_plan_create(
+    _check(ctx, call, load_library().psgd_adamw_plan_create(
         ctx, arr, len(tensors), param_dtype, grad_dtype, state, ctypes.byref(h)))
     return h.value
 

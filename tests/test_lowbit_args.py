@@ -180,3 +180,34 @@ def test_the_words_of_a_step_have_their_type_size_and_device(lib):  # noqa: F811
     group.step(hp)
     assert len(lib.args("psgd_adamw_prepare")) == len(lib.args("psgd_adamw_update")) == 3
     group.plan = group.ctx = None
+
+
+def test_a_list_has_the_types_and_the_device_of_its_tensors(lib):  # noqa: F811
+    """A code of another type than the tensors' would have the kernels step past their ends."""
+    ctx = B.psgd_create(1, 1)
+    on = lambda n, dtype, device=1: _On(torch.zeros(n, dtype=dtype), device)  # noqa: E731
+
+    def tensor(param, grad, device=1, bits=8):
+        p, g = on(100, param, device), on(100, grad, device)
+        if bits == 32:
+            return B.make_adamw_tensor(p, g, on(128, torch.float32, device), on(128, torch.float32, device))
+        return B.make_adamw_tensor(p, g, on(128, torch.uint8, device), on(128, torch.uint8, device), on(2, torch.uint8, device),
+                                   on(2, torch.uint8, device))
+
+    f32, f16, bf16 = torch.float32, torch.float16, torch.bfloat16
+    create = lambda ts, p, g, s: B.psgd_adamw_plan_create(ctx, ts, p, g, s)  # noqa: E731
+    good = tensor(bf16, f32)
+    create([good], B.PSGD_BF16, B.PSGD_F32, B.PSGD_STATE_BYTE)
+    create([tensor(f16, f16, bits=32)], B.PSGD_F16, B.PSGD_F16, B.PSGD_STATE_F32)
+    create([B.psgd_adamw_tensor.from_buffer_copy(good)], B.PSGD_F32, B.PSGD_F32, B.PSGD_STATE_BYTE)   # a struct of the caller's own
+    for codes in ((B.PSGD_F32, B.PSGD_F32), (B.PSGD_F16, B.PSGD_F32), (B.PSGD_BF16, B.PSGD_BF16)):
+        _raises(B.PSGD_EDTYPE, lambda: create([good], *codes, B.PSGD_STATE_BYTE))
+    _raises(B.PSGD_EDTYPE, lambda: create([good, tensor(f32, f32)], B.PSGD_BF16, B.PSGD_F32, B.PSGD_STATE_BYTE))
+    _raises(B.PSGD_EINVAL, lambda: create([good], B.PSGD_BF16, B.PSGD_F32, B.PSGD_STATE_F32), "state")
+    _raises(B.PSGD_EINVAL, lambda: create([good, tensor(bf16, f32, bits=32)], B.PSGD_BF16, B.PSGD_F32, B.PSGD_STATE_BYTE), "state")
+    _raises(B.PSGD_EINVAL, lambda: create([tensor(bf16, f32, 0)], B.PSGD_BF16, B.PSGD_F32, B.PSGD_STATE_BYTE), "device 1")
+    _raises(B.PSGD_EINVAL, lambda: create([good, tensor(bf16, f32, 0)], B.PSGD_BF16, B.PSGD_F32, B.PSGD_STATE_BYTE), "device 1")
+    _raises(B.PSGD_EINVAL, lambda: B.make_adamw_tensor(on(64, f32), on(64, f32), on(64, f32, 0), on(64, f32)), "one GPU")
+    _raises(B.PSGD_EDTYPE, lambda: tensor(torch.float64, f32))
+    _raises(B.PSGD_EDTYPE, lambda: tensor(f32, torch.int32))
+    assert len(lib.args("psgd_adamw_plan_create")) == 3
