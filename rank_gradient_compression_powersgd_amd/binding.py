@@ -777,6 +777,8 @@ def psgd_mx_quantize(ctx: int, x, row=None, col=None, stochastic: bool = False, 
         import torch
         if step.dtype != torch.int32:
             raise PsgdError(call, PSGD_EDTYPE, "step must be int32")
+        if step.numel() < 1:
+            raise PsgdError(call, PSGD_EINVAL, "step must be one int32")
         on.append(step)
     m, n = x.shape
     _same_device(call, *on, ctx=ctx)

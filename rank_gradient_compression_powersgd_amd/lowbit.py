@@ -210,6 +210,8 @@ class MxLinear:
         B._same_device("psgd_mx_product", self.w_row.data, *[v for v in (dy2, err, scale, step) if v is not None])
         if step is not None and step.dtype != torch.int32:
             raise B.PsgdError("psgd_mx_quantize", B.PSGD_EDTYPE, "step must be int32")
+        if step is not None and step.numel() < 1:
+            raise B.PsgdError("psgd_mx_quantize", B.PSGD_EINVAL, "step must be one int32")
         if err is not None:
             if self.x_col is None or self.x_col.k != t:
                 raise B.PsgdError("psgd_mx_product", B.PSGD_EINVAL, "backward() needs the forward() of the same tokens before it")

@@ -211,3 +211,14 @@ def test_a_list_has_the_types_and_the_device_of_its_tensors(lib):  # noqa: F811
     _raises(B.PSGD_EDTYPE, lambda: tensor(torch.float64, f32))
     _raises(B.PSGD_EDTYPE, lambda: tensor(f32, torch.int32))
     assert len(lib.args("psgd_adamw_plan_create")) == 3
+
+
+def test_an_empty_step_count_is_refused(lib):  # noqa: F811
+    """Its address is NULL, which means step 0."""
+    ctx = B.psgd_create(1, 1)
+    x, row, none = _On(torch.zeros(10, 20), 1), _Data(10, 20, 1), _On(torch.zeros(0, dtype=torch.int32), 1)
+    _raises(B.PSGD_EINVAL, lambda: B.psgd_mx_quantize(ctx, x, row, stochastic=True, step=none), "one int32")
+    layer = lowbit.MxLinear.__new__(lowbit.MxLinear)
+    layer.ctx, layer.n_in, layer.n_out, layer.device, layer.w_row = None, 20, 30, torch.device("cuda", 1), _Data(20, 30, 1)
+    _raises(B.PSGD_EINVAL, lambda: layer.backward(_On(torch.zeros(10, 30), 1), step=none), "one int32")
+    assert not lib.args("psgd_mx_quantize")
