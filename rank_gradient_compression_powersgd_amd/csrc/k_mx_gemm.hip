@@ -587,18 +587,24 @@ hipError_t go(const MxProduct& a, int tile, hipStream_t s) {
 
 // Kernel, tiles and parts by a sum of what they cost, in microseconds: a launch that ends with one tile's
 // results, stages of the CU with most tiles, and the parts' way through memory; for few rows a launch, and
-// what its workgroups read, at the rate of the L2s. Measured, tiles of 256 / 128 / 64:
+// what its workgroups read at the rate of the L2s, or one workgroup's way through all panels where that takes
+// longer. Measured, tiles of 256 / 128 / 64:
 //   1280 x 1984, k = 3968    28.3 / 13.8 / 14.1     512 x 4096, k = 4096      27.9 / 13.4 / 11.5
 //   2048 x 2048, k = 2048    19.6 / 10.6 / 12.4     4096 x 4096, k = 4096     40.6 / 49.0 / 69.0
 //   20480 x 1984, k = 3968   88.5 / 95.3 / 144      20480 x 15872, k = 3968    601 /  726 / 1170
 // in two parts 1280 x 1984, k = 3968: 33.3 / 23.8 / 22.6; 3968 x 1488, k = 20480: 104 / 77.6 / 103 whole,
 // 79.6 / 84.1 / 118 in two parts; few rows / tiles of 64, 64 x 1984, k = 3968: 4.9 / 8.3; 64 x 11904: 11.8 / 9.0;
-// 16 x 11904: 5.5 / 8.6; 1 x 32768, k = 4096: 18.0 / 14.0.
+// 16 x 11904: 5.5 / 8.6; 1 x 32768, k = 4096: 18.0 / 14.0; few rows / tiles of 64 in eight parts, 64 x 64, k = 8192:
+// 7.6 / 9.8; 20480: 14.3 / 11.3; 81920: 48 / 19; 327680: 295 / 49; 16 x 64, k = 40960: 12.3 / 13.8; 81920: 22 / 18.
 MxPlan mx_plan(int64_t m, int64_t n, int64_t panels) {
   static constexpr struct { int tile; double start, stage; } kinds[] = {{64, 4.9, 0.11}, {128, 4.8, 0.27}, {256, 8.3, 0.80}};
   MxPlan best{0, 1};
   double least = -1;
-  if (m <= 64) least = 2.6 + (double)((n + 15) / 16) * (double)(((m + 15) / 16 + 1) * panels) * 16 * kMxRowBytes / 13e6;
+  if (m <= 64) {
+    const int64_t high = (m + 15) / 16, held = high > 2 ? 4 : high;      // MFMA tiles that exist, and that are multiplied
+    least = 2.6 + std::max((double)((n + 15) / 16) * (double)((high + 1) * panels) * 16 * kMxRowBytes / 13e6,
+                           (double)panels * (0.017 + 0.014 * (double)held));
+  }
   for (const auto& k : kinds) {
     const int64_t tiles = ((m + k.tile - 1) / k.tile) * ((n + k.tile - 1) / k.tile);
     for (int splits = 1; splits <= 8 && (splits == 1 || panels / splits >= 8); splits *= 2) {

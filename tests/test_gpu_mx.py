@@ -742,3 +742,20 @@ def test_a_captured_layer_replays_as_the_eager_one():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, y2) and torch.equal(dx, dx2) and torch.equal(err, want) and want.any(), t
+
+
+@pytest.mark.parametrize("m,n,k", [(64, 64, 131067), (1, 70, 400001), (40, 513, 70000), (16, 33, 262144)])
+def test_products_of_few_rows_and_columns_and_very_long_sums(ctx, m, n, k):
+    """Exactly: sums of -1, 0 and 1 below 2^24 round nothing in fp32."""
+    import torch
+    from rank_gradient_compression_powersgd_amd import MxTensor, psgd_mx_product, psgd_mx_quantize
+    from rank_gradient_compression_powersgd_amd import binding
+    assert binding.psgd_mx_product_workspace(m, n, k) >= 2 * 4 * m * n
+    x, w = (torch.randint(-1, 2, (r, k), device="cuda").to(torch.bfloat16) for r in (m, n))
+    a, b = MxTensor(m, k), MxTensor(n, k)
+    psgd_mx_quantize(ctx, x, a)
+    psgd_mx_quantize(ctx, w, b)
+    c = torch.full((m, n), 3.0, device="cuda")
+    psgd_mx_product(ctx, a, b, c, accumulate=True)
+    want = 3.0 + x.double() @ w.double().t().contiguous()
+    assert torch.equal(c.double(), want)

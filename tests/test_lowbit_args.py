@@ -222,3 +222,21 @@ def test_an_empty_step_count_is_refused(lib):  # noqa: F811
     layer.ctx, layer.n_in, layer.n_out, layer.device, layer.w_row = None, 20, 30, torch.device("cuda", 1), _Data(20, 30, 1)
     _raises(B.PSGD_EINVAL, lambda: layer.backward(_On(torch.zeros(10, 30), 1), step=none), "one int32")
     assert not lib.args("psgd_mx_quantize")
+
+
+def test_few_rows_and_columns_share_a_long_sum():
+    """The kernel for few rows gives 16 columns of C one workgroup for all of k. Where these are few and k is long, tiles in
+    parts are several times as fast; where k is short or workgroups are many, the one launch is."""
+    parts = lambda m, n, k: B.psgd_mx_product_workspace(m, n, k) // (4 * m * n)  # noqa: E731
+    for m, n, k in ((64, 64, 327680), (64, 512, 81920), (16, 64, 163840), (1, 1, 2 ** 20), (33, 64, 40960), (64, 1984, 20480)):
+        assert parts(m, n, k) >= 2, (m, n, k)
+    for m, n, k in ((64, 64, 3968), (16, 64, 20480), (1, 496, 15872), (64, 1984, 3968), (16, 11904, 3968), (1, 32768, 4096), (17, 512, 8192)):
+        assert parts(m, n, k) == 0, (m, n, k)
+
+
+@pytest.mark.parametrize("m", [1, 16, 64, 65, 1000, 4096])
+@pytest.mark.parametrize("n", [1, 64, 1488, 11904])
+def test_a_part_has_eight_panels_at_least(m, n):
+    for k in (1, 1000, 3968, 20480, 200000, 2 ** 20):
+        parts = B.psgd_mx_product_workspace(m, n, k) // (4 * m * n)
+        assert parts <= -(-k // 128) // 8
