@@ -104,18 +104,30 @@ MFMA_PEAK_TFLOPS = {"bf16": 2500.0, "f16": 2500.0, "f64": 78.6}
 COPY_BYTES = 1 << 31          # the calibration copy reads and writes 2 GiB per launch
 
 
-def kernel_source_hash() -> str:
-    """sha256 over the code of the library's HIP sources (line comments and blank lines left
-    out, so that comment edits keep recorded counters valid): counters taken on other code are
-    stale."""
-    import glob
+def kernel_sources(csrc: str) -> list:
+    """The HIP sources that a step's counters depend on: those that define a kernel of KERNEL_SLOT, the runtime that
+    launches them, and the headers of csrc that these include. The other operators' files are not among them."""
+    import re
+    code = {f: open(os.path.join(csrc, f), encoding="utf-8").read() for f in os.listdir(csrc) if f.endswith((".hip", ".h"))}
+    defined = re.compile(r"^void (?:%s)\(" % "|".join(KERNEL_SLOT), re.MULTILINE)
+    found, todo = set(), [f for f in code if f == "runtime.hip" or defined.search(code[f])]
+    while todo:
+        f = todo.pop()
+        if f in code and f not in found:
+            found.add(f)
+            todo += re.findall(r'^#include "([^"]+)"', code[f], re.MULTILINE)
+    return sorted(found)
+
+
+def kernel_source_hash(csrc: str = os.path.join(ROOT, "rank_gradient_compression_powersgd_amd", "csrc")) -> str:
+    """sha256 over the code of the step's HIP sources (line comments and blank lines left out, so that comment edits
+    keep recorded counters valid): counters taken on other code are stale."""
     import hashlib
     h = hashlib.sha256()
-    for f in sorted(glob.glob(os.path.join(ROOT, "rank_gradient_compression_powersgd_amd", "csrc", "*"))):
-        if f.endswith((".hip", ".h")):
-            with open(f, encoding="utf-8") as fh:
-                code = [ln.split("//", 1)[0].rstrip() for ln in fh]
-            h.update(os.path.basename(f).encode() + b"\0" + "\n".join(c for c in code if c).encode())
+    for f in kernel_sources(csrc):
+        with open(os.path.join(csrc, f), encoding="utf-8") as fh:
+            code = [ln.split("//", 1)[0].rstrip() for ln in fh]
+        h.update(f.encode() + b"\0" + "\n".join(c for c in code if c).encode())
     return h.hexdigest()[:16]
 
 

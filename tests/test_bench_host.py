@@ -122,3 +122,31 @@ def test_trace_summary_counts_steps_and_splits_the_two_gemms(tmp_path, capsys):
     mtp = next(l for l in out.splitlines() if l.startswith("| k_gemm_nt (M^T P_hat)"))
     assert mq.split("|")[2].strip() == "3" and float(mq.split("|")[3]) == pytest.approx(100.0)
     assert float(mtp.split("|")[4]) == pytest.approx(0.05)
+
+
+def test_counters_go_stale_with_the_steps_sources_only(tmp_path):
+    """Sources of other operators, added or changed, leave them valid; a kernel of the step, its runtime or a header they
+    share does not."""
+    import shutil
+    csrc = os.path.join(ROOT, "rank_gradient_compression_powersgd_amd", "csrc")
+    d = tmp_path / "csrc"
+    d.mkdir()
+    for f in os.listdir(csrc):
+        if f.endswith((".hip", ".h")):
+            shutil.copy(os.path.join(csrc, f), d / f)
+    names = bench.kernel_sources(str(d))
+    assert {"k_ef_mq.hip", "k_mtp.hip", "k_decomp.hip", "k_gs.hip", "runtime.hip", "psgd_internal.h"} <= set(names)
+    assert not {"k_adamw.hip", "k_mx.hip", "k_mx_gemm.hip", "lowbit.hip", "mx.h", "k_embed.hip", "k_ns_gemm.hip"} & set(names)
+    h = bench.kernel_source_hash(str(d))
+    assert h == bench.kernel_source_hash()
+    (d / "k_other.hip").write_text('#include "psgd_internal.h"\nvoid k_other() {}\n')
+    for other in ("k_adamw.hip", "mx.h", "lowbit.hip"):
+        (d / other).write_text((d / other).read_text() + "\nint more;\n")
+    (d / "k_gs.hip").write_text((d / "k_gs.hip").read_text() + "\n// a comment\n")
+    assert bench.kernel_source_hash(str(d)) == h
+    for own in names:
+        text = (d / own).read_text()
+        (d / own).write_text(text + "\nint more;\n")
+        assert bench.kernel_source_hash(str(d)) != h, own
+        (d / own).write_text(text)
+    assert bench.kernel_source_hash(str(d)) == h
