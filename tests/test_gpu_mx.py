@@ -759,3 +759,43 @@ def test_products_of_few_rows_and_columns_and_very_long_sums(ctx, m, n, k):
     psgd_mx_product(ctx, a, b, c, accumulate=True)
     want = 3.0 + x.double() @ w.double().t().contiguous()
     assert torch.equal(c.double(), want)
+
+
+def test_random_bits_of_pairs_past_32_bits(ctx):
+    """The last rows of a matrix whose pairs of neighbours pass 2^32, in the middle of a lane's four pairs of a row (rows
+    alone) and of its 32 rows (columns, and rows with them), bit by bit."""
+    import types
+
+    import torch
+    from rank_gradient_compression_powersgd_amd import MxTensor, psgd_mx_quantize
+    n, half, first = 4100, 2050, 2095104 - 128                              # first: a whole panel's and group's
+    cross = 2 ** 32 // half                                                  # the row whose pairs pass it
+    m, at = cross + 200, 2 ** 32 - cross * half
+    assert cross % 32 != 0 and at % 4 == 2 and first % 128 == 0 and first < cross // 32 * 32
+    x = torch.zeros(m, n, dtype=torch.bfloat16, device="cuda")
+    tail, _ = _matrix(m - first, n, "bf16", 5)
+    x[first:] = tail
+    xv = _np(x[first:])
+    h = L.hash_bits(L.hash_key(13, 0, 0), np.arange(first * half, m * half, dtype=np.uint64)).reshape(m - first, half)
+    u = (np.stack([h, (h << np.uint32(16)) | (h >> np.uint32(16))], 2).reshape(m - first, n) >> np.uint32(10)) * 2.0 ** -22
+
+    def rows_of(mx):
+        p, g = -(-n // 128), -(-m // 64)
+        codes, exps = mx.data[:p * m * 64].view(p, m, 64)[:, first:], mx.data[p * m * 64:p * (m * 64 + g * 256)].view(p, g, 256)[:, first // 64:]
+        return types.SimpleNamespace(data=torch.cat([codes.reshape(-1), exps.reshape(-1)]))
+
+    def columns_of(mx):
+        p, g = -(-m // 128), -(-n // 64)
+        codes, exps = mx.data[:p * n * 64].view(p, n * 64)[first // 128:], mx.data[p * n * 64:p * (n * 64 + g * 256)].view(p, g * 256)[first // 128:]
+        return types.SimpleNamespace(data=torch.cat([codes.reshape(-1), exps.reshape(-1)]))
+
+    row, col = MxTensor(m, n), MxTensor(n, m)
+    psgd_mx_quantize(ctx, x, row, stochastic=True, seed=13)
+    _check(rows_of(row), xv, u, "rows alone")
+    row.data.zero_()
+    psgd_mx_quantize(ctx, x, row, col, stochastic=True, seed=13)
+    _check(rows_of(row), xv, u, "rows with columns")
+    _check(columns_of(col), xv.T, u.T, "columns with rows")
+    col.data.zero_()
+    psgd_mx_quantize(ctx, x, None, col, stochastic=True, seed=13)
+    _check(columns_of(col), xv.T, u.T, "columns alone")
