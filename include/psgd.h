@@ -481,9 +481,10 @@ typedef enum psgd_rounding { PSGD_NEAREST = 0, PSGD_STOCHASTIC = 1 } psgd_roundi
  *     64 elements, of their largest magnitude (one more from 1.875 times its power of two on). m1: sign,
  *     4 exponent and 3 fraction bits; m2: 5 exponent and 3 fraction bits, the largest field standing for
  *     the byte's exponent, both with subnormals: 3 fraction bits down to 2^-14 (m1) and 2^-30 (m2) of the
- *     largest. A positive m2 never becomes 0. Byte 255: a moment of the 64 was past 1.875 2^127 (m2 where |c g| is
- *     past 1.8e19), and psgd_adamw_moments gives NaN for all of them. The next step takes m1 as 0 and, of such m2,
- *     m2 as 1.875 2^127: the 64 parameters stand still, but for weight decay, until m2 has decayed.
+ *     largest. A positive m2 never gets code 0; its lowest code is a number of fp32 from byte 11 on (a largest m2 of
+ *     2^-116 in the group), and 0 below. Byte 255: a moment of the 64 was past 1.875 2^127 (m2 where |c g|
+ *     comes to 1.8e19), and psgd_adamw_moments gives NaN for all of them. The next step takes the group's m1 as 0 and
+ *     such m2 as 1.875 2^127: the 64 parameters stand still, but for weight decay, until m2 has decayed.
  * All zero is the state before the first step, in both forms. Elements past numel are written as 0.
  * Moments rounded to nearest stand still once a step changes them by less than half a code; with
  * PSGD_STOCHASTIC their expectation moves as in fp32.
@@ -544,7 +545,8 @@ psgd_status psgd_adamw_moments(psgd_ctx* ctx, const uint8_t* m1, const uint8_t* 
  *     codes   byte (p rows + r) 64 + i, p < P, r < rows, i < 64: elements 128 p + 2 i (low nibble), + 1
  *     scales  behind them, byte ((p G + r / 64) 64 + 16 g + r % 16) 4 + r / 16 % 4: elements
  *             128 p + 32 g .. + 31 of row r, g < 4
- *   Elements at or beyond k are 0 with s = 1. 0 <= rows, k <= 2^25.
+ *   Elements at or beyond k are 0 with s = 1. 0 <= rows, k <= 2^25; psgd_mx_quantize and psgd_mx_dequantize take
+ *   matrices of ceil(m / 64) ceil(n / 128) < 2^24 (PSGD_EUNSUPPORTED past that).
  *
  * psgd_mx_quantize: x (m x n, row-major, fp16, bf16 or fp32, any leading dimension >= n) to `row` (m x n,
  *   blocks along the rows) and to `col` (x transposed, n x m, blocks along the columns); either may be
@@ -555,7 +557,8 @@ psgd_status psgd_adamw_moments(psgd_ctx* ctx, const uint8_t* m1, const uint8_t* 
  *                      a step)
  *   s >= 1. A block that holds an infinity or NaN gets s = 255 and codes 0.
  *   seed, step_dev (NULL: 0) are not read with PSGD_NEAREST. Two neighbours of a row share a hash; the
- *   two directions share their bits.
+ *   two directions share their bits, and so do calls of one seed and step: an element that is rounded again and again
+ *   (a layer's microbatches, its steps) averages out over seeds and steps only.
  * psgd_mx_dequantize: the values, rounded to any type (bf16 and fp32 hold them, but for 2^128, to which
  *   magnitudes near fp32's largest round), out row-major, ld_out >= k.
  * psgd_mx_product: C (m x n, fp16, bf16 or fp32, any leading dimension >= n) = s A B^T, a m x k, b n x k,

@@ -16,9 +16,9 @@
 //
 // Bound: memory. A chunk's loads are all sent for before its first use, so a workgroup (4096 elements, 256
 // threads) keeps 57 KB under way. 188.9 million elements (fp32 parameters, bf16 gradients, 8-bit moments, 14.06
-// bytes each): 470 us, 5.6 TB/s; their norm 71 to 104 us, their moments' values 200 (5.7 TB/s). 23.6 million
-// (bf16, fp32 gradients, 12.06 bytes): 55, 15 and 23 us. 0.76 million: 7, 3 and 3 us, what dependent launches of
-// this kind take at least.
+// bytes each): 493 us in the median of 30 passes, 473 at best (5.4 and 5.6 TB/s); their norm 105 and 74 us, their
+// moments' values 199 and 194 (5.7 TB/s). 23.6 million (bf16, fp32 gradients, 12.06 bytes): 57 to 65, 15 and 23 us.
+// 0.76 million: 7, 3.6 and 3.3 us, and 2.1 for the norm's last sum, which is about what a launch takes here.
 //
 // The moments' arithmetic is rounded operation by operation (no fused multiply-add), so that codes do
 // not depend on how the compiler contracts an expression.

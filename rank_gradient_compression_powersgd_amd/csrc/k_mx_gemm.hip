@@ -4,10 +4,11 @@
 // P is B (the columns i of C), Q is A (its rows j): a lane then holds C[j][i .. i + 3], consecutive in a
 // row of C.
 //
-// Bound: under full load the chip's power. 64 MFMAs a wave and stage take 0.59 us with every CU at work
-// (16 cycles each at 1.74 GHz; 0.49 on 40 CUs), 0.65 with the reads from LDS, 0.81 with the loads into it:
-// 5.3 PFLOP/s. A 256-wide tile of 16-bit results takes 4 us more to store. 20480 x 15872, k = 3968, bf16:
-// 601 to 620 us, 4.2 to 4.3 PFLOP/s (bf16 library products reach 1.37).
+// Bound: the MFMAs at the clock that full load leaves, and beside them the operands' way into LDS. 64 MFMAs a wave
+// and stage take 0.59 us with every CU at work (16 cycles each at 1.74 GHz; 0.49 on 40 CUs), 0.65 with the
+// reads from LDS, 0.81 with the loads into it: 5.3 PFLOP/s. A 256-wide tile of 16-bit results takes 4 us more
+// to store. 20480 x 15872, k = 3968, bf16: 601 to 622 us, 4.1 to 4.3 PFLOP/s (bf16 library products reach
+// 1.37); over the whole kernel the matrix pipe is busy in 50% of the cycles, and no LDS access waits for a bank.
 #include <algorithm>
 #include <type_traits>
 #include <utility>

@@ -203,7 +203,8 @@ class MxLinear:
         """dx = dy W^T, in dy's dtype, and err += scale x^T dy (err: in x out fp32, the error buffer of an
         in-place matrix of a PowerSGDGroup; scale: its one-element fp32 multiplier, or None), which uses up
         the forward() before it: a second such call is refused. dy is rounded
-        stochastically by seed and step (one-element int32 device tensor, which the caller advances, or None)."""
+        stochastically by seed and step (one-element int32 device tensor, which the caller advances; None: 0).
+        Calls of one step draw the same bits: what is to average out, microbatches too, needs a step of its own."""
         import torch
         dy2 = self._tokens(dy, self.n_out, "dy")
         t, stream = dy2.shape[0], B._stream(None, self.device.index)
