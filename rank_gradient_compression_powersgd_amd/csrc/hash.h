@@ -1,7 +1,7 @@
 // Random bits of stochastic rounding: a hash of the caller's seed, the step, a tensor and an element's
 // index, so that the same call gives the same bits wherever an element is computed. Two rounds of
-// xor-shift and multiplication by odd constants (the fractions of the square roots of 5 and 3):
-// flipping any input bit flips every output bit with probability 0.5 +- 0.005.
+// xor-shift and multiplication by odd constants (the fractions of the square roots of 7, made odd,
+// and of 3): flipping any input bit flips every output bit with probability 0.5 +- 0.005.
 #pragma once
 
 #include <hip/hip_runtime.h>
