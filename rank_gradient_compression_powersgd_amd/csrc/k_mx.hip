@@ -12,7 +12,8 @@
 // Bound: to nearest, memory (20480 x 3968 bf16, both directions, 249 MB: 40 us, 6.3 TB/s, with 81 MB of it still in
 // the last cache, 49 us, 5.1 TB/s, with none; rows alone 29 us; 20480 x 1984 fp16 35 to 39 us, 3.2 to 3.6 TB/s). By
 // random bits the vector instructions come close to it: a conversion of 14 cycles per element and direction and
-// a hash per two elements, 25 of 55 us (4.5 TB/s); 61 to 77 us where nothing is in a cache. Loads of the next block ahead of this one's work cost waves and gained nothing (55 -> 62 us).
+// a hash per two elements, 25 of 55 us (4.5 TB/s); 61 to 77 us where nothing is in a cache. Loads of the next block
+// ahead of this one's work cost waves and gained nothing (55 -> 62 us).
 #include <type_traits>
 #include <utility>
 
